@@ -18,7 +18,12 @@
  *    its own;
  *  - zopt_grad_sq_norm, zopt_grad_clip_stats and zopt_adamw_shard_step_clipped:
  *    the gradient norm of the shard, the clip statistics, and the AdamW step
- *    taking its gradient scale from them in device memory.
+ *    taking its gradient scale from them in device memory;
+ *
+ * and the operators that produce its gradients where memory is shortest:
+ * zopt_linear_xent (a vocabulary projection's loss and gradients without the
+ * logits), zopt_glu_forward / zopt_glu_backward (the gated feed-forward) and
+ * zopt_act8_* (activation checkpoints in 8 bits).
  *
  * Conventions common to every call
  * --------------------------------
@@ -595,6 +600,150 @@ zopt_status zopt_set_ns_workgroup_limit(int32_t n);
  * Errors: ZOPT_ERR_HYPER (form not 0, 1 or 2).
  */
 zopt_status zopt_set_ns_form(int32_t form);
+
+/*
+ * Gradients of a large vocabulary and of the gated feed-forward block, and
+ * activation checkpoints in 8 bits: the operators that produce what the calls
+ * above step, where a training rank's memory goes -- the logits, the
+ * pre-activations and the activations kept between forward and backward.
+ * Their gradients are bf16 and may be written straight into a flat gradient
+ * vector (any element offset), such as zopt_adamw_shard_step and
+ * zopt_muon_step read.
+ *
+ * Matrices are row-major; a row stride counts elements between rows (>= the
+ * row's length, <= 2^31).  Widths (D, V, F, N, cols) are 1 .. 2^21, rows T
+ * 0 .. 2^30.  Products run on bf16 matrix cores with fp32 accumulation; every
+ * result is the same on every run.  An operand whose row length, row stride
+ * or base is not a multiple of 8 elements (16 bytes) is copied into the
+ * workspace first; nothing else depends on alignment but speed.
+ *
+ * workspace: device scratch, 256-byte aligned, of at least the size that the
+ * call with workspace == NULL writes to *workspace_bytes.  That size depends
+ * on the sizes, strides, the alignment of the operands and which optional
+ * pointers are NULL, so query with the arguments of the call.
+ */
+
+/*
+ * zopt_linear_xent -- softmax cross entropy of a vocabulary projection, with
+ * its gradients, without the logits:
+ *   z_tv  = sum_d x_td w_vd                         (fp32, never stored)
+ *   row_t = log sum_v exp(z_tv) - z_t,target        (0 for ignored rows)
+ *   loss  = s sum_t row_t,   s = 1, or 1 / (rows not ignored) with mean = 1
+ *                            (0 where every row is ignored)
+ *   P_tv  = softmax(z_t)_v - [v = target_t]         (0 for ignored rows)
+ *   dx    = s grad_scale P w,   dw = s grad_scale P^T x
+ * Rows are taken in pieces whose exponentials fill at most 2 GiB of the
+ * workspace; they are kept there in 16 bits (fp16, relative to the largest of
+ * 64 neighbouring logits), so that each of the call's three products is
+ * computed once.  P is rounded to bf16 for the last two.
+ *
+ * Arguments
+ *   x       bf16 [T, D], row stride ldx.     w   bf16 [V, D], row stride ldw.
+ *   target  int64 [T], device.  Rows whose target is ignore_index take no
+ *           part: whatever x holds there reaches neither loss nor dw.  Any
+ *           other target outside [0, V) makes its row's loss NaN, and with it
+ *           loss, dw and that row of dx; no memory is read at it.
+ *   mean    0 or 1.          grad_scale   finite.
+ *   loss    one float, device, written.
+ *   row_loss  float [T], device, written; NULL: not wanted.
+ *   dx      bf16 [T, D], row stride lddx; NULL: not wanted.
+ *   dw      bf16 [V, D], row stride lddw; NULL: not wanted.  With neither,
+ *           only the loss is computed.  T = 0 writes loss 0 and dw zero.
+ *
+ * Errors: ZOPT_ERR_NULL (workspace_bytes; with a workspace w, loss, or with
+ * T > 0 x or target); ZOPT_ERR_SIZE (T, D, V or a stride out of range);
+ * ZOPT_ERR_HYPER (mean, grad_scale); ZOPT_ERR_WORKSPACE; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t ldx,
+                             const uint16_t *w, int64_t ldw, const int64_t *target,
+                             int64_t ignore_index, int32_t mean, float grad_scale, float *loss,
+                             float *row_loss, uint16_t *dx, int64_t lddx, uint16_t *dw,
+                             int64_t lddw, void *workspace, size_t *workspace_bytes,
+                             void *stream);
+
+/*
+ * 8-bit activation checkpoints.  A bf16 matrix [rows, cols] is kept as
+ *   q      e4m3 (OCP, 4 exponent and 3 mantissa bits) [rows, cols], and
+ *   scale  one byte b per 32 neighbouring columns of a row, [rows, ceil(cols / 32)]:
+ * an element is q * 2^(b - 127).  b is the smallest that brings the block's
+ * largest magnitude to at most 448 (e4m3's largest), but at least 3; values
+ * are divided by the power of two (exact) and rounded to nearest even, so an
+ * element is off by at most 2^-4 of itself, or 2^-10 2^(b - 127).  (With
+ * b = 247 values are held to 240 2^120, so that a finite one stays a finite
+ * bf16.)  A block with a NaN or an infinity gets b = 255 and reads back as NaN.
+ *
+ * zopt_act8_pack writes q and scale from x; zopt_act8_unpack writes x from
+ * them (exact: every value is a bf16).  rows = 0 enqueues nothing.
+ * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_act8_pack(int64_t rows, int64_t cols, const uint16_t *x, int64_t ldx, uint8_t *q,
+                           uint8_t *scale, void *stream);
+zopt_status zopt_act8_unpack(int64_t rows, int64_t cols, const uint8_t *q, const uint8_t *scale,
+                             uint16_t *x, int64_t ldx, void *stream);
+
+/*
+ * zopt_act8_wgrad -- the weight gradient of a linear layer y = x w^T whose
+ * input was kept as an 8-bit checkpoint: dw [N, D] = dy^T x, with
+ *   dy        bf16 [T, N], row stride lddy;
+ *   q, scale  the checkpoint of x [T, D];
+ *   dw        bf16 [N, D], row stride lddw, written (zero for T = 0).
+ * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE; ZOPT_ERR_WORKSPACE; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_act8_wgrad(int64_t T, int64_t N, int64_t D, const uint16_t *dy, int64_t lddy,
+                            const uint8_t *q, const uint8_t *scale, uint16_t *dw, int64_t lddw,
+                            void *workspace, size_t *workspace_bytes, void *stream);
+
+/* Activations of the gated feed-forward block. */
+enum {
+    ZOPT_ACT_SILU = 0, /* g / (1 + exp(-g))                                      */
+    ZOPT_ACT_GELU = 1  /* g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2      */
+};
+
+/*
+ * zopt_glu_forward -- the gated feed-forward's first half in one kernel:
+ *   g = x w_gate^T,  u = x w_up^T  (fp32),   h = act(g) u
+ *   x               bf16 [T, D], row stride ldx.
+ *   w_gate, w_up    bf16 [F, D], both with row stride ldw (two halves of one
+ *                   fused [2 F, D] weight, or two matrices).
+ *   act             ZOPT_ACT_*.
+ *   h               bf16 [T, F], row stride ldh, written.
+ *   g8, g_scale, u8, u_scale   where g and u go as 8-bit checkpoints
+ *                   ([T, F] each, from their fp32 values), for
+ *                   zopt_glu_backward; all four or none (NULL).
+ * T = 0 enqueues nothing.
+ * Errors: ZOPT_ERR_NULL (also some but not all of the checkpoint);
+ * ZOPT_ERR_SIZE; ZOPT_ERR_HYPER (act); ZOPT_ERR_WORKSPACE; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_glu_forward(int64_t T, int64_t D, int64_t F, const uint16_t *x, int64_t ldx,
+                             const uint16_t *w_gate, const uint16_t *w_up, int64_t ldw,
+                             int32_t act, uint16_t *h, int64_t ldh, uint8_t *g8,
+                             uint8_t *g_scale, uint8_t *u8, uint8_t *u_scale, void *workspace,
+                             size_t *workspace_bytes, void *stream);
+
+/*
+ * zopt_glu_backward -- gradients of zopt_glu_forward from dh:
+ *   du = dh act(g),  dg = dh u act'(g)             (rounded to bf16)
+ *   dx = dg w_gate + du w_up,  dw_gate = dg^T x,  dw_up = du^T x
+ *   dh        bf16 [T, F], row stride lddh.
+ *   x, ldx    the forward's input, or x8, x_scale: its 8-bit checkpoint
+ *             (then x is not read and the gradients are those of the values
+ *             the checkpoint stands for).
+ *   g8, g_scale, u8, u_scale   the forward's checkpoint of g and u; all NULL:
+ *             g and u are computed again from x.
+ *   h         bf16 [T, F], row stride ldh, written with act(g) u (for the
+ *             weight gradient of the projection after it); NULL: not wanted.
+ *   dx        bf16 [T, D], row stride lddx;  dw_gate, dw_up  bf16 [F, D], row
+ *             stride lddw; written (T = 0: the weight gradients zero).
+ * Other arguments and errors as zopt_glu_forward.
+ */
+zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const uint16_t *dh, int64_t lddh,
+                              const uint16_t *x, int64_t ldx, const uint8_t *x8,
+                              const uint8_t *x_scale, const uint16_t *w_gate,
+                              const uint16_t *w_up, int64_t ldw, int32_t act, const uint8_t *g8,
+                              const uint8_t *g_scale, const uint8_t *u8, const uint8_t *u_scale,
+                              uint16_t *h, int64_t ldh, uint16_t *dx, int64_t lddx,
+                              uint16_t *dw_gate, uint16_t *dw_up, int64_t lddw, void *workspace,
+                              size_t *workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }

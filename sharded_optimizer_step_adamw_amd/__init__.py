@@ -23,12 +23,16 @@ Entry points (same names as the C ABI in include/zopt.h):
   grad_sq_norm_noalloc  the same with the library's own scratch (allocates nothing)
   grad_clip_stats    clip statistics (device scalars) from summed squares
   adamw_shard_step_clipped   AdamW taking grad_scale from the clip statistics
+  linear_xent_loss / linear_xent_grad   cross entropy of a vocabulary projection,
+                     alone or with its gradients, without the logits (zopt_linear_xent)
+  glu_forward / glu_backward   the gated feed-forward block's gate / up part
+  act8_pack / act8_unpack / act8_wgrad   activation checkpoints in 8 bits (Act8)
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -113,6 +117,20 @@ def _lib_or_raise() -> ctypes.CDLL:
         L.zopt_muon_groups_output_view.argtypes = [i32, pi32, pi64, pi64, i32, vp, i32, i32, pp,
                                                    pi64]
         L.zopt_muon_groups_output_view.restype = ctypes.c_int
+        size_p = ctypes.POINTER(ctypes.c_size_t)
+        L.zopt_linear_xent.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, i64, i32, f32, vp, vp,
+                                       vp, i64, vp, i64, vp, size_p, vp]
+        L.zopt_act8_pack.argtypes = [i64, i64, vp, i64, vp, vp, vp]
+        L.zopt_act8_unpack.argtypes = [i64, i64, vp, vp, vp, i64, vp]
+        L.zopt_act8_wgrad.argtypes = [i64, i64, i64, vp, i64, vp, vp, vp, i64, vp, size_p, vp]
+        L.zopt_glu_forward.argtypes = [i64, i64, i64, vp, i64, vp, vp, i64, i32, vp, i64, vp, vp,
+                                       vp, vp, vp, size_p, vp]
+        L.zopt_glu_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, i32,
+                                        vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, size_p,
+                                        vp]
+        for f in (L.zopt_linear_xent, L.zopt_act8_pack, L.zopt_act8_unpack, L.zopt_act8_wgrad,
+                  L.zopt_glu_forward, L.zopt_glu_backward):
+            f.restype = ctypes.c_int
         _lib = L
     return _lib
 
@@ -538,3 +556,279 @@ def muon_groups_output_view(workspace: torch.Tensor, shapes: Sequence[tuple], ns
 __all__ = ["adamw_shard_step", "muon_step", "muon_workspace_bytes", "muon_output_view",
            "muon_step_groups", "muon_groups_workspace_bytes", "muon_groups_output_view",
            "round_bf16", "shard_len", "lib", "ZoptError", "LIB_PATH", "MAX_BATCH", "MAX_GROUPS"]
+
+
+# ------------------------------------------------------ operators of the gradients
+
+ACTIVATIONS = {"silu": 0, "gelu": 1}
+
+
+class Act8(NamedTuple):
+    """A bf16 matrix [rows, cols] kept in 8 bits: q, float8_e4m3fn [rows,
+    cols], and scale, uint8 [rows, ceil(cols / 32)]; an element is
+    q * 2^(scale - 127) (zopt_act8_pack)."""
+    q: torch.Tensor
+    scale: torch.Tensor
+
+
+def _need_rows(t, dtype, rows, cols, name, device=None) -> int:
+    """Checks that t is a GPU matrix [rows, cols] of dtype with contiguous
+    rows (None: any size there) and returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, need {dtype}")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (
+            cols is not None and t.shape[1] != cols):
+        want = tuple("any" if s is None else s for s in (rows, cols))
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {want}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a GPU tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    r, c = t.shape
+    if c == 0:
+        raise ValueError(f"{name}: rows are empty")
+    if c > 1 and t.stride(1) != 1 or r > 1 and t.stride(0) < c:
+        raise ValueError(f"{name}: strides {t.stride()}, need contiguous rows that do not overlap")
+    return t.stride(0) if r > 1 else c
+
+
+def _need_act8(a, rows, cols, name, device=None) -> None:
+    if not isinstance(a, Act8):
+        raise TypeError(f"{name}: expected an Act8")
+    _need_rows(a.q, torch.float8_e4m3fn, rows, cols, f"{name}.q", device)
+    r, c = a.q.shape
+    _need_rows(a.scale, torch.uint8, r, (c + 31) // 32, f"{name}.scale", a.q.device)
+    if not a.q.is_contiguous() or not a.scale.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+class _On:
+    """Where a call's outputs and workspace come from when the caller gives
+    none: memory of the call's own stream, so that the allocator reuses it
+    only after the call."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.handle = _stream(device, stream)
+        self.other = self.handle != torch.cuda.current_stream(device).cuda_stream
+
+    def empty(self, shape, dtype):
+        if not self.other:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=self.device)):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, need):
+        if given is None:
+            return self.empty(need, torch.uint8)
+        _need(given, torch.uint8, need, "workspace", self.device)
+        return given
+
+
+def _sized(fn, args, where, on, workspace):
+    """Runs fn(*args, workspace, size, stream) with a workspace of the size
+    that the same call asks for."""
+    size = ctypes.c_size_t(0)
+    _check(fn(*args, None, ctypes.byref(size), None), f"{where}(workspace query)")
+    ws = on.workspace(workspace, int(size.value))
+    size.value = ws.numel()
+    _check(fn(*args, ws.data_ptr(), ctypes.byref(size), on.handle), where)
+
+
+def _linear_xent(x, w, target, ignore_index, mean, grad_scale, loss, row_loss, dx, dw, want_dx,
+                 want_dw, workspace, stream):
+    ldx = _need_rows(x, torch.bfloat16, None, None, "x")
+    dev = x.device
+    T, D = x.shape
+    ldw = _need_rows(w, torch.bfloat16, None, D, "w", dev)
+    V = w.shape[0]
+    _need(target, torch.int64, T, "target", dev)
+    if target.dim() != 1 or target.shape[0] != T:
+        raise ValueError(f"target: shape {tuple(target.shape)}, need ({T},)")
+    on = _On(dev, stream)
+    if loss is None:
+        loss = on.empty(1, torch.float32)
+    if row_loss is None:
+        row_loss = on.empty(T, torch.float32)
+    _need(loss, torch.float32, 1, "loss", dev)
+    _need(row_loss, torch.float32, T, "row_loss", dev)
+    if dx is None and want_dx:
+        dx = on.empty((T, D), torch.bfloat16)
+    if dw is None and want_dw:
+        dw = on.empty((V, D), torch.bfloat16)
+    lddx = D if dx is None else _need_rows(dx, torch.bfloat16, T, D, "dx", dev)
+    lddw = D if dw is None else _need_rows(dw, torch.bfloat16, V, D, "dw", dev)
+    # (a tensor of no rows has no address; the call takes NULL for "not wanted")
+    args = (T, D, V, _ptr(x), ldx, _ptr(w), ldw, _ptr(target), int(ignore_index), int(mean),
+            float(grad_scale), _ptr(loss), _ptr(row_loss), _ptr(dx), lddx, _ptr(dw), lddw)
+    _sized(lib().zopt_linear_xent, args, "zopt_linear_xent", on, workspace)
+    return loss, row_loss, dx, dw
+
+
+def linear_xent_loss(x, w, target, ignore_index: int = -100, mean: bool = True,
+                     loss: Optional[torch.Tensor] = None,
+                     row_loss: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """Softmax cross entropy of the projection x w^T (zopt_linear_xent): x
+    bf16 [T, D], w bf16 [V, D], target int64 [T].  Returns (loss, row_loss),
+    fp32 [1] and [T]: the rows' losses, 0 where target is ignore_index, and
+    their sum, or mean over the rows not ignored."""
+    return _linear_xent(x, w, target, ignore_index, mean, 1.0, loss, row_loss, None, None, False,
+                        False, workspace, stream)[:2]
+
+
+def linear_xent_grad(x, w, target, ignore_index: int = -100, mean: bool = True,
+                     grad_scale: float = 1.0, want_dx: bool = True, want_dw: bool = True,
+                     loss: Optional[torch.Tensor] = None,
+                     row_loss: Optional[torch.Tensor] = None,
+                     dx: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None):
+    """linear_xent_loss with the gradients of grad_scale * loss: returns
+    (loss, row_loss, dx, dw), dx bf16 [T, D] and dw bf16 [V, D] (None where
+    not wanted).  dw may be a [V, D] view of a flat gradient vector."""
+    return _linear_xent(x, w, target, ignore_index, mean, grad_scale, loss, row_loss, dx, dw,
+                        want_dx, want_dw, workspace, stream)
+
+
+def _act8_empty(rows, cols, on) -> Act8:
+    return Act8(on.empty((rows, cols), torch.float8_e4m3fn),
+                on.empty((rows, (cols + 31) // 32), torch.uint8))
+
+
+def act8_pack(x, out: Optional[Act8] = None, stream=None) -> Act8:
+    """The 8-bit checkpoint of x, bf16 [rows, cols] (zopt_act8_pack)."""
+    ldx = _need_rows(x, torch.bfloat16, None, None, "x")
+    rows, cols = x.shape
+    on = _On(x.device, stream)
+    if out is None:
+        out = _act8_empty(rows, cols, on)
+    _need_act8(out, rows, cols, "out", x.device)
+    _check(lib().zopt_act8_pack(rows, cols, _ptr(x), ldx, _ptr(out.q), _ptr(out.scale), on.handle),
+           "zopt_act8_pack")
+    return out
+
+
+def act8_unpack(a: Act8, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The bf16 matrix that a checkpoint stands for (zopt_act8_unpack)."""
+    _need_act8(a, None, None, "a")
+    rows, cols = a.q.shape
+    on = _On(a.q.device, stream)
+    if out is None:
+        out = on.empty((rows, cols), torch.bfloat16)
+    ld = _need_rows(out, torch.bfloat16, rows, cols, "out", a.q.device)
+    _check(lib().zopt_act8_unpack(rows, cols, _ptr(a.q), _ptr(a.scale), _ptr(out), ld, on.handle),
+           "zopt_act8_unpack")
+    return out
+
+
+def act8_wgrad(dy, a: Act8, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """dy^T x, bf16 [N, D], of dy bf16 [T, N] and the checkpoint a of x [T, D]:
+    a linear layer's weight gradient (zopt_act8_wgrad)."""
+    lddy = _need_rows(dy, torch.bfloat16, None, None, "dy")
+    T, N = dy.shape
+    _need_act8(a, T, None, "a", dy.device)
+    D = a.q.shape[1]
+    on = _On(dy.device, stream)
+    if out is None:
+        out = on.empty((N, D), torch.bfloat16)
+    ld = _need_rows(out, torch.bfloat16, N, D, "out", dy.device)
+    _sized(lib().zopt_act8_wgrad, (T, N, D, _ptr(dy), lddy, _ptr(a.q), _ptr(a.scale), _ptr(out), ld),
+           "zopt_act8_wgrad", on, workspace)
+    return out
+
+
+def _glu_weights(w_gate, w_up, D, dev):
+    ldw = _need_rows(w_gate, torch.bfloat16, None, D, "w_gate", dev)
+    F = w_gate.shape[0]
+    if _need_rows(w_up, torch.bfloat16, F, D, "w_up", dev) != ldw:
+        raise ValueError("w_up: row stride differs from w_gate's")
+    if F == 0:
+        raise ValueError("w_gate: no rows")
+    return F, ldw
+
+
+def _act_id(act):
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act: {act!r}, need one of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[act]
+
+
+def glu_forward(x, w_gate, w_up, act: str = "silu", checkpoint=False,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None):
+    """h = act(x w_gate^T) * (x w_up^T), bf16 [T, F] (zopt_glu_forward): x bf16
+    [T, D], w_gate and w_up bf16 [F, D] with one row stride, act "silu" or
+    "gelu" (tanh form).  With checkpoint=True, or a pair of Act8 to fill,
+    returns (h, (g, u)) with the two products kept in 8 bits for
+    glu_backward."""
+    ldx = _need_rows(x, torch.bfloat16, None, None, "x")
+    T, D = x.shape
+    dev = x.device
+    F, ldw = _glu_weights(w_gate, w_up, D, dev)
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty((T, F), torch.bfloat16)
+    ldh = _need_rows(out, torch.bfloat16, T, F, "out", dev)
+    kept = None
+    if checkpoint is True:
+        kept = (_act8_empty(T, F, on), _act8_empty(T, F, on))
+    elif checkpoint:
+        kept = checkpoint
+    if kept is not None:
+        _need_act8(kept[0], T, F, "checkpoint[0]", dev)
+        _need_act8(kept[1], T, F, "checkpoint[1]", dev)
+    c = [None] * 4 if kept is None else [_ptr(t) for a in kept for t in a]
+    _sized(lib().zopt_glu_forward, (T, D, F, _ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw,
+                                    _act_id(act), _ptr(out), ldh, *c),
+           "zopt_glu_forward", on, workspace)
+    return out if kept is None else (out, kept)
+
+
+def glu_backward(dh, x, w_gate, w_up, act: str = "silu", checkpoint=None,
+                 dx: Optional[torch.Tensor] = None, dw_gate: Optional[torch.Tensor] = None,
+                 dw_up: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dx, dw_gate, dw_up) of glu_forward from dh, bf16 [T, F]
+    (zopt_glu_backward).  x is the forward's input or its Act8; checkpoint the
+    pair that glu_forward returned, or None to compute g and u again.  h, if
+    given, receives act(g) u."""
+    lddh = _need_rows(dh, torch.bfloat16, None, None, "dh")
+    T, dev = dh.shape[0], dh.device
+    if isinstance(x, Act8):
+        _need_act8(x, T, None, "x", dev)
+        D, xa = x.q.shape[1], (None, x.q.shape[1], _ptr(x.q), _ptr(x.scale))
+    else:
+        ldx = _need_rows(x, torch.bfloat16, T, None, "x", dev)
+        D, xa = x.shape[1], (_ptr(x), ldx, None, None)
+    F, ldw = _glu_weights(w_gate, w_up, D, dev)
+    _need_rows(dh, torch.bfloat16, T, F, "dh", dev)
+    c = [None] * 4
+    if checkpoint is not None:
+        _need_act8(checkpoint[0], T, F, "checkpoint[0]", dev)
+        _need_act8(checkpoint[1], T, F, "checkpoint[1]", dev)
+        c = [_ptr(t) for a in checkpoint for t in a]
+    on = _On(dev, stream)
+    if dx is None:
+        dx = on.empty((T, D), torch.bfloat16)
+    if dw_gate is None:
+        dw_gate = on.empty((F, D), torch.bfloat16)
+    if dw_up is None:
+        dw_up = torch.empty_strided(dw_gate.shape, dw_gate.stride(), dtype=torch.bfloat16,
+                                    device=dev) if not on.other else on.empty((F, D), torch.bfloat16)
+    lddx = _need_rows(dx, torch.bfloat16, T, D, "dx", dev)
+    lddw = _need_rows(dw_gate, torch.bfloat16, F, D, "dw_gate", dev)
+    if _need_rows(dw_up, torch.bfloat16, F, D, "dw_up", dev) != lddw:
+        raise ValueError("dw_up: row stride differs from dw_gate's")
+    ldh = F if h is None else _need_rows(h, torch.bfloat16, T, F, "h", dev)
+    _sized(lib().zopt_glu_backward, (T, D, F, _ptr(dh), lddh, *xa, _ptr(w_gate), _ptr(w_up), ldw,
+                                     _act_id(act), *c, _ptr(h), ldh, _ptr(dx), lddx, _ptr(dw_gate),
+                                     _ptr(dw_up), lddw),
+           "zopt_glu_backward", on, workspace)
+    return dx, dw_gate, dw_up

@@ -1,0 +1,437 @@
+// train_api.hip -- the C-ABI entry points of the gradient operators (declared
+// in zopt.h): linear cross entropy, the gated feed-forward block, 8-bit
+// activation checkpoints.
+//
+// As everywhere in the library, arguments are checked first, the launches are
+// planned on the host, and everything is enqueued on the caller's stream
+// without synchronising.  Each call's plan is made by one function that both
+// the size query and the call itself run, so they cannot disagree.
+#include <cmath>
+
+#include "train_internal.h"
+#include "zopt.h"
+
+#define ZOPT_EXPORT extern "C" __attribute__((visibility("default")))
+
+namespace zopt {
+namespace {
+
+constexpr int64_t kMaxSide = 1 << 21;          // D, F, V: a 256-row panel stays below 2^31 bytes
+constexpr int64_t kMaxRows = 1 << 30;          // T
+constexpr int64_t kMaxStride = (1 << 22) - 8;  // of an operand read in place
+// Exponentials of the logits held at once (2 GiB, under 1% of the 288 GB).
+// Rows are taken in as few pieces as that allows: every piece after the first
+// reads and writes the fp32 sums of dW once (8 V D bytes), and 8192 rows of a
+// 131072-word vocabulary are one piece.
+constexpr int64_t kPieceBytes = (int64_t)1 << 31;
+
+inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// Offsets into a workspace, in order, 256-byte aligned.
+struct Carve {
+    size_t off = 0;
+    size_t take(int64_t bytes) {
+        const size_t at = off;
+        off += (size_t)up(bytes, 256);
+        return at;
+    }
+    // (never 0: a NULL workspace asks for the size)
+    size_t total() const { return off > 0 ? off : 256; }
+};
+
+// A 16-bit operand [rows, cols] as the products read it: in place if its
+// contiguous side, stride and base are multiples of 8 elements, else a padded
+// copy in the workspace.
+struct Input {
+    const uint16_t *p;
+    int64_t ld, rows, cols;
+    bool copy;
+    size_t at;
+};
+Input input(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, bool force, Carve &c) {
+    Input in{p, ld, rows, cols, false, 0};
+    in.copy = force || !aligned16(p) || (ld & 7) || (cols & 7) || ld > kMaxStride;
+    if (in.copy) {
+        in.ld = up(cols, 8);
+        in.at = c.take(rows * in.ld * 2);
+    }
+    return in;
+}
+hipError_t place(Input &in, int64_t src_ld, char *ws, const int64_t *target, int64_t ignore, hipStream_t s) {
+    if (!in.copy) return hipSuccess;
+    uint16_t *dst = reinterpret_cast<uint16_t *>(ws + in.at);
+    const hipError_t e = launch_pad_copy(in.p, src_ld, in.rows, in.cols, dst, target, ignore, s);
+    in.p = dst;
+    return e;
+}
+// rows [r0, r0 + n) of an operand that the reduction runs along (outer: rows)
+TgOperand along(const Input &in, int64_t r0, int64_t n) {
+    return TgOperand{in.p + r0 * in.ld, in.ld, (int32_t)n, (int32_t)up(in.cols, 8)};
+}
+// ... and across (reduction over the rows)
+TgOperand across(const Input &in, int64_t r0, int64_t n) {
+    return TgOperand{in.p + r0 * in.ld, in.ld, (int32_t)up(in.cols, 8), (int32_t)n};
+}
+TgSegment segment(const TgOperand &a, const TgOperand &b) {
+    const int32_t k = a.k > b.k ? a.k : b.k;
+    return TgSegment{a, b, (k + 31) / 32};
+}
+
+bool range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
+bool stride_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= ((int64_t)1 << 31); }
+
+zopt_status device(hipError_t e) { return e == hipSuccess ? ZOPT_OK : ZOPT_ERR_DEVICE; }
+#define ZOPT_TRY(x)                                 \
+    do {                                            \
+        const hipError_t e_ = (x);                  \
+        if (e_ != hipSuccess) return ZOPT_ERR_DEVICE; \
+    } while (0)
+
+zopt_status workspace_check(size_t need, void *workspace, size_t given) {
+    if (given < need || ((uintptr_t)workspace & 255)) return ZOPT_ERR_WORKSPACE;
+    return ZOPT_OK;
+}
+
+// ------------------------------------------------------- cross entropy plan
+
+struct XentPlan {
+    Input x, w;
+    int64_t piece;   // rows of a piece
+    int32_t pieces, groups;
+    int64_t lde;     // row stride of the exponentials
+    int64_t ldsum;
+    size_t e, stats, zt, lse, row, scal, sum, total;
+};
+XentPlan xent_plan(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw,
+                   bool dx, bool dw) {
+    XentPlan p{};
+    Carve c;
+    // (dW sums over rows: an ignored row must not reach it, whatever it holds)
+    p.x = input(x, ldx, T, D, dw, c);
+    p.w = input(w, ldw, V, D, false, c);
+    p.lde = up(V, 64);
+    p.groups = (int32_t)((V + kXentGroup - 1) / kXentGroup);
+    int64_t most = kPieceBytes / (2 * p.lde) / 256 * 256;
+    if (most < 256) most = 256;
+    p.pieces = (int32_t)((T + most - 1) / most);
+    if (p.pieces < 1) p.pieces = 1;
+    p.piece = up((T + p.pieces - 1) / p.pieces, 256);
+    if (p.piece > T) p.piece = T;
+    p.ldsum = up(D, 4);
+    if (dx || dw) p.e = c.take(p.piece * p.lde * 2);
+    p.stats = c.take(p.piece * p.groups * (int64_t)sizeof(float2));
+    p.zt = c.take(p.piece * 4);
+    p.lse = c.take(p.piece * 4);
+    p.row = c.take(T * 4);
+    p.scal = c.take(kXentScalars * 4);
+    if (dw && p.pieces > 1) p.sum = c.take(V * p.ldsum * 4);
+    p.total = c.total();
+    return p;
+}
+
+// ------------------------------------------------------------ gated block plan
+
+struct GluPlan {
+    Input x, wg, wu;
+    int64_t fp;      // row stride of dg and du
+    size_t dg, du, total;
+};
+GluPlan glu_plan(int64_t T, int64_t D, int64_t F, const uint16_t *x, int64_t ldx, const uint8_t *x8,
+                 const uint16_t *wg, const uint16_t *wu, int64_t ldw, bool back) {
+    GluPlan p{};
+    Carve c;
+    p.x = input(x, ldx, T, D, x8 != nullptr, c);
+    p.wg = input(wg, ldw, F, D, false, c);
+    p.wu = input(wu, ldw, F, D, false, c);
+    p.fp = up(F, 8);
+    if (back) {
+        p.dg = c.take(T * p.fp * 2);
+        p.du = c.take(T * p.fp * 2);
+    }
+    p.total = c.total();
+    return p;
+}
+
+bool vec8(const void *p, int64_t ld) { return aligned16(p) && (ld & 7) == 0; }
+bool vec4(const void *p, int64_t ld) { return ((uintptr_t)p & 7) == 0 && (ld & 3) == 0; }
+
+}  // namespace
+}  // namespace zopt
+
+using namespace zopt;
+
+ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t ldx,
+                                         const uint16_t *w, int64_t ldw, const int64_t *target, int64_t ignore_index,
+                                         int32_t mean, float grad_scale, float *loss, float *row_loss, uint16_t *dx,
+                                         int64_t lddx, uint16_t *dw, int64_t lddw, void *workspace,
+                                         size_t *workspace_bytes, void *stream) {
+    if (workspace_bytes == nullptr) return ZOPT_ERR_NULL;
+    if (!range(T, 0, kMaxRows) || !range(D, 1, kMaxSide) || !range(V, 1, kMaxSide)) return ZOPT_ERR_SIZE;
+    if (!stride_ok(ldx, D) || !stride_ok(ldw, D)) return ZOPT_ERR_SIZE;
+    if ((dx != nullptr && !stride_ok(lddx, D)) || (dw != nullptr && !stride_ok(lddw, D))) return ZOPT_ERR_SIZE;
+    XentPlan p = xent_plan(T, D, V, x, ldx, w, ldw, dx != nullptr, dw != nullptr);
+    if (workspace == nullptr) {
+        *workspace_bytes = p.total;
+        return ZOPT_OK;
+    }
+    if (w == nullptr || loss == nullptr || (T > 0 && (x == nullptr || target == nullptr))) return ZOPT_ERR_NULL;
+    if ((mean != 0 && mean != 1) || !std::isfinite(grad_scale)) return ZOPT_ERR_HYPER;
+    const zopt_status st = workspace_check(p.total, workspace, *workspace_bytes);
+    if (st != ZOPT_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    float *scal = reinterpret_cast<float *>(ws + p.scal);
+    float *row = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(ws + p.row);
+    ZOPT_TRY(launch_xent_count(target, T, ignore_index, mean, grad_scale, scal, s));
+    if (T == 0) {
+        ZOPT_TRY(launch_xent_total(row, 0, scal, loss, s));
+        if (dw != nullptr) ZOPT_TRY(launch_fill_zero(dw, lddw, V, D, s));
+        return ZOPT_OK;
+    }
+    ZOPT_TRY(place(p.x, ldx, ws, dw != nullptr ? target : nullptr, ignore_index, s));
+    ZOPT_TRY(place(p.w, ldw, ws, nullptr, 0, s));
+    uint16_t *e = dx != nullptr || dw != nullptr ? reinterpret_cast<uint16_t *>(ws + p.e) : nullptr;
+    float2 *stats = reinterpret_cast<float2 *>(ws + p.stats);
+    float *zt = reinterpret_cast<float *>(ws + p.zt), *lse = reinterpret_cast<float *>(ws + p.lse);
+    for (int32_t k = 0; k < p.pieces; ++k) {
+        const int64_t r0 = k * p.piece, n = T - r0 < p.piece ? T - r0 : p.piece;
+        if (n <= 0) break;
+        TgLaunch L{};
+        L.nprob = 1;
+        L.M = (int32_t)n;
+        L.N = (int32_t)V;
+        L.prob[0].nseg = 1;
+        L.prob[0].seg[0] = segment(along(p.x, r0, n), along(p.w, 0, V));
+        L.e = e;
+        L.lde = e != nullptr ? p.lde : 0;
+        L.stats = stats;
+        L.ldstat = n;
+        L.target = target + r0;
+        L.zt = zt;
+        ZOPT_TRY(launch_tg(kTgXent, false, false, L, s));
+        ZOPT_TRY(launch_xent_lse(stats, n, p.groups, target + r0, ignore_index, (int32_t)V, zt, n, lse, row + r0, s));
+        if (e == nullptr) continue;
+        ZOPT_TRY(launch_xent_probs(e, p.lde, n, (int32_t)V, stats, n, lse, row + r0, target + r0,
+                                   ignore_index, s));
+        const Input P{e, p.lde, n, V, false, 0};
+        if (dx != nullptr) {
+            TgLaunch G{};
+            G.nprob = 1;
+            G.M = (int32_t)n;
+            G.N = (int32_t)D;
+            G.prob[0].nseg = 1;
+            G.prob[0].seg[0] = segment(along(P, 0, n), across(p.w, 0, V));
+            G.prob[0].out = dx + r0 * lddx;
+            G.ldc = lddx;
+            G.vec = vec4(dx, lddx);
+            G.alpha = scal + kXentGrad;
+            ZOPT_TRY(launch_tg(kTgStore, false, true, G, s));
+        }
+        if (dw != nullptr) {
+            TgLaunch G{};
+            G.nprob = 1;
+            G.M = (int32_t)V;
+            G.N = (int32_t)D;
+            G.prob[0].nseg = 1;
+            G.prob[0].seg[0] = segment(across(P, 0, n), across(p.x, r0, n));
+            G.prob[0].out = dw;
+            G.prob[0].sum = reinterpret_cast<float *>(ws + p.sum);
+            G.ldc = lddw;
+            G.vec = vec4(dw, lddw);
+            G.alpha = scal + kXentGrad;
+            G.ldsum = p.ldsum;
+            G.sum_in = k > 0;
+            G.sum_out = r0 + n < T;
+            ZOPT_TRY(launch_tg(kTgStore, true, true, G, s));
+        }
+    }
+    ZOPT_TRY(launch_xent_total(row, T, scal, loss, s));
+    return ZOPT_OK;
+}
+
+ZOPT_EXPORT zopt_status zopt_glu_forward(int64_t T, int64_t D, int64_t F, const uint16_t *x, int64_t ldx,
+                                         const uint16_t *w_gate, const uint16_t *w_up, int64_t ldw, int32_t act,
+                                         uint16_t *h, int64_t ldh, uint8_t *g8, uint8_t *g_scale, uint8_t *u8,
+                                         uint8_t *u_scale, void *workspace, size_t *workspace_bytes, void *stream) {
+    if (workspace_bytes == nullptr) return ZOPT_ERR_NULL;
+    if (!range(T, 0, kMaxRows) || !range(D, 1, kMaxSide) || !range(F, 1, kMaxSide)) return ZOPT_ERR_SIZE;
+    if (!stride_ok(ldx, D) || !stride_ok(ldw, D) || !stride_ok(ldh, F)) return ZOPT_ERR_SIZE;
+    GluPlan p = glu_plan(T, D, F, x, ldx, nullptr, w_gate, w_up, ldw, false);
+    if (workspace == nullptr) {
+        *workspace_bytes = p.total;
+        return ZOPT_OK;
+    }
+    if (w_gate == nullptr || w_up == nullptr || (T > 0 && (x == nullptr || h == nullptr))) return ZOPT_ERR_NULL;
+    const bool keep = g8 != nullptr || g_scale != nullptr || u8 != nullptr || u_scale != nullptr;
+    if (keep && T > 0 && (g8 == nullptr || g_scale == nullptr || u8 == nullptr || u_scale == nullptr))
+        return ZOPT_ERR_NULL;
+    if (act != kActSilu && act != kActGelu) return ZOPT_ERR_HYPER;
+    const zopt_status st = workspace_check(p.total, workspace, *workspace_bytes);
+    if (st != ZOPT_OK) return st;
+    if (T == 0) return ZOPT_OK;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    ZOPT_TRY(place(p.x, ldx, ws, nullptr, 0, s));
+    ZOPT_TRY(place(p.wg, ldw, ws, nullptr, 0, s));
+    ZOPT_TRY(place(p.wu, ldw, ws, nullptr, 0, s));
+    TgLaunch L{};
+    L.nprob = 1;
+    L.M = (int32_t)T;
+    L.N = (int32_t)F;
+    L.prob[0].nseg = 1;
+    L.prob[0].seg[0] = segment(along(p.x, 0, T), along(p.wg, 0, F));
+    L.prob[0].seg[1] = segment(along(p.x, 0, T), along(p.wu, 0, F));
+    L.act = act;
+    L.h = h;
+    L.ldc = ldh;
+    L.vec = vec8(h, ldh);
+    L.g8 = g8;
+    L.gs = g_scale;
+    L.u8 = u8;
+    L.us = u_scale;
+    return device(launch_tg(kTgGlu, false, false, L, s));
+}
+
+ZOPT_EXPORT zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const uint16_t *dh, int64_t lddh,
+                                          const uint16_t *x, int64_t ldx, const uint8_t *x8, const uint8_t *x_scale,
+                                          const uint16_t *w_gate, const uint16_t *w_up, int64_t ldw, int32_t act,
+                                          const uint8_t *g8, const uint8_t *g_scale, const uint8_t *u8,
+                                          const uint8_t *u_scale, uint16_t *h, int64_t ldh, uint16_t *dx,
+                                          int64_t lddx, uint16_t *dw_gate, uint16_t *dw_up, int64_t lddw,
+                                          void *workspace, size_t *workspace_bytes, void *stream) {
+    if (workspace_bytes == nullptr) return ZOPT_ERR_NULL;
+    if (!range(T, 0, kMaxRows) || !range(D, 1, kMaxSide) || !range(F, 1, kMaxSide)) return ZOPT_ERR_SIZE;
+    if (!stride_ok(lddh, F) || !stride_ok(ldw, D) || (x8 == nullptr && !stride_ok(ldx, D))) return ZOPT_ERR_SIZE;
+    if (!stride_ok(lddx, D) || !stride_ok(lddw, D) || (h != nullptr && !stride_ok(ldh, F))) return ZOPT_ERR_SIZE;
+    GluPlan p = glu_plan(T, D, F, x, ldx, x8, w_gate, w_up, ldw, true);
+    if (workspace == nullptr) {
+        *workspace_bytes = p.total;
+        return ZOPT_OK;
+    }
+    if (w_gate == nullptr || w_up == nullptr || dw_gate == nullptr || dw_up == nullptr) return ZOPT_ERR_NULL;
+    if (T > 0 && (dh == nullptr || dx == nullptr)) return ZOPT_ERR_NULL;
+    if (T > 0 && (x8 == nullptr ? x == nullptr : x_scale == nullptr)) return ZOPT_ERR_NULL;
+    const bool kept = g8 != nullptr || g_scale != nullptr || u8 != nullptr || u_scale != nullptr;
+    if (kept && T > 0 && (g8 == nullptr || g_scale == nullptr || u8 == nullptr || u_scale == nullptr))
+        return ZOPT_ERR_NULL;
+    if (act != kActSilu && act != kActGelu) return ZOPT_ERR_HYPER;
+    const zopt_status st = workspace_check(p.total, workspace, *workspace_bytes);
+    if (st != ZOPT_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    if (T == 0) {
+        ZOPT_TRY(launch_fill_zero(dw_gate, lddw, F, D, s));
+        ZOPT_TRY(launch_fill_zero(dw_up, lddw, F, D, s));
+        return ZOPT_OK;
+    }
+    if (x8 != nullptr) {
+        uint16_t *dst = reinterpret_cast<uint16_t *>(ws + p.x.at);
+        ZOPT_TRY(launch_act8_unpack(x8, x_scale, T, D, dst, p.x.ld, p.x.ld, s));
+        p.x.p = dst;
+    } else {
+        ZOPT_TRY(place(p.x, ldx, ws, nullptr, 0, s));
+    }
+    ZOPT_TRY(place(p.wg, ldw, ws, nullptr, 0, s));
+    ZOPT_TRY(place(p.wu, ldw, ws, nullptr, 0, s));
+    uint16_t *dg = reinterpret_cast<uint16_t *>(ws + p.dg), *du = reinterpret_cast<uint16_t *>(ws + p.du);
+    if (kept) {
+        ZOPT_TRY(launch_glu_back_act8(g8, g_scale, u8, u_scale, dh, lddh, T, F, act, dg, du, p.fp, h, ldh, s));
+    } else {
+        TgLaunch L{};
+        L.nprob = 1;
+        L.M = (int32_t)T;
+        L.N = (int32_t)F;
+        L.prob[0].nseg = 1;
+        L.prob[0].seg[0] = segment(along(p.x, 0, T), along(p.wg, 0, F));
+        L.prob[0].seg[1] = segment(along(p.x, 0, T), along(p.wu, 0, F));
+        L.act = act;
+        L.h = h;
+        L.ldc = ldh;
+        L.vec = vec8(h, ldh);
+        L.dh = dh;
+        L.lddh = lddh;
+        L.dhvec = vec8(dh, lddh);
+        L.dg = dg;
+        L.du = du;
+        L.lddg = p.fp;
+        ZOPT_TRY(launch_tg(kTgGluBack, false, false, L, s));
+    }
+    const Input DG{dg, p.fp, T, F, false, 0}, DU{du, p.fp, T, F, false, 0};
+    {
+        TgLaunch G{};
+        G.nprob = 1;
+        G.M = (int32_t)T;
+        G.N = (int32_t)D;
+        G.prob[0].nseg = 2;
+        G.prob[0].seg[0] = segment(along(DG, 0, T), across(p.wg, 0, F));
+        G.prob[0].seg[1] = segment(along(DU, 0, T), across(p.wu, 0, F));
+        G.prob[0].out = dx;
+        G.ldc = lddx;
+        G.vec = vec4(dx, lddx);
+        ZOPT_TRY(launch_tg(kTgStore, false, true, G, s));
+    }
+    TgLaunch G{};
+    G.nprob = 2;
+    G.M = (int32_t)F;
+    G.N = (int32_t)D;
+    G.prob[0].nseg = G.prob[1].nseg = 1;
+    G.prob[0].seg[0] = segment(across(DG, 0, T), across(p.x, 0, T));
+    G.prob[1].seg[0] = segment(across(DU, 0, T), across(p.x, 0, T));
+    G.prob[0].out = dw_gate;
+    G.prob[1].out = dw_up;
+    G.ldc = lddw;
+    G.vec = vec4(dw_gate, lddw) && vec4(dw_up, lddw);
+    return device(launch_tg(kTgStore, true, true, G, s));
+}
+
+ZOPT_EXPORT zopt_status zopt_act8_pack(int64_t rows, int64_t cols, const uint16_t *x, int64_t ldx, uint8_t *q,
+                                       uint8_t *scale, void *stream) {
+    if (!range(rows, 0, kMaxRows) || !range(cols, 1, kMaxSide) || !stride_ok(ldx, cols)) return ZOPT_ERR_SIZE;
+    if (rows == 0) return ZOPT_OK;
+    if (x == nullptr || q == nullptr || scale == nullptr) return ZOPT_ERR_NULL;
+    return device(launch_act8_pack(x, ldx, rows, cols, q, scale, static_cast<hipStream_t>(stream)));
+}
+
+ZOPT_EXPORT zopt_status zopt_act8_unpack(int64_t rows, int64_t cols, const uint8_t *q, const uint8_t *scale,
+                                         uint16_t *x, int64_t ldx, void *stream) {
+    if (!range(rows, 0, kMaxRows) || !range(cols, 1, kMaxSide) || !stride_ok(ldx, cols)) return ZOPT_ERR_SIZE;
+    if (rows == 0) return ZOPT_OK;
+    if (x == nullptr || q == nullptr || scale == nullptr) return ZOPT_ERR_NULL;
+    return device(launch_act8_unpack(q, scale, rows, cols, x, ldx, cols, static_cast<hipStream_t>(stream)));
+}
+
+ZOPT_EXPORT zopt_status zopt_act8_wgrad(int64_t T, int64_t N, int64_t D, const uint16_t *dy, int64_t lddy,
+                                        const uint8_t *q, const uint8_t *scale, uint16_t *dw, int64_t lddw,
+                                        void *workspace, size_t *workspace_bytes, void *stream) {
+    if (workspace_bytes == nullptr) return ZOPT_ERR_NULL;
+    if (!range(T, 0, kMaxRows) || !range(N, 1, kMaxSide) || !range(D, 1, kMaxSide)) return ZOPT_ERR_SIZE;
+    if (!stride_ok(lddy, N) || !stride_ok(lddw, D)) return ZOPT_ERR_SIZE;
+    Carve c;
+    Input x = input(nullptr, D, T, D, true, c);
+    Input y = input(dy, lddy, T, N, false, c);
+    if (workspace == nullptr) {
+        *workspace_bytes = c.total();
+        return ZOPT_OK;
+    }
+    if (dw == nullptr || (T > 0 && (dy == nullptr || q == nullptr || scale == nullptr))) return ZOPT_ERR_NULL;
+    const zopt_status st = workspace_check(c.total(), workspace, *workspace_bytes);
+    if (st != ZOPT_OK) return st;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    char *ws = static_cast<char *>(workspace);
+    if (T == 0) return device(launch_fill_zero(dw, lddw, N, D, s));
+    uint16_t *dst = reinterpret_cast<uint16_t *>(ws + x.at);
+    ZOPT_TRY(launch_act8_unpack(q, scale, T, D, dst, x.ld, x.ld, s));
+    x.p = dst;
+    ZOPT_TRY(place(y, lddy, ws, nullptr, 0, s));
+    TgLaunch G{};
+    G.nprob = 1;
+    G.M = (int32_t)N;
+    G.N = (int32_t)D;
+    G.prob[0].nseg = 1;
+    G.prob[0].seg[0] = segment(across(y, 0, T), across(x, 0, T));
+    G.prob[0].out = dw;
+    G.ldc = lddw;
+    G.vec = vec4(dw, lddw);
+    return device(launch_tg(kTgStore, true, true, G, s));
+}

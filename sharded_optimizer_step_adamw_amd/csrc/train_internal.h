@@ -1,0 +1,243 @@
+// train_internal.h -- declarations shared by the operators that produce a
+// rank's gradients: linear cross entropy, the gated feed-forward block and
+// 8-bit activation checkpoints (train_gemm.hip, train_rows.hip, train_api.hip).
+#pragma once
+
+#include "zopt_internal.h"
+
+namespace zopt {
+
+// ------------------------------------------------------- matrix products
+//
+// C[M x N] = sum over segments of A B^T.  Each operand is a 16-bit matrix
+// whose contiguous side is a multiple of 8 elements, as are its row stride
+// and its base's alignment (operands that are not are copied into the
+// workspace first); outer is the side that indexes C (M or N), k the reduction.
+//   row-major  [outer, k]   (k contiguous)
+//   k-major    [k, outer]   (outer contiguous)
+// Everything outside outer x k reads as zero.
+struct TgOperand {
+    const uint16_t *p;
+    int64_t ld;        // elements between rows, < 2^22
+    int32_t outer, k;  // extents
+};
+
+struct TgSegment {
+    TgOperand a, b;
+    int32_t stages;    // ceil(max(a.k, b.k) / 32)
+};
+
+// What becomes of a tile:
+//   kTgStore    alpha * sum -> bf16 (or fp32 sums, see below)
+//   kTgXent     exponentials and row statistics of a piece of logits
+//   kTgGlu      act(g) u from interleaved gate / up columns, with checkpoints
+//   kTgGluBack  dg, du (and h) from g, u and dh
+enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3 };
+
+enum TgAct : int { kActSilu = 0, kActGelu = 1 };
+
+struct TgProblem {
+    TgSegment seg[2];
+    int32_t nseg;
+    uint16_t *out;     // bf16 [M, N], row stride ldc
+    float *sum;        // fp32 [M, N] (row stride ldsum), or NULL
+};
+
+struct TgLaunch {
+    TgProblem prob[2];
+    int32_t nprob;
+    int32_t M, N;             // output sizes (Glu: N = feed-forward width)
+    int32_t tiles_m, tiles_n; // grid of output tiles
+    int64_t ldc;
+    int32_t vec;              // outputs take vector stores
+    // kTgStore
+    const float *alpha;       // device scalar, or NULL: 1
+    int64_t ldsum;
+    int32_t sum_in, sum_out;  // add prob.sum first; write fp32 to prob.sum (else bf16 to out)
+    // kTgXent: e [M, lde] fp16 (NULL: statistics only), per 64-column group g
+    // and row r stats[g * ldstat + r] = (max, sum of exponentials); the
+    // target's logit to zt
+    uint16_t *e;
+    int64_t lde;
+    float2 *stats;
+    int64_t ldstat;
+    const int64_t *target;
+    float *zt;
+    // kTgGlu / kTgGluBack (row strides: h ldc; q F bytes; scale ceil(F / 32); dh lddh; dg, du lddg)
+    int32_t act;
+    uint16_t *h;              // kTgGluBack: may be NULL
+    uint8_t *g8, *u8;         // checkpoint values, or NULL
+    uint8_t *gs, *us;
+    const uint16_t *dh;
+    int64_t lddh;
+    int32_t dhvec;
+    uint16_t *dg, *du;        // row stride lddg, columns [N, round up to 8) written as zero
+    int64_t lddg;
+};
+
+constexpr int kXentGroup = 64;  // columns per statistics group
+
+// a_km / b_km: operand is k-major.  kTgXent and the Glu kinds: both row-major.
+hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStream_t stream);
+
+// ------------------------------------------------------------- row passes
+
+// dst [rows, round8(cols)] = src [rows, cols], zero beyond cols and in rows
+// whose target is `ignore` (target NULL: none).
+hipError_t launch_pad_copy(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols,
+                           uint16_t *dst, const int64_t *target, int64_t ignore,
+                           hipStream_t stream);
+hipError_t launch_fill_zero(uint16_t *dst, int64_t ld, int64_t rows, int64_t cols,
+                            hipStream_t stream);
+
+hipError_t launch_act8_pack(const uint16_t *x, int64_t ld, int64_t rows, int64_t cols, uint8_t *q,
+                            uint8_t *scale, hipStream_t stream);
+// columns [cols, cols_out) are written as zero
+hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
+                              uint16_t *x, int64_t ld, int64_t cols_out, hipStream_t stream);
+
+// Scalars of a linear cross entropy call in device memory.
+enum : int { kXentShare = 0, kXentGrad = 1, kXentScalars = 2 };
+// scal[kXentShare] = 1 or 1 / valid rows (0 if none); scal[kXentGrad] = that * grad_scale
+hipError_t launch_xent_count(const int64_t *target, int64_t rows, int64_t ignore, int32_t mean,
+                             float grad_scale, float *scal, hipStream_t stream);
+// lse and row loss of rows [0, rows) from the group statistics
+hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups,
+                           const int64_t *target, int64_t ignore, int32_t V, const float *zt,
+                           int64_t rows, float *lse, float *row_loss, hipStream_t stream);
+// e (fp16 exponentials) -> P = softmax - onehot (bf16), in place, columns [V, lde) zero
+hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V,
+                             const float2 *stats, int64_t ldstat, const float *lse,
+                             const float *row_loss, const int64_t *target, int64_t ignore,
+                             hipStream_t stream);
+hipError_t launch_xent_total(const float *row_loss, int64_t rows, const float *scal, float *loss,
+                             hipStream_t stream);
+
+// dg, du (row stride lddg, zero in columns [F, round8(F))) and h (or NULL)
+// from a checkpoint of g and u and from dh
+hipError_t launch_glu_back_act8(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8,
+                                const uint8_t *us, const uint16_t *dh, int64_t lddh, int64_t rows,
+                                int64_t F, int32_t act, uint16_t *dg, uint16_t *du, int64_t lddg,
+                                uint16_t *h, int64_t ldh, hipStream_t stream);
+
+// ---------------------------------------------------------- device helpers
+
+// two fp32 -> two bf16 / fp16, round to nearest even, one instruction each; a
+// NaN stays a NaN
+typedef __bf16 tg_bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 tg_f16x2 __attribute__((ext_vector_type(2)));
+typedef float tg_f32x2 __attribute__((ext_vector_type(2)));
+typedef float tg_f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t tg_u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t tg_u32x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t tg_pack_bf16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(tg_f32x2{lo, hi}, tg_bf16x2));
+}
+__device__ __forceinline__ uint32_t tg_pack_f16(float lo, float hi) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(tg_f32x2{lo, hi}, tg_f16x2));
+}
+
+// An activation's value and derivative.  silu(g) = g s(g) with the logistic
+// s; gelu's tanh form is g s(y), y = sqrt(8 / pi) (g + 0.044715 g^3), since
+// (1 + tanh(y / 2)) / 2 = s(y).
+struct TgActValue {
+    float a, da;
+};
+__device__ __forceinline__ TgActValue tg_act(float g, int32_t act) {
+    float y = g, dy = 1.0f;
+    if (act == kActGelu) {
+        const float k = 1.5957691216057308f;
+        const float g2 = g * g;
+        y = k * (g + 0.044715f * (g2 * g));
+        dy = k * (1.0f + 0.134145f * g2);
+    }
+    const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-y));
+    return {g * s, s + g * (s * (1.0f - s)) * dy};
+}
+
+// The 8-bit checkpoint's scale byte from the bit pattern of a block's largest
+// magnitude (as an integer, so NaN > Inf > finite): the smallest power of two
+// 2^(byte - 127) with amax <= 448 * 2^(byte - 127), 448 = 1.75 * 2^8 being
+// e4m3's largest value, and at least 2^-124, below which a product with
+// e4m3's subnormals would leave bf16's; 255 if a value is not finite.
+__device__ __forceinline__ uint32_t tg_scale_byte(uint32_t amax_bits) {
+    if (amax_bits >= 0x7F800000u) return 255u;
+    const int e = (int)(amax_bits >> 23) - 8 + ((amax_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return e < 3 ? 3u : (uint32_t)e;
+}
+// 2^(127 - byte), what values are multiplied with (NaN for byte 255), and
+// 2^(byte - 127), what they are read back with
+__device__ __forceinline__ float tg_scale_in(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float((254u - byte) << 23);
+}
+__device__ __forceinline__ float tg_scale_out(uint32_t byte) {
+    return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
+}
+// Eight fp32 -> eight e4m3 of v * 2^(127 - byte), round to nearest even, low
+// first.  At the topmost scale, 2^120, 240 is the largest code: the next one,
+// 256, stands for 2^128, which no bf16 holds (and 240 is within 2^-4 of every
+// value up to the largest fp32).
+__device__ __forceinline__ tg_u32x2 tg_pack_e4m3(const float (&x)[8], uint32_t byte) {
+    const float s = tg_scale_in(byte), top = byte == 247u ? 240.0f : 448.0f;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = __builtin_amdgcn_fmed3f(x[k] * s, -top, top);
+    int lo = 0, hi = 0;
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], lo, false);
+    lo = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], lo, true);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[4], v[5], hi, false);
+    hi = __builtin_amdgcn_cvt_pk_fp8_f32(v[6], v[7], hi, true);
+    return tg_u32x2{(uint32_t)lo, (uint32_t)hi};
+}
+__device__ __forceinline__ void tg_unpack_e4m3(tg_u32x2 q, float s, float (&v)[8]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int w = (int)(h ? q.y : q.x);
+        const tg_f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+        const tg_f32x2 b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+        v[4 * h + 0] = a.x * s;
+        v[4 * h + 1] = a.y * s;
+        v[4 * h + 2] = b.x * s;
+        v[4 * h + 3] = b.y * s;
+    }
+}
+
+// up to 8 bytes / 16-bit values at p, of which the first n (< 8: the others
+// are not touched) exist; vec: p is aligned for one access
+__device__ __forceinline__ tg_u32x2 tg_load8b(const uint8_t *p, int n, bool vec) {
+    if (vec && n >= 8) return *reinterpret_cast<const tg_u32x2 *>(p);
+    tg_u32x2 r{0, 0};
+    for (int k = 0; k < 8; ++k)
+        if (k < n) {
+            if (k < 4) r.x |= (uint32_t)p[k] << (8 * k);
+            else r.y |= (uint32_t)p[k] << (8 * (k - 4));
+        }
+    return r;
+}
+__device__ __forceinline__ void tg_store8b(uint8_t *p, tg_u32x2 v, int n, bool vec) {
+    if (vec && n >= 8) {
+        *reinterpret_cast<tg_u32x2 *>(p) = v;
+        return;
+    }
+    for (int k = 0; k < 8; ++k)
+        if (k < n) p[k] = (uint8_t)((k < 4 ? v.x >> (8 * k) : v.y >> (8 * (k - 4))) & 0xFFu);
+}
+__device__ __forceinline__ tg_u32x4 tg_load8h(const uint16_t *p, int n, bool vec) {
+    if (vec && n >= 8) return *reinterpret_cast<const tg_u32x4 *>(p);
+    tg_u32x4 r{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < n) r[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
+    return r;
+}
+__device__ __forceinline__ void tg_store8h(uint16_t *p, tg_u32x4 v, int n, bool vec) {
+    if (vec && n >= 8) {
+        *reinterpret_cast<tg_u32x4 *>(p) = v;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        if (k < n) p[k] = (uint16_t)((v[k >> 1] >> (16 * (k & 1))) & 0xFFFFu);
+}
+
+}  // namespace zopt
