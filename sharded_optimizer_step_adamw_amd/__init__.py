@@ -624,21 +624,33 @@ class _On:
         with torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=self.device)):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def workspace(self, given, need):
-        if given is None:
-            return self.empty(need, torch.uint8)
-        _need(given, torch.uint8, need, "workspace", self.device)
-        return given
+
+_sizes = {}
 
 
-def _sized(fn, args, where, on, workspace):
+def _sized(fn, args, pointers, where, on, workspace):
     """Runs fn(*args, workspace, size, stream) with a workspace of the size
-    that the same call asks for."""
-    size = ctypes.c_size_t(0)
-    _check(fn(*args, None, ctypes.byref(size), None), f"{where}(workspace query)")
-    ws = on.workspace(workspace, int(size.value))
-    size.value = ws.numel()
-    _check(fn(*args, ws.data_ptr(), ctypes.byref(size), on.handle), where)
+    that the same call asks for.  That size depends on the arguments but for
+    where the pointers (indices `pointers` of args) point, their alignment
+    apart; it is asked for once per such set of arguments."""
+    if workspace is None:
+        key = list(args)
+        for i in pointers:
+            p = key[i]
+            key[i] = None if p is None else p & 15
+        key = (where, *key)
+        need = _sizes.get(key)
+        if need is None:
+            size = ctypes.c_size_t(0)
+            _check(fn(*args, None, ctypes.byref(size), None), f"{where}(workspace query)")
+            if len(_sizes) >= 4096:
+                _sizes.clear()
+            need = _sizes[key] = int(size.value)
+        workspace = on.empty(need, torch.uint8)
+    else:
+        _need(workspace, torch.uint8, 0, "workspace", on.device)
+    size = ctypes.c_size_t(workspace.numel())
+    _check(fn(*args, workspace.data_ptr(), ctypes.byref(size), on.handle), where)
 
 
 def _linear_xent(x, w, target, ignore_index, mean, grad_scale, loss, row_loss, dx, dw, want_dx,
@@ -667,7 +679,7 @@ def _linear_xent(x, w, target, ignore_index, mean, grad_scale, loss, row_loss, d
     # (a tensor of no rows has no address; the call takes NULL for "not wanted")
     args = (T, D, V, _ptr(x), ldx, _ptr(w), ldw, _ptr(target), int(ignore_index), int(mean),
             float(grad_scale), _ptr(loss), _ptr(row_loss), _ptr(dx), lddx, _ptr(dw), lddw)
-    _sized(lib().zopt_linear_xent, args, "zopt_linear_xent", on, workspace)
+    _sized(lib().zopt_linear_xent, args, (3, 5, 7, 11, 12, 13, 15), "zopt_linear_xent", on, workspace)
     return loss, row_loss, dx, dw
 
 
@@ -740,7 +752,7 @@ def act8_wgrad(dy, a: Act8, out: Optional[torch.Tensor] = None,
         out = on.empty((N, D), torch.bfloat16)
     ld = _need_rows(out, torch.bfloat16, N, D, "out", dy.device)
     _sized(lib().zopt_act8_wgrad, (T, N, D, _ptr(dy), lddy, _ptr(a.q), _ptr(a.scale), _ptr(out), ld),
-           "zopt_act8_wgrad", on, workspace)
+           (3, 5, 6, 7), "zopt_act8_wgrad", on, workspace)
     return out
 
 
@@ -787,7 +799,7 @@ def glu_forward(x, w_gate, w_up, act: str = "silu", checkpoint=False,
     c = [None] * 4 if kept is None else [_ptr(t) for a in kept for t in a]
     _sized(lib().zopt_glu_forward, (T, D, F, _ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw,
                                     _act_id(act), _ptr(out), ldh, *c),
-           "zopt_glu_forward", on, workspace)
+           (3, 5, 6, 9, 11, 12, 13, 14), "zopt_glu_forward", on, workspace)
     return out if kept is None else (out, kept)
 
 
@@ -830,5 +842,5 @@ def glu_backward(dh, x, w_gate, w_up, act: str = "silu", checkpoint=None,
     _sized(lib().zopt_glu_backward, (T, D, F, _ptr(dh), lddh, *xa, _ptr(w_gate), _ptr(w_up), ldw,
                                      _act_id(act), *c, _ptr(h), ldh, _ptr(dx), lddx, _ptr(dw_gate),
                                      _ptr(dw_up), lddw),
-           "zopt_glu_backward", on, workspace)
+           (3, 5, 7, 8, 9, 10, 13, 14, 15, 16, 17, 19, 21, 22), "zopt_glu_backward", on, workspace)
     return dx, dw_gate, dw_up

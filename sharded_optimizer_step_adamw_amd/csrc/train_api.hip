@@ -49,9 +49,12 @@ struct Input {
     bool copy;
     size_t at;
 };
+bool in_place(const uint16_t *p, int64_t ld, int64_t cols) {
+    return aligned16(p) && !(ld & 7) && !(cols & 7) && ld <= kMaxStride;
+}
 Input input(const uint16_t *p, int64_t ld, int64_t rows, int64_t cols, bool force, Carve &c) {
     Input in{p, ld, rows, cols, false, 0};
-    in.copy = force || !aligned16(p) || (ld & 7) || (cols & 7) || ld > kMaxStride;
+    in.copy = force || !in_place(p, ld, cols);
     if (in.copy) {
         in.ld = up(cols, 8);
         in.at = c.take(rows * in.ld * 2);
@@ -78,6 +81,38 @@ TgSegment segment(const TgOperand &a, const TgOperand &b) {
     return TgSegment{a, b, (k + 31) / 32};
 }
 
+// A product's launch over one or two problems of the same sizes.
+struct Product {
+    TgLaunch L{};
+    Product(TgEpilogue epi, int64_t M, int64_t N, const TgSegment &s0, const TgSegment *s1 = nullptr) : epi(epi) {
+        L.nprob = 1;
+        L.M = (int32_t)M;
+        L.N = (int32_t)N;
+        L.prob[0].seg[0] = s0;
+        L.prob[0].nseg = s1 ? 2 : 1;
+        if (s1) L.prob[0].seg[1] = *s1;
+    }
+    void second(const TgSegment &s) {
+        L.prob[1].seg[0] = s;
+        L.prob[1].nseg = 1;
+        L.nprob = 2;
+    }
+    // scratch for the parts of a split reduction
+    size_t parts() {
+        plan_tg(epi, L);
+        return tg_part_bytes(L);
+    }
+    hipError_t run(bool a_km, bool b_km, char *part, hipStream_t s) {
+        plan_tg(epi, L);
+        L.part = reinterpret_cast<float *>(part);
+        return launch_tg(epi, a_km, b_km, L, s);
+    }
+
+   private:
+    TgEpilogue epi;
+};
+inline size_t larger(size_t a, size_t b) { return a > b ? a : b; }
+
 bool range(int64_t v, int64_t lo, int64_t hi) { return v >= lo && v <= hi; }
 bool stride_ok(int64_t ld, int64_t cols) { return ld >= cols && ld <= ((int64_t)1 << 31); }
 
@@ -100,8 +135,22 @@ struct XentPlan {
     int64_t piece;   // rows of a piece
     int32_t pieces, groups;
     int64_t lde;     // row stride of the exponentials
-    int64_t ldsum;
-    size_t e, stats, zt, lse, row, scal, sum, total;
+    size_t e, stats, zt, lse, row, factor, sum, part, total;
+    Input probs(char *ws, int64_t n) const {
+        return Input{reinterpret_cast<const uint16_t *>(ws + e), lde, n, w.rows, false, 0};
+    }
+    Product logits(int64_t r0, int64_t n) const {
+        return Product(kTgXent, n, w.rows, segment(along(x, r0, n), along(w, 0, w.rows)));
+    }
+    Product dx(char *ws, int64_t n) const {
+        return Product(kTgStore, n, w.cols, segment(along(probs(ws, n), 0, n), across(w, 0, w.rows)));
+    }
+    Product dw(char *ws, int64_t r0, int64_t n) const {
+        Product p(kTgStore, w.rows, w.cols, segment(across(probs(ws, n), 0, n), across(x, r0, n)));
+        p.L.sum_in = r0 > 0;
+        p.L.sum_out = r0 + n < x.rows;
+        return p;
+    }
 };
 XentPlan xent_plan(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t ldx, const uint16_t *w, int64_t ldw,
                    bool dx, bool dw) {
@@ -118,14 +167,22 @@ XentPlan xent_plan(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t l
     if (p.pieces < 1) p.pieces = 1;
     p.piece = up((T + p.pieces - 1) / p.pieces, 256);
     if (p.piece > T) p.piece = T;
-    p.ldsum = up(D, 4);
     if (dx || dw) p.e = c.take(p.piece * p.lde * 2);
     p.stats = c.take(p.piece * p.groups * (int64_t)sizeof(float2));
     p.zt = c.take(p.piece * 4);
     p.lse = c.take(p.piece * 4);
     p.row = c.take(T * 4);
-    p.scal = c.take(kXentScalars * 4);
-    if (dw && p.pieces > 1) p.sum = c.take(V * p.ldsum * 4);
+    p.factor = c.take(4);
+    if (dw && p.pieces > 1) p.sum = c.take(V * up(D, 4) * 4);
+    size_t parts = 0;
+    for (int32_t k = 0; k < p.pieces; ++k) {
+        const int64_t r0 = k * p.piece, n = T - r0 < p.piece ? T - r0 : p.piece;
+        if (n <= 0) break;
+        if (k > 0 && r0 + n < T) continue;  // (pieces between are as the first)
+        if (dx) parts = larger(parts, p.dx(nullptr, n).parts());
+        if (dw) parts = larger(parts, p.dw(nullptr, r0, n).parts());
+    }
+    p.part = c.take(parts);
     p.total = c.total();
     return p;
 }
@@ -135,19 +192,39 @@ XentPlan xent_plan(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t l
 struct GluPlan {
     Input x, wg, wu;
     int64_t fp;      // row stride of dg and du
-    size_t dg, du, total;
+    size_t dg, du, part, total;
+    Input grad(char *ws, size_t at) const {
+        return Input{reinterpret_cast<const uint16_t *>(ws + at), fp, x.rows, wg.rows, false, 0};
+    }
+    Product products(TgEpilogue epi) const {
+        const TgSegment up = segment(along(x, 0, x.rows), along(wu, 0, wu.rows));
+        return Product(epi, x.rows, wg.rows, segment(along(x, 0, x.rows), along(wg, 0, wg.rows)), &up);
+    }
+    Product dx(char *ws) const {
+        const TgSegment up = segment(along(grad(ws, du), 0, x.rows), across(wu, 0, wu.rows));
+        return Product(kTgStore, x.rows, x.cols,
+                       segment(along(grad(ws, dg), 0, x.rows), across(wg, 0, wg.rows)), &up);
+    }
+    Product dw(char *ws) const {
+        Product p(kTgStore, wg.rows, x.cols, segment(across(grad(ws, dg), 0, x.rows), across(x, 0, x.rows)));
+        p.second(segment(across(grad(ws, du), 0, x.rows), across(x, 0, x.rows)));
+        return p;
+    }
 };
 GluPlan glu_plan(int64_t T, int64_t D, int64_t F, const uint16_t *x, int64_t ldx, const uint8_t *x8,
                  const uint16_t *wg, const uint16_t *wu, int64_t ldw, bool back) {
     GluPlan p{};
     Carve c;
     p.x = input(x, ldx, T, D, x8 != nullptr, c);
-    p.wg = input(wg, ldw, F, D, false, c);
-    p.wu = input(wu, ldw, F, D, false, c);
+    // (the products take both with one row stride)
+    const bool copy = !in_place(wg, ldw, D) || !in_place(wu, ldw, D);
+    p.wg = input(wg, ldw, F, D, copy, c);
+    p.wu = input(wu, ldw, F, D, copy, c);
     p.fp = up(F, 8);
     if (back) {
         p.dg = c.take(T * p.fp * 2);
         p.du = c.take(T * p.fp * 2);
+        if (T > 0) p.part = c.take(larger(p.dx(nullptr).parts(), p.dw(nullptr).parts()));
     }
     p.total = c.total();
     return p;
@@ -181,14 +258,15 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
     if (st != ZOPT_OK) return st;
     hipStream_t s = static_cast<hipStream_t>(stream);
     char *ws = static_cast<char *>(workspace);
-    float *scal = reinterpret_cast<float *>(ws + p.scal);
+    float *factor = reinterpret_cast<float *>(ws + p.factor);
     float *row = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(ws + p.row);
-    ZOPT_TRY(launch_xent_count(target, T, ignore_index, mean, grad_scale, scal, s));
     if (T == 0) {
-        ZOPT_TRY(launch_xent_total(row, 0, scal, loss, s));
+        ZOPT_TRY(launch_xent_total(row, 0, target, ignore_index, mean, loss, s));
         if (dw != nullptr) ZOPT_TRY(launch_fill_zero(dw, lddw, V, D, s));
         return ZOPT_OK;
     }
+    if (dx != nullptr || dw != nullptr)
+        ZOPT_TRY(launch_xent_count(target, T, ignore_index, mean, grad_scale, factor, s));
     ZOPT_TRY(place(p.x, ldx, ws, dw != nullptr ? target : nullptr, ignore_index, s));
     ZOPT_TRY(place(p.w, ldw, ws, nullptr, 0, s));
     uint16_t *e = dx != nullptr || dw != nullptr ? reinterpret_cast<uint16_t *>(ws + p.e) : nullptr;
@@ -197,56 +275,38 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
     for (int32_t k = 0; k < p.pieces; ++k) {
         const int64_t r0 = k * p.piece, n = T - r0 < p.piece ? T - r0 : p.piece;
         if (n <= 0) break;
-        TgLaunch L{};
-        L.nprob = 1;
-        L.M = (int32_t)n;
-        L.N = (int32_t)V;
-        L.prob[0].nseg = 1;
-        L.prob[0].seg[0] = segment(along(p.x, r0, n), along(p.w, 0, V));
+        Product logits = p.logits(r0, n);
+        TgLaunch &L = logits.L;
         L.e = e;
         L.lde = e != nullptr ? p.lde : 0;
         L.stats = stats;
         L.ldstat = n;
         L.target = target + r0;
         L.zt = zt;
-        ZOPT_TRY(launch_tg(kTgXent, false, false, L, s));
+        ZOPT_TRY(logits.run(false, false, nullptr, s));
         ZOPT_TRY(launch_xent_lse(stats, n, p.groups, target + r0, ignore_index, (int32_t)V, zt, n, lse, row + r0, s));
         if (e == nullptr) continue;
         ZOPT_TRY(launch_xent_probs(e, p.lde, n, (int32_t)V, stats, n, lse, row + r0, target + r0,
                                    ignore_index, s));
-        const Input P{e, p.lde, n, V, false, 0};
         if (dx != nullptr) {
-            TgLaunch G{};
-            G.nprob = 1;
-            G.M = (int32_t)n;
-            G.N = (int32_t)D;
-            G.prob[0].nseg = 1;
-            G.prob[0].seg[0] = segment(along(P, 0, n), across(p.w, 0, V));
-            G.prob[0].out = dx + r0 * lddx;
-            G.ldc = lddx;
-            G.vec = vec4(dx, lddx);
-            G.alpha = scal + kXentGrad;
-            ZOPT_TRY(launch_tg(kTgStore, false, true, G, s));
+            Product g = p.dx(ws, n);
+            g.L.prob[0].out = dx + r0 * lddx;
+            g.L.ldc = lddx;
+            g.L.vec = vec4(dx, lddx);
+            g.L.alpha = factor;
+            ZOPT_TRY(g.run(false, true, ws + p.part, s));
         }
         if (dw != nullptr) {
-            TgLaunch G{};
-            G.nprob = 1;
-            G.M = (int32_t)V;
-            G.N = (int32_t)D;
-            G.prob[0].nseg = 1;
-            G.prob[0].seg[0] = segment(across(P, 0, n), across(p.x, r0, n));
-            G.prob[0].out = dw;
-            G.prob[0].sum = reinterpret_cast<float *>(ws + p.sum);
-            G.ldc = lddw;
-            G.vec = vec4(dw, lddw);
-            G.alpha = scal + kXentGrad;
-            G.ldsum = p.ldsum;
-            G.sum_in = k > 0;
-            G.sum_out = r0 + n < T;
-            ZOPT_TRY(launch_tg(kTgStore, true, true, G, s));
+            Product g = p.dw(ws, r0, n);
+            g.L.prob[0].out = dw;
+            g.L.prob[0].sum = reinterpret_cast<float *>(ws + p.sum);
+            g.L.ldc = lddw;
+            g.L.vec = vec4(dw, lddw);
+            g.L.alpha = factor;
+            ZOPT_TRY(g.run(true, true, ws + p.part, s));
         }
     }
-    ZOPT_TRY(launch_xent_total(row, T, scal, loss, s));
+    ZOPT_TRY(launch_xent_total(row, T, target, ignore_index, mean, loss, s));
     return ZOPT_OK;
 }
 
@@ -275,13 +335,8 @@ ZOPT_EXPORT zopt_status zopt_glu_forward(int64_t T, int64_t D, int64_t F, const 
     ZOPT_TRY(place(p.x, ldx, ws, nullptr, 0, s));
     ZOPT_TRY(place(p.wg, ldw, ws, nullptr, 0, s));
     ZOPT_TRY(place(p.wu, ldw, ws, nullptr, 0, s));
-    TgLaunch L{};
-    L.nprob = 1;
-    L.M = (int32_t)T;
-    L.N = (int32_t)F;
-    L.prob[0].nseg = 1;
-    L.prob[0].seg[0] = segment(along(p.x, 0, T), along(p.wg, 0, F));
-    L.prob[0].seg[1] = segment(along(p.x, 0, T), along(p.wu, 0, F));
+    Product both = p.products(kTgGlu);
+    TgLaunch &L = both.L;
     L.act = act;
     L.h = h;
     L.ldc = ldh;
@@ -290,7 +345,7 @@ ZOPT_EXPORT zopt_status zopt_glu_forward(int64_t T, int64_t D, int64_t F, const 
     L.gs = g_scale;
     L.u8 = u8;
     L.us = u_scale;
-    return device(launch_tg(kTgGlu, false, false, L, s));
+    return device(both.run(false, false, nullptr, s));
 }
 
 ZOPT_EXPORT zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const uint16_t *dh, int64_t lddh,
@@ -338,13 +393,8 @@ ZOPT_EXPORT zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const
     if (kept) {
         ZOPT_TRY(launch_glu_back_act8(g8, g_scale, u8, u_scale, dh, lddh, T, F, act, dg, du, p.fp, h, ldh, s));
     } else {
-        TgLaunch L{};
-        L.nprob = 1;
-        L.M = (int32_t)T;
-        L.N = (int32_t)F;
-        L.prob[0].nseg = 1;
-        L.prob[0].seg[0] = segment(along(p.x, 0, T), along(p.wg, 0, F));
-        L.prob[0].seg[1] = segment(along(p.x, 0, T), along(p.wu, 0, F));
+        Product both = p.products(kTgGluBack);
+        TgLaunch &L = both.L;
         L.act = act;
         L.h = h;
         L.ldc = ldh;
@@ -355,34 +405,19 @@ ZOPT_EXPORT zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const
         L.dg = dg;
         L.du = du;
         L.lddg = p.fp;
-        ZOPT_TRY(launch_tg(kTgGluBack, false, false, L, s));
+        ZOPT_TRY(both.run(false, false, nullptr, s));
     }
-    const Input DG{dg, p.fp, T, F, false, 0}, DU{du, p.fp, T, F, false, 0};
-    {
-        TgLaunch G{};
-        G.nprob = 1;
-        G.M = (int32_t)T;
-        G.N = (int32_t)D;
-        G.prob[0].nseg = 2;
-        G.prob[0].seg[0] = segment(along(DG, 0, T), across(p.wg, 0, F));
-        G.prob[0].seg[1] = segment(along(DU, 0, T), across(p.wu, 0, F));
-        G.prob[0].out = dx;
-        G.ldc = lddx;
-        G.vec = vec4(dx, lddx);
-        ZOPT_TRY(launch_tg(kTgStore, false, true, G, s));
-    }
-    TgLaunch G{};
-    G.nprob = 2;
-    G.M = (int32_t)F;
-    G.N = (int32_t)D;
-    G.prob[0].nseg = G.prob[1].nseg = 1;
-    G.prob[0].seg[0] = segment(across(DG, 0, T), across(p.x, 0, T));
-    G.prob[1].seg[0] = segment(across(DU, 0, T), across(p.x, 0, T));
-    G.prob[0].out = dw_gate;
-    G.prob[1].out = dw_up;
-    G.ldc = lddw;
-    G.vec = vec4(dw_gate, lddw) && vec4(dw_up, lddw);
-    return device(launch_tg(kTgStore, true, true, G, s));
+    Product gx = p.dx(ws);
+    gx.L.prob[0].out = dx;
+    gx.L.ldc = lddx;
+    gx.L.vec = vec4(dx, lddx);
+    ZOPT_TRY(gx.run(false, true, ws + p.part, s));
+    Product gw = p.dw(ws);
+    gw.L.prob[0].out = dw_gate;
+    gw.L.prob[1].out = dw_up;
+    gw.L.ldc = lddw;
+    gw.L.vec = vec4(dw_gate, lddw) && vec4(dw_up, lddw);
+    return device(gw.run(true, true, ws + p.part, s));
 }
 
 ZOPT_EXPORT zopt_status zopt_act8_pack(int64_t rows, int64_t cols, const uint16_t *x, int64_t ldx, uint8_t *q,
@@ -410,6 +445,8 @@ ZOPT_EXPORT zopt_status zopt_act8_wgrad(int64_t T, int64_t N, int64_t D, const u
     Carve c;
     Input x = input(nullptr, D, T, D, true, c);
     Input y = input(dy, lddy, T, N, false, c);
+    Product g(kTgStore, N, D, segment(across(y, 0, T), across(x, 0, T)));
+    const size_t part = c.take(T > 0 ? g.parts() : 0);
     if (workspace == nullptr) {
         *workspace_bytes = c.total();
         return ZOPT_OK;
@@ -424,14 +461,9 @@ ZOPT_EXPORT zopt_status zopt_act8_wgrad(int64_t T, int64_t N, int64_t D, const u
     ZOPT_TRY(launch_act8_unpack(q, scale, T, D, dst, x.ld, x.ld, s));
     x.p = dst;
     ZOPT_TRY(place(y, lddy, ws, nullptr, 0, s));
-    TgLaunch G{};
-    G.nprob = 1;
-    G.M = (int32_t)N;
-    G.N = (int32_t)D;
-    G.prob[0].nseg = 1;
-    G.prob[0].seg[0] = segment(across(y, 0, T), across(x, 0, T));
-    G.prob[0].out = dw;
-    G.ldc = lddw;
-    G.vec = vec4(dw, lddw);
-    return device(launch_tg(kTgStore, true, true, G, s));
+    g.L.prob[0].seg[0] = segment(across(y, 0, T), across(x, 0, T));
+    g.L.prob[0].out = dw;
+    g.L.ldc = lddw;
+    g.L.vec = vec4(dw, lddw);
+    return device(g.run(true, true, ws + part, s));
 }

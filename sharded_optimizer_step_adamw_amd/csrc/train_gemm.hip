@@ -15,6 +15,8 @@
 // are put into LDS in an order that makes the columns of blocks 2 j' and
 // 2 j' + 1 together eight consecutive ones of a 32-column span (lane q:
 // columns 8 q .. 8 q + 7), so that epilogues work on and store 16 bytes.
+#include <utility>
+
 #include "train_internal.h"
 
 namespace zopt {
@@ -26,69 +28,102 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 32;  // reduction elements per stage
 
-// Tile t of a tiles_m x tiles_n grid.
+// f(0), f(1), ... with the index as a type
+template <int... M, class F>
+__device__ __forceinline__ void for_each(std::integer_sequence<int, M...>, F f) {
+    (f(std::integral_constant<int, M>{}), ...);
+}
+
+// The lane's index, computed afresh where it is used between tiles, so that
+// what is derived from it holds no registers across the main loop.
+__device__ __forceinline__ int lane_id() {
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    return l;
+}
+
+// Tile t of a tiles_m x tiles_n grid: bands of 16 tile rows, in a band groups
+// of 8 columns, in a group runs of 4 rows, column by column.  A round of 256
+// tiles is then about 16 x 16 and an XCD's 32 about 4 x 8: few operand panels
+// in each L2, and few of them read more than once from HBM.
 __device__ __forceinline__ void tile_at(int t, int tm, int tn, int &ti, int &tj) {
-    ti = t % tm;
-    tj = t / tm;
+    const int band = t / (16 * tn), r0 = band * 16;
+    t -= band * 16 * tn;
+    const int h = tm - r0 < 16 ? tm - r0 : 16;
+    const int group = t / (8 * h), c0 = group * 8;
+    t -= group * 8 * h;
+    const int w = tn - c0 < 8 ? tn - c0 : 8;
+    const int run = t / (4 * w), q0 = run * 4;
+    t -= run * 4 * w;
+    const int hh = h - q0 < 4 ? h - q0 : 4;
+    tj = c0 + t / hh;
+    ti = r0 + q0 + t % hh;
 }
 
 // Row statistics and exponentials of a logits tile.  A wave's 64 columns are
 // one statistics group: m = their largest logit, s = the sum of exp(z - m),
 // and e = exp(z - m) in (0, 1] kept in fp16 (11 bits; what is lost below
-// 2^-14 is under 2^-25 of the group's largest).
+// 2^-14 is under 2^-25 of the group's largest).  exp(z - m) is taken as
+// 2^(z log2 e - m log2 e) in one multiply-add, off by 2^-24 of |m| log2 e.
 template <int FM>
-__device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0,
-                                              int lane) {
-    const int c = lane & 15, q = lane >> 4;
-    if (C0 >= (int)L.lde && C0 >= L.N) return;
-    const int64_t group = C0 / kXentGroup;
+__device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0) {
+    const int lane = lane_id(), c = lane & 15, q = lane >> 4;
+    if (C0 >= L.N) return;  // (lde - N < 64: no column of e lies in a group past N's last)
+    float2 *stats = L.stats + (int64_t)(C0 / kXentGroup) * L.ldstat + R0 + c;
+    const int64_t *target = L.target + R0 + c;
+    uint16_t *e = L.e + (int64_t)(R0 + c) * L.lde + C0 + q * 8;
+    const int rows = L.M - R0 - c, cols = L.N - C0 - q * 8;
+    const bool whole = C0 + 64 <= L.N, keep = L.e != nullptr;
+    constexpr float kLog2e = 1.4426950408889634f;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int row = R0 + i * 16 + c;
         float z[16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int k = 0; k < 16; ++k) z[k] = acc[i][k >> 2][k & 3];
+        if (!whole) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int col = C0 + h * 32 + q * 8 + k;
-                z[h * 8 + k] = col < L.N ? acc[i][2 * h + (k >> 2)][k & 3] : -INFINITY;
-            }
+            for (int k = 0; k < 16; ++k) z[k] = (k >> 3) * 32 + (k & 7) < cols ? z[k] : -INFINITY;
+        }
         float m = z[0];
 #pragma unroll
         for (int k = 1; k < 16; ++k) m = fmaxf(m, z[k]);
         m = fmaxf(m, __shfl_xor(m, 16));
         m = fmaxf(m, __shfl_xor(m, 32));
-        if (row < L.M) {
-            const int64_t t = L.target[row];
-            const int64_t rel = t - C0 - q * 8;
+        const bool live = i * 16 < rows;
+        // the target's logit, where it is one of this lane's columns
+        int64_t rel = -1;
+        if (live) rel = *target - C0 - q * 8;
+        if (rel >= 0 && rel < 40 && (rel & 31) < 8) {
+            const int at = (int)((rel >> 5) * 8 + (rel & 7));
+            float v = z[0];
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (rel == (k >> 3) * 32 + (k & 7)) L.zt[row] = z[k];
+            for (int k = 1; k < 16; ++k) v = at == k ? z[k] : v;
+            L.zt[R0 + c + i * 16] = v;
         }
         // a group of -inf alone: exponentials 0, not NaN
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = m == -INFINITY ? 0.0f : m * kLog2e;
         float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            z[k] = __expf(z[k] - ref);
+            z[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[k], kLog2e, -ref));
             s += z[k];
         }
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
-        if (row < L.M) {
-            if (q == 0 && C0 < L.N) L.stats[group * L.ldstat + row] = make_float2(m, s);
-            if (L.e != nullptr) {
+        if (live) {
+            if (q == 0) *stats = make_float2(m, s);
+            if (keep) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int col = C0 + h * 32 + q * 8;
-                    if (col < L.lde)
-                        *reinterpret_cast<tg_u32x4 *>(L.e + (int64_t)row * L.lde + col) =
-                            tg_u32x4{tg_pack_f16(z[8 * h], z[8 * h + 1]), tg_pack_f16(z[8 * h + 2], z[8 * h + 3]),
-                                     tg_pack_f16(z[8 * h + 4], z[8 * h + 5]),
-                                     tg_pack_f16(z[8 * h + 6], z[8 * h + 7])};
-                }
+                for (int h = 0; h < 2; ++h)
+                    *reinterpret_cast<tg_u32x4 *>(e + h * 32) =
+                        tg_u32x4{tg_pack_f16(z[8 * h], z[8 * h + 1]), tg_pack_f16(z[8 * h + 2], z[8 * h + 3]),
+                                 tg_pack_f16(z[8 * h + 4], z[8 * h + 5]), tg_pack_f16(z[8 * h + 6], z[8 * h + 7])};
             }
         }
+        stats += 16;
+        target += 16;
+        e += 16 * L.lde;
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -128,8 +163,8 @@ __device__ __forceinline__ void act8_store(const float (&v)[8], int n, uint8_t *
 // Gate and up columns of a tile: blocks 0, 1 are the gate's 32 columns, 2, 3
 // the up projection's same columns; C0 is the first of them.
 template <int FM, bool BACK>
-__device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0, int lane) {
-    const int c = lane & 15, q = lane >> 4;
+__device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0) {
+    const int lane = lane_id(), c = lane & 15, q = lane >> 4;
     const int F = L.N;
     if (C0 >= F) return;
     const int col = C0 + q * 8;
@@ -174,201 +209,523 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
     }
 }
 
-// A tile of sums: alpha * acc to bf16, or fp32 sums kept for a later call.
+// four columns of a row, col .. col + 3, of which those below N exist
+__device__ __forceinline__ void store4(const TgLaunch &L, uint16_t *o, tg_f32x4 v, float alpha, int col) {
+    const tg_u32x2 p{tg_pack_bf16(v[0] * alpha, v[1] * alpha), tg_pack_bf16(v[2] * alpha, v[3] * alpha)};
+    if (L.vec && col + 4 <= L.N) {
+        *reinterpret_cast<tg_u32x2 *>(o) = p;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (col + k < L.N) o[k] = (uint16_t)((k < 2 ? p.x : p.y) >> (16 * (k & 1)));
+    }
+}
+
+// A tile of sums: alpha * acc to bf16, fp32 sums kept for a later call, or
+// this part of a split reduction in fp32.
 // PERM: the column order of a row-major B (eight consecutive per lane).
 template <int FM, int FN, bool PERM>
-__device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProblem &P, tg_f32x4 (&acc)[FM][FN],
-                                               int R0, int C0, int lane) {
-    const int c = lane & 15, q = lane >> 4;
+__device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProblem &P, int part,
+                                               tg_f32x4 (&acc)[FM][FN], int R0, int C0) {
+    const int lane = lane_id(), c = lane & 15, q = lane >> 4;
     const float alpha = L.alpha ? *L.alpha : 1.0f;
+    // the lane's first column, and the one of block j
+    const int first = C0 + (PERM ? q * 8 : q * 4);
+    auto at = [](int j) __attribute__((always_inline)) { return PERM ? (j >> 1) * 32 + (j & 1) * 4 : j * 16; };
+    const int rows = L.M - R0 - c, cols = L.N - first;  // what is left from the lane's first place on
+    const bool parts = L.splits > 1, in = L.sum_in != 0;
+    float *s = parts ? L.part + part * L.part_stride : P.sum;
+    s += (int64_t)(R0 + c) * L.ldsum + first;  // (rows of fp32 sums are padded to a multiple of 4)
+    const int64_t sstep = 16 * L.ldsum;
+    auto sum = [&](int i, int j) __attribute__((always_inline)) {
+        tg_f32x4 v = acc[i][j];
+        if (in) v += *reinterpret_cast<const tg_f32x4 *>(s + at(j));
+        return v;
+    };
+    uint16_t *o = P.out + (int64_t)(R0 + c) * L.ldc + first;
+    const int64_t step = 16 * L.ldc;
+    if (parts || L.sum_out) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-        const int row = R0 + i * 16 + c;
-        if (row >= L.M) continue;
+        for (int i = 0; i < FM; ++i) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int col = C0 + (PERM ? (j >> 1) * 32 + q * 8 + (j & 1) * 4 : j * 16 + q * 4);
-            if (col >= L.N) continue;
-            tg_f32x4 v = acc[i][j];
-            if (L.sum_in || L.sum_out) {
-                // (rows of fp32 sums are padded to a multiple of 4)
-                tg_f32x4 *s = reinterpret_cast<tg_f32x4 *>(P.sum + (int64_t)row * L.ldsum + col);
-                if (L.sum_in) v += *s;
-                if (L.sum_out) {
-                    *s = v;
-                    continue;
+            for (int j = 0; j < FN; ++j)
+                if (i * 16 < rows && at(j) < cols) *reinterpret_cast<tg_f32x4 *>(s + at(j)) = sum(i, j);
+            s += sstep;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else if (L.vec && (L.N & 3) == 0) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                if (i * 16 < rows && at(j) < cols) {
+                    const tg_f32x4 v = sum(i, j) * alpha;
+                    *reinterpret_cast<tg_u32x2 *>(o + at(j)) =
+                        tg_u32x2{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3])};
                 }
             }
-            uint16_t *o = P.out + (int64_t)row * L.ldc + col;
-            const tg_u32x2 p{tg_pack_bf16(v[0] * alpha, v[1] * alpha), tg_pack_bf16(v[2] * alpha, v[3] * alpha)};
-            if (L.vec && col + 4 <= L.N) {
-                *reinterpret_cast<tg_u32x2 *>(o) = p;
-            } else {
+            o += step;
+            s += sstep;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (col + k < L.N) o[k] = (uint16_t)((k < 2 ? p.x : p.y) >> (16 * (k & 1)));
-            }
+        for (int i = 0; i < FM; ++i) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                if (i * 16 < rows && at(j) < cols) {
+                    const tg_f32x4 v = sum(i, j) * alpha;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (at(j) + k < cols) o[at(j) + k] = (uint16_t)tg_pack_bf16(v[k], 0.0f);
+                }
+            o += step;
+            s += sstep;
+            __builtin_amdgcn_sched_barrier(0);
         }
     }
 }
 
-// One BM x BM output tile per workgroup of WR x 2 waves, each BM / WR x 64
-// columns from 16 x 16 x 32 MFMAs with fp32 accumulators.  Stages of 32
-// reduction elements go from global memory straight to LDS, 16 bytes a lane;
-// a lane outside the operand reads past the buffer descriptor's end, which
-// gives zeros.  LDS layouts (as in the Newton-Schulz kernels): row-major rows
-// of 64 bytes, 16-byte chunk c of row r at slot c ^ ((r >> 1) & 3); k-major
-// rows of 2 BM bytes, 32-byte unit u of row r at unit u ^ qsw(r).
+// Tiles.  A BM x BM tile per workgroup, its waves BM / WR x 64 each, from
+// 16 x 16 x 32 MFMAs with fp32 accumulators.  WPE: waves per SIMD.
+template <int BM>
+struct Cfg;
+template <>
+struct Cfg<256> { static constexpr int WR = 2, WC = 4, WPE = 2; };
+template <>
+struct Cfg<128> { static constexpr int WR = 2, WC = 2, WPE = 2; };
+template <>
+struct Cfg<64> { static constexpr int WR = 4, WC = 1, WPE = 4; };
+
+constexpr int kStages = 4;
+// s_waitcnt: vmcnt <= n and lgkmcnt = 0 (gfx9 field layout: vmcnt[3:0],
+// expcnt[6:4], lgkmcnt[11:8], vmcnt high bits[15:14])
+#define WAIT_VM_LGKM0(n) ((((n) & 15) | (((n) >> 4) << 14) | (7 << 4)))
+
+// The main loop.  The reduction advances in stages of 32 through four LDS
+// buffers that buffer_load ... lds fills three stages ahead (16 bytes a lane;
+// a lane outside the operand reads past its descriptor's end, which gives
+// zeros).  A stage's body: barrier (everyone's loads of the next stage have
+// landed and everyone has read this one's fragments) -> loads of the stage
+// four ahead into the buffer just freed -> the next stage's fragments, read
+// between this stage's MFMAs -> wait for those reads and for this wave's
+// loads of the stage after.
+//
+// The kernel is persistent: one round of resident workgroups walks all tiles,
+// and from a tile's last four stages on the loads are those of the
+// workgroup's next tile, so that its operands arrive while this one is
+// finished and stored.  A tile's stages are padded with zero stages to an
+// even number, four at least.
+//
+// LDS layouts: row-major rows of 64 bytes, 16-byte chunk c of row r at slot
+// c ^ ((r >> 1) & 3); k-major rows of 2 BM bytes, 32-byte unit u of row r at
+// unit u ^ qsw(r), read with ds_read_b64_tr_b16: lane 4 q + p of a 16-lane
+// group addresses row +q, columns 4 p .. 4 p + 3 of a 4 x 16 block, and lane
+// i receives rows +0 .. +3 of column i.  Both spread each read over all
+// banks.  The transposing reads are inline assembly: as ordinary loads the
+// compiler could not tell them from the copies in flight into other buffers
+// and would wait for those.  Each is waited for within the stage's body.
 template <int BM, int EPI, bool AKM, bool BKM>
-__global__ __launch_bounds__(256) void tg_kernel(TgLaunch L) {
-    constexpr int NW = 4, WC = 2, WR = 2, WTM = BM / WR, WTN = BM / WC, FM = WTM / 16, FN = WTN / 16;
-    static_assert(WTN == 64, "a wave holds 64 columns");
-    constexpr int ROW = 64, OPB = BM * ROW, LOADS = OPB / 1024 / NW;
+__global__ __launch_bounds__(Cfg<BM>::WR *Cfg<BM>::WC * 64)
+__attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
+    constexpr int WR = Cfg<BM>::WR, WC = Cfg<BM>::WC, NW = WR * WC;
+    constexpr int WTM = BM / WR, FM = WTM / 16, FN = 4;
+    static_assert(BM / WC == 64, "a wave holds 64 columns");
+    constexpr int ROW = 64, OPB = BM * ROW, STAGE = 2 * OPB, LOADS = OPB / 1024 / NW, LPS = 2 * LOADS;
+    static_assert(LOADS >= 1 && LOADS * NW * 1024 == OPB, "whole kilobytes");
     constexpr int QRB = 2 * BM, QCH = QRB / 16;
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * OPB];
+    static_assert(!GLU || NW % 4 == 0, "a wave loads rows of the gate or of the up projection");
+    constexpr int BN = GLU ? BM / 2 : BM;  // output columns of a tile
+    constexpr int kOut = 0x7FFFFFF0;       // a byte offset past every descriptor
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * STAGE];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / WC, wc = wave % WC;
-    const uint32_t lds_base = (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds);
-
-    const int per = L.tiles_m * L.tiles_n;
-    const int pi = blockIdx.x / per;
-    const TgProblem &P = L.prob[pi];
-    int ti, tj;
-    tile_at(blockIdx.x - pi * per, L.tiles_m, L.tiles_n, ti, tj);
-    // gate / up tiles hold BM / 2 columns of each
-    const int m0 = ti * BM, n0 = tj * (GLU ? BM / 2 : BM);
+    const int grid = gridDim.x;
+    const uint32_t lds_base =
+        (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds);
 
     auto qsw = [](int r) __attribute__((always_inline)) {
         return BM >= 128 ? (r & 3) | (((r >> 3) & 1) << 2) : ((r >> 1) & 1) | (((r >> 3) & 1) << 1);
     };
 
-    tg_f32x4 acc[FM][FN];
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = tg_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    // kilobyte kb of an operand's stage: 16 rows (row-major), or 1024 / QRB
-    // k rows; the lane's byte offset from the stage's corner
-    auto load_rows = [&](const TgOperand &o, const uint16_t *base, int left, int k0, int kb, int row, int dst)
-                         __attribute__((always_inline)) {
-        // left: rows of the operand from the tile's first one on
-        const int lrow = lane >> 2, chunk = (lane & 3) ^ ((lrow >> 1) & 3);
-        const int kleft = o.k - k0;
-        const int rows = left < BM ? left : BM;
-        const int bytes = kleft > 0 && rows > 0 ? ((rows - 1) * (int)o.ld + kleft) * 2 : 0;
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc((void *)(base + k0), (short)0, bytes, 0x00020000);
-        int off = chunk * 8 < kleft ? (row * (int)o.ld + chunk * 8) * 2 : 0x7FFFFFF0;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, LDS_ADDR(&lds[dst + kb * 1024]), 16, off, 0, 0, 0);
+    struct Tile {
+        int prob, split, m0, n0, stage0, live, stages;  // live: real stages; stages: padded
     };
-    auto load_cols = [&](const TgOperand &o, int c0, int k0, int kb, int dst) __attribute__((always_inline)) {
-        const int r = kb * (1024 / QRB) + lane / QCH, s16 = lane % QCH;
-        const int kleft = o.k - k0, rows = kleft < kBK ? kleft : kBK;
-        const int bytes = rows > 0 ? ((rows - 1) * (int)o.ld + (o.outer - c0)) * 2 : 0;
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            (void *)(o.p + (int64_t)k0 * o.ld + c0), (short)0, bytes, 0x00020000);
-        const int col = (((s16 >> 1) ^ qsw(r)) << 4) + ((s16 & 1) << 3);
-        int off = col < o.outer - c0 ? (r * (int)o.ld + col) * 2 : 0x7FFFFFF0;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, LDS_ADDR(&lds[dst + kb * 1024]), 16, off, 0, 0, 0);
+    // slot -> tile (false: a padding slot).  Workgroups go to the 8 XCDs in
+    // turn; XCD x takes the x-th contiguous eighth of each round of resident
+    // tiles, and consecutive tiles form blocks of the grid, so that each L2
+    // serves few operand panels.
+    auto locate = [&](int slot, Tile &T) __attribute__((always_inline)) -> bool {
+        const int base = slot - slot % grid;
+        const int rem = L.padded - base < grid ? L.padded - base : grid;
+        int t = base + (slot & 7) * (rem >> 3) + ((slot - base) >> 3);
+        if (t >= L.total) return false;
+        const int per = L.tiles_m * L.tiles_n;
+        const int item = t / per;
+        T.prob = item / L.splits;
+        T.split = item - T.prob * L.splits;
+        int ti, tj;
+        tile_at(t - item * per, L.tiles_m, L.tiles_n, ti, tj);
+        T.m0 = ti * BM;
+        T.n0 = tj * BN;
+        const TgProblem &P = L.prob[T.prob];
+        const int all = P.seg[0].stages + (!GLU && P.nseg > 1 ? P.seg[1].stages : 0);
+        T.stage0 = T.split * L.split_stages;
+        T.live = all - T.stage0 < L.split_stages ? all - T.stage0 : L.split_stages;
+        T.stages = T.live <= 4 ? 4 : (T.live + 1) & ~1;
+        return true;
+    };
+    auto seek = [&](int slot, Tile &T) __attribute__((always_inline)) -> int {
+        for (; slot < L.padded; slot += grid)
+            if (locate(slot, T)) return slot;
+        return -1;
     };
 
-    for (int s = 0; s < P.nseg; ++s) {
-        const TgSegment &S = P.seg[s];
-        for (int st = 0; st < S.stages; ++st) {
-            const int k0 = st * kBK;
-            __syncthreads();
-#pragma unroll
-            for (int x = 0; x < LOADS; ++x) {
-                const int kb = x * NW + wave;
-                if constexpr (AKM) {
-                    load_cols(S.a, m0, k0, kb, 0);
-                } else {
-                    load_rows(S.a, S.a.p + (int64_t)m0 * S.a.ld, S.a.outer - m0, k0, kb, kb * 16 + (lane >> 2), 0);
-                }
-                if constexpr (BKM) {
-                    load_cols(S.b, n0, k0, kb, OPB);
-                } else {
-                    // LDS row n of block kb holds the tile's column
-                    // 32 (kb / 2) + 8 (n / 4) + 4 (kb % 2) + n % 4; gate / up:
-                    // block kb % 4 of wave kb / 4, gate in blocks 0, 1
-                    const int n = lane >> 2;
-                    const int sub = 8 * (n >> 2) + 4 * (kb & 1) + (n & 3);
-                    const TgOperand &o = GLU && (kb & 2) ? P.seg[1].b : S.b;
-                    const int row = (GLU ? (kb >> 2) * 32 : (kb >> 1) * 32) + sub;
-                    load_rows(o, o.p + (int64_t)n0 * o.ld, o.outer - n0, k0, kb, row, OPB);
-                }
-            }
-            __builtin_amdgcn_s_waitcnt(0);
-            __syncthreads();
-            bf16x8 fa[FM], fb[FN];
-            const int fr = lane & 15, fh = lane >> 4;
-            const int foff = fr * ROW + ((fh ^ ((fr >> 1) & 3)) << 4);
-            const int tg = lane >> 4, tq = (lane >> 2) & 3, tp = lane & 3;
-            const int tpo = ((tp >> 1) << 4) + ((tp & 1) << 3), tr = 8 * tg + tq;
-            auto tread = [&](int unit, int op) __attribute__((always_inline)) {
-                tg_u32x2 lo, hi;
-                const uint32_t a = lds_base + op + tr * QRB + ((unit ^ qsw(tr)) << 5) + tpo;
-                asm volatile("ds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%3\n\ts_waitcnt lgkmcnt(0)"
-                             : "=&v"(lo), "=&v"(hi)
-                             : "v"(a), "i"(4 * QRB)
-                             : "memory");
-                return __builtin_bit_cast(bf16x8, tg_u32x4{lo.x, lo.y, hi.x, hi.y});
-            };
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                if constexpr (AKM)
-                    fa[i] = tread(wr * (WTM / 16) + i, 0);
-                else
-                    fa[i] = *reinterpret_cast<const bf16x8 *>(&lds[wr * WTM * ROW + i * 16 * ROW + foff]);
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (BKM)
-                    fb[j] = tread(wc * (WTN / 16) + j, OPB);
-                else
-                    fb[j] = *reinterpret_cast<const bf16x8 *>(&lds[OPB + wc * WTN * ROW + j * 16 * ROW + foff]);
-            }
-#pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    // ------------------------------------------------ the load stream
+    // Of each operand: the tile's corner at the stream's current reduction
+    // index, what is left of the reduction, the byte extent of the panel's
+    // rows before the last (row-major) or of one row (k-major), and each
+    // lane's byte offset per kilobyte.
+    const uint16_t *pa = nullptr, *pb = nullptr;
+    int ka = 0, kb = 0, lda = 0, ldb = 0, ea = 0, eb = 0, seg_left = 0, total_left = 0;
+    int sprob = 0, sm0 = 0, sn0 = 0;
+    int va[LOADS], vb[LOADS];
+    const int chunk8 = ((lane & 3) ^ ((lane >> 3) & 3)) << 3;  // row-major: the lane's k offset
+    auto corner = [&](const TgOperand &o, bool km, int c0, int extent, int k0, const uint16_t *&p, int &k, int &ld,
+                      int &e) __attribute__((always_inline)) {
+        ld = (int)o.ld;
+        k = o.k - k0;
+        if (km) {
+            p = o.p + (int64_t)k0 * o.ld + c0;
+            e = (o.outer - c0) * 2;
+        } else {
+            p = o.p + (int64_t)c0 * o.ld + k0;
+            const int left = o.outer - c0;
+            e = ((left < extent ? left : extent) - 1) * ld * 2;
         }
-        if (GLU) break;  // (the second segment holds the up projection's rows)
+    };
+    auto open_segment = [&](int s, int k0) __attribute__((always_inline)) {
+        const TgProblem &P = L.prob[sprob];
+        const TgSegment &S = P.seg[s];
+        seg_left = S.stages - k0 / kBK;
+        corner(S.a, AKM, sm0, BM, k0, pa, ka, lda, ea);
+        // gate / up: LDS blocks 0, 1 of each four hold the gate's rows (wave
+        // w fills blocks w, w + NW, ...)
+        corner(GLU && (wave & 2) ? P.seg[1].b : S.b, BKM, sn0, BN, k0, pb, kb, ldb, eb);
+    };
+    auto stream = [&](const Tile &T, bool live) __attribute__((always_inline)) {
+        total_left = live ? T.live : 0;
+        sprob = T.prob;
+        sm0 = T.m0;
+        sn0 = T.n0;
+        const int s0 = L.prob[T.prob].seg[0].stages;
+        if (!GLU && T.stage0 >= s0)
+            open_segment(1, (T.stage0 - s0) * kBK);
+        else
+            open_segment(0, T.stage0 * kBK);
+#pragma unroll
+        for (int x = 0; x < LOADS; ++x) {
+            const int kilo = x * NW + wave;
+            if constexpr (AKM) {
+                const int r = kilo * (1024 / QRB) + lane / QCH, s16 = lane % QCH;
+                const int col = (((s16 >> 1) ^ qsw(r)) << 4) + ((s16 & 1) << 3);
+                va[x] = col * 2 < ea ? (r * lda + col) * 2 : kOut;
+            } else {
+                va[x] = ((kilo * 16 + (lane >> 2)) * lda + chunk8) * 2;
+            }
+            if constexpr (BKM) {
+                const int r = kilo * (1024 / QRB) + lane / QCH, s16 = lane % QCH;
+                const int col = (((s16 >> 1) ^ qsw(r)) << 4) + ((s16 & 1) << 3);
+                vb[x] = col * 2 < eb ? (r * ldb + col) * 2 : kOut;
+            } else {
+                // LDS row n of block `kilo` holds the tile's column 32 (kilo / 2)
+                // + 8 (n / 4) + 4 (kilo % 2) + n % 4; gate / up: of the 32
+                // columns of wave kilo / 4
+                const int n = lane >> 2, sub = 8 * (n >> 2) + 4 * (kilo & 1) + (n & 3);
+                const int row = (GLU ? (kilo >> 2) * 32 : (kilo >> 1) * 32) + sub;
+                vb[x] = (row * ldb + chunk8) * 2;
+            }
+        }
+    };
+    auto extent = [&](bool km, int k, int ld, int e) __attribute__((always_inline)) -> int {
+        if (total_left <= 0 || k <= 0) return 0;
+        if (km) return ((k < kBK ? k : kBK) - 1) * ld * 2 + e;
+        return e + k * 2;
+    };
+    // load y of a stage: the operands' kilobytes in turn
+    __amdgpu_buffer_rsrc_t ra, rb;
+    auto open_stage = [&]() __attribute__((always_inline)) {
+        ra = __builtin_amdgcn_make_buffer_rsrc((void *)pa, (short)0, extent(AKM, ka, lda, ea), 0x00020000);
+        rb = __builtin_amdgcn_make_buffer_rsrc((void *)pb, (short)0, extent(BKM, kb, ldb, eb), 0x00020000);
+    };
+    auto gload = [&](int sbase, int y) __attribute__((always_inline)) {
+        const int kilo = (y >> 1) * NW + wave;
+        // (a chunk past the row's end would be the next row's)
+        if (y & 1) {
+            const int o = BKM || chunk8 < kb ? vb[y >> 1] : kOut;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_ADDR(&lds[sbase + OPB + kilo * 1024]), 16, o, 0, 0, 0);
+        } else {
+            const int o = AKM || chunk8 < ka ? va[y >> 1] : kOut;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_ADDR(&lds[sbase + kilo * 1024]), 16, o, 0, 0, 0);
+        }
+    };
+    auto close_stage = [&]() __attribute__((always_inline)) {
+        pa += AKM ? (int64_t)kBK * lda : kBK;
+        pb += BKM ? (int64_t)kBK * ldb : kBK;
+        ka -= kBK;
+        kb -= kBK;
+        --total_left;
+        // (real stages left after a segment's last: there is a second one)
+        if (!GLU && --seg_left == 0 && total_left > 0) open_segment(1, 0);
+    };
+
+    // -------------------------------------------------- fragments and products
+    const int fr = lane & 15, fh = lane >> 4;
+    const int foff = fr * ROW + ((fh ^ ((fr >> 1) & 3)) << 4);
+    const int tr = 8 * fh + ((lane >> 2) & 3), tp = lane & 3;
+    const uint32_t toff = lds_base + tr * QRB + ((tp >> 1) << 4) + ((tp & 1) << 3) + (qsw(tr) << 5);
+    bf16x8 fa[2][FM], fb[2][FN];
+    // block `blk` of an operand: unit (first + blk) ^ qsw(row), i.e. the
+    // address of block 0 with blk's bits flipped
+    auto tread = [&](uint32_t at, auto BLK) __attribute__((always_inline)) {
+        tg_u32x2 lo, hi;
+        uint32_t t;
+        asm volatile(
+            "v_xor_b32 %2, %3, %4\n\tds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%5"
+            : "=&v"(lo), "=&v"(hi), "=&v"(t)
+            : "i"(decltype(BLK)::value << 5), "v"(at), "i"(4 * QRB));
+        return __builtin_bit_cast(bf16x8, tg_u32x4{lo.x, lo.y, hi.x, hi.y});
+    };
+    // fragment y of a stage: A's blocks, then B's
+    auto read = [&](int buf, int sbase, auto Y) __attribute__((always_inline)) {
+        constexpr int y = decltype(Y)::value;
+        if constexpr (y < FM) {
+            if constexpr (AKM)
+                fa[buf][y] = tread((toff + sbase) ^ ((wr * FM) << 5), Y);
+            else
+                fa[buf][y] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + (wr * WTM + y * 16) * ROW + foff]);
+        } else {
+            constexpr int j = y - FM;
+            if constexpr (BKM)
+                fb[buf][j] = tread((toff + sbase + OPB) ^ ((wc * FN) << 5), std::integral_constant<int, j>{});
+            else
+                fb[buf][j] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + OPB + (wc * 64 + j * 16) * ROW + foff]);
+        }
+    };
+    // (after a wait: nothing that uses the fragments moves above it)
+    auto tie = [&](int buf) __attribute__((always_inline)) {
+        if constexpr (AKM)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(fa[buf][i]));
+        if constexpr (BKM)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(fb[buf][j]));
+    };
+    tg_f32x4 acc[FM][FN];
+    // steps of a stage's body: product m, then one load or fragment read
+    auto steps = [&](auto PAR, int cbase, int nbase) __attribute__((always_inline)) {
+        constexpr int par = decltype(PAR)::value;
+        constexpr int kSteps = FM * FN > LPS + FM + FN ? FM * FN : LPS + FM + FN;
+        for_each(std::make_integer_sequence<int, kSteps>{}, [&](auto MM) __attribute__((always_inline)) {
+            constexpr int m = decltype(MM)::value;
+            if constexpr (m < FM * FN) {
+                constexpr int i = m / FN, j = m % FN;
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[par][j], fa[par][i], acc[i][j], 0, 0, 0);
+            }
+            if constexpr (m < LPS)
+                gload(cbase, m);
+            else if constexpr (m - LPS < FM + FN)
+                read(par ^ 1, nbase, std::integral_constant<int, m - LPS>{});
+            __builtin_amdgcn_sched_barrier(0);
+        });
+    };
+    int cur = 0;
+    auto body = [&](auto PAR) __attribute__((always_inline)) {
+        constexpr int par = decltype(PAR)::value;
+        const int nxt = (cur + 1) & (kStages - 1);
+        __builtin_amdgcn_s_barrier();
+        open_stage();
+        __builtin_amdgcn_sched_barrier(0);
+        steps(PAR, cur * STAGE, nxt * STAGE);
+        close_stage();
+        __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0((kStages - 2) * LPS));
+        __builtin_amdgcn_sched_barrier(0);
+        tie(par ^ 1);
+        cur = nxt;
+    };
+
+    Tile cu, nx{};
+    int slot = seek(blockIdx.x, cu);
+    if (slot < 0) return;
+    stream(cu, true);
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+        open_stage();
+#pragma unroll
+        for (int y = 0; y < LPS; ++y) gload(s * STAGE, y);
+        close_stage();
     }
-    const int R0 = m0 + wr * WTM;
-    if constexpr (EPI == kTgXent)
-        xent_epilogue<FM>(L, acc, R0, n0 + wc * WTN, lane);
-    else if constexpr (GLU)
-        glu_epilogue<FM, EPI == kTgGluBack>(L, acc, R0, n0 + wc * 32, lane);
-    else
-        store_epilogue<FM, FN, !BKM>(L, P, acc, R0, n0 + wc * WTN, lane);
+    __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0((kStages - 1) * LPS));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    for_each(std::make_integer_sequence<int, FM + FN>{},
+             [&](auto Y) __attribute__((always_inline)) { read(0, 0, Y); });
+    __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0((kStages - 2) * LPS));
+    __builtin_amdgcn_sched_barrier(0);
+    tie(0);
+    for (;;) {
+        const int nslot = seek(slot + grid, nx);
+        const bool more = nslot >= 0;
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = tg_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        int kt = 0;
+#pragma clang loop unroll(disable)
+        for (; kt < cu.stages - kStages; kt += 2) {
+            body(std::integral_constant<int, 0>{});
+            body(std::integral_constant<int, 1>{});
+        }
+        // the last four stages load the next tile's first ones (or zeros)
+        stream(more ? nx : cu, more);
+        for (; kt < cu.stages; kt += 2) {
+            body(std::integral_constant<int, 0>{});
+            body(std::integral_constant<int, 1>{});
+        }
+        const TgProblem &P = L.prob[cu.prob];
+        const int R0 = cu.m0 + wr * WTM;
+        if constexpr (EPI == kTgXent)
+            xent_epilogue<FM>(L, acc, R0, cu.n0 + wc * 64);
+        else if constexpr (GLU)
+            glu_epilogue<FM, EPI == kTgGluBack>(L, acc, R0, cu.n0 + wc * 32);
+        else
+            store_epilogue<FM, FN, !BKM>(L, P, cu.prob * L.splits + cu.split, acc, R0, cu.n0 + wc * 64);
+        if (!more) break;
+        cu = nx;
+        slot = nslot;
+    }
+    // the loads past the last tile write zeros to LDS: they end before it does
+    __builtin_amdgcn_s_waitcnt(0);
+}
+
+// out = bf16(alpha * sum over splits of part), four columns a thread, in
+// split order
+__global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
+    const int64_t per = (L.N + 3) / 4, one = per * L.M, total = one * L.nprob;
+    const float alpha = L.alpha ? *L.alpha : 1.0f;
+    for (int64_t id = blockIdx.x * (int64_t)256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
+        const int pi = id >= one ? 1 : 0;
+        const int64_t k = id - pi * one, row = k / per, col = (k - row * per) * 4;
+        const float *p = L.part + (int64_t)pi * L.splits * L.part_stride + row * L.ldsum + col;
+        tg_f32x4 v = *reinterpret_cast<const tg_f32x4 *>(p);
+        for (int s = 1; s < L.splits; ++s) v += *reinterpret_cast<const tg_f32x4 *>(p + s * L.part_stride);
+        store4(L, L.prob[pi].out + row * L.ldc + col, v, alpha, (int)col);
+    }
+}
+
+int compute_units() {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 8)
+        cus = 256;
+    return cus / 8 * 8;
 }
 
 template <int BM, int EPI, bool AKM, bool BKM>
 hipError_t run(TgLaunch &L, hipStream_t stream) {
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
-    constexpr int BN = GLU ? BM / 2 : BM;
+    constexpr int BN = GLU ? BM / 2 : BM, threads = Cfg<BM>::WR * Cfg<BM>::WC * 64;
     L.tiles_m = (L.M + BM - 1) / BM;
     L.tiles_n = (L.N + BN - 1) / BN;
-    const int64_t grid = (int64_t)L.tiles_m * L.tiles_n * L.nprob;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((tg_kernel<BM, EPI, AKM, BKM>), dim3((uint32_t)grid), dim3(256), 0, stream, L);
-    return hipGetLastError();
+    const int64_t total = (int64_t)L.tiles_m * L.tiles_n * L.nprob * L.splits;
+    if (total > 0x7FFFFF00) return hipErrorInvalidValue;
+    L.total = (int32_t)total;
+    L.padded = (L.total + 7) / 8 * 8;
+    const int64_t round = (int64_t)compute_units() * (Cfg<BM>::WPE * 4 / (threads / 64));
+    const uint32_t grid = (uint32_t)(L.padded < round ? L.padded : round);
+    hipLaunchKernelGGL((tg_kernel<BM, EPI, AKM, BKM>), dim3(grid), dim3(threads), 0, stream, L);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && EPI == kTgStore && L.splits > 1) {
+        const int64_t work = (int64_t)L.M * ((L.N + 3) / 4) * L.nprob;
+        const int64_t blocks = (work + 255) / 256;
+        hipLaunchKernelGGL(tg_join_kernel, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, L);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <int EPI, bool AKM, bool BKM>
+hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
+    if (L.tile == 256) return run<256, EPI, AKM, BKM>(L, stream);
+    if (L.tile == 128) return run<128, EPI, AKM, BKM>(L, stream);
+    return run<64, EPI, AKM, BKM>(L, stream);
 }
 
 }  // namespace
 
+// Tile and split, by an estimate of the launch's time in microseconds from
+// figures measured on the card (256 CUs):
+//   stage   one workgroup alone on its CU takes 0.66 / 0.27 / 0.17 a stage of
+//           32 on tiles of 256 / 128 / 64, bound by latency; a CU with all it
+//           holds (1 / 2 / 4 of them) 0.86 / 0.47 / 0.52 for all together
+//   tile    its first loads and its epilogue: about 4 / 2 / 1.5 plain, 10 / 7 /
+//           6 with exponentials
+//   split   a second launch (4) and 8 bytes an output and part at 5 TB/s
+// So a reduction is split where its tiles leave CUs idle: [256, 50304] x
+// [50304, 768] takes 1.05 ms whole on 256 tiles, 0.18 ms in 16 parts on 128
+// ones.  Checked against a sweep of 18 shapes x 3 tiles x 10 splits: within a
+// few microseconds of the best, 5% at most.
+void plan_tg(TgEpilogue epi, TgLaunch &L) {
+    struct Figures {
+        int tile, held;
+        double alone, full, plain, heavy;
+    };
+    static constexpr Figures figures[3] = {
+        {256, 1, 0.66, 0.86, 4.0, 10.0}, {128, 2, 0.27, 0.235, 2.0, 7.0}, {64, 4, 0.17, 0.13, 1.5, 6.0}};
+    constexpr int64_t cus = 256;
+    const bool glu = epi == kTgGlu || epi == kTgGluBack;
+    int all = L.prob[0].seg[0].stages;
+    if (epi == kTgStore && L.prob[0].nseg > 1) all += L.prob[0].seg[1].stages;
+    double best = 0;
+    for (const Figures &f : figures) {
+        const int64_t bn = glu ? f.tile / 2 : f.tile;
+        const int64_t tiles = (L.M + f.tile - 1) / f.tile * ((L.N + bn - 1) / bn) * L.nprob;
+        const bool may = epi == kTgStore && !L.sum_in && !L.sum_out && tiles < 4 * cus;
+        for (int split = 1; split <= (may ? 32 : 1); ++split) {
+            const int per = (all + split - 1) / split;
+            if (split > 1 && per < 8) break;
+            const int parts = (all + per - 1) / per;
+            if (parts != split) continue;
+            const int64_t on = (tiles * parts + cus - 1) / cus, rounds = on / f.held, rest = on % f.held;
+            auto load = [&](double n) { return f.alone > n * f.full ? f.alone : n * f.full; };
+            double t = per * (rounds * load(f.held) + (rest ? load((double)rest) : 0.0)) +
+                       (double)(rounds + (rest ? 1 : 0)) * (epi == kTgStore ? f.plain : f.heavy);
+            if (parts > 1) t += 4.0 + 8.0 * parts * (double)L.M * L.N * L.nprob / 5.0e6;
+            if (best == 0 || t < best) {
+                best = t;
+                L.tile = f.tile;
+                L.splits = parts;
+                L.split_stages = per;
+            }
+        }
+    }
+    L.ldsum = (L.N + 3) / 4 * 4;
+    L.part_stride = (int64_t)L.M * L.ldsum;
+}
+
+size_t tg_part_bytes(const TgLaunch &L) {
+    return L.splits > 1 ? (size_t)L.splits * L.nprob * L.part_stride * 4 : 0;
+}
+
 hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStream_t stream) {
-    if (epi == kTgXent) return run<128, kTgXent, false, false>(L, stream);
-    if (epi == kTgGlu) return run<128, kTgGlu, false, false>(L, stream);
-    if (epi == kTgGluBack) return run<128, kTgGluBack, false, false>(L, stream);
+    if (epi == kTgXent) return run_tile<kTgXent, false, false>(L, stream);
+    if (epi == kTgGlu) return run_tile<kTgGlu, false, false>(L, stream);
+    if (epi == kTgGluBack) return run_tile<kTgGluBack, false, false>(L, stream);
     if (!b_km) return hipErrorInvalidValue;
-    return a_km ? run<128, kTgStore, true, true>(L, stream) : run<128, kTgStore, false, true>(L, stream);
+    return a_km ? run_tile<kTgStore, true, true>(L, stream) : run_tile<kTgStore, false, true>(L, stream);
 }
 
 }  // namespace zopt

@@ -47,7 +47,11 @@ struct TgLaunch {
     TgProblem prob[2];
     int32_t nprob;
     int32_t M, N;             // output sizes (Glu: N = feed-forward width)
-    int32_t tiles_m, tiles_n; // grid of output tiles
+    int32_t tile, tiles_m, tiles_n;  // tile side, grid of output tiles
+    int32_t splits, split_stages;    // kTgStore: the reduction in parts of split_stages stages
+    int32_t total, padded;           // tiles of all problems and parts; rounded up to 8
+    float *part;              // splits > 1: fp32 parts, part_stride each
+    int64_t part_stride;
     int64_t ldc;
     int32_t vec;              // outputs take vector stores
     // kTgStore
@@ -77,6 +81,11 @@ struct TgLaunch {
 
 constexpr int kXentGroup = 64;  // columns per statistics group
 
+// Chooses tile and split (sets tile, splits, split_stages, ldsum, part_stride)
+// from the sizes, problems and segments; the parts' fp32 scratch.
+void plan_tg(TgEpilogue epi, TgLaunch &L);
+size_t tg_part_bytes(const TgLaunch &L);
+
 // a_km / b_km: operand is k-major.  kTgXent and the Glu kinds: both row-major.
 hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStream_t stream);
 
@@ -96,11 +105,9 @@ hipError_t launch_act8_pack(const uint16_t *x, int64_t ld, int64_t rows, int64_t
 hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
                               uint16_t *x, int64_t ld, int64_t cols_out, hipStream_t stream);
 
-// Scalars of a linear cross entropy call in device memory.
-enum : int { kXentShare = 0, kXentGrad = 1, kXentScalars = 2 };
-// scal[kXentShare] = 1 or 1 / valid rows (0 if none); scal[kXentGrad] = that * grad_scale
+// *factor = grad_scale, or grad_scale / rows that take part (0 if none)
 hipError_t launch_xent_count(const int64_t *target, int64_t rows, int64_t ignore, int32_t mean,
-                             float grad_scale, float *scal, hipStream_t stream);
+                             float grad_scale, float *factor, hipStream_t stream);
 // lse and row loss of rows [0, rows) from the group statistics
 hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups,
                            const int64_t *target, int64_t ignore, int32_t V, const float *zt,
@@ -110,8 +117,8 @@ hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V,
                              const float2 *stats, int64_t ldstat, const float *lse,
                              const float *row_loss, const int64_t *target, int64_t ignore,
                              hipStream_t stream);
-hipError_t launch_xent_total(const float *row_loss, int64_t rows, const float *scal, float *loss,
-                             hipStream_t stream);
+hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t *target,
+                             int64_t ignore, int32_t mean, float *loss, hipStream_t stream);
 
 // dg, du (row stride lddg, zero in columns [F, round8(F))) and h (or NULL)
 // from a checkpoint of g and u and from dh

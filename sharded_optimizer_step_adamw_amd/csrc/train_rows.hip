@@ -106,61 +106,82 @@ __global__ __launch_bounds__(kThreads) void act8_unpack_kernel(const uint8_t *__
     }
 }
 
-// valid rows, and the factors of the loss and of the gradients
-__global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t *__restrict__ target, int64_t rows,
-                                                          int64_t ignore, int mean, float grad_scale,
-                                                          float *__restrict__ scal) {
+// The number of rows that take part, summed over a block of 1024 threads.
+__device__ __forceinline__ long long valid_rows(const int64_t *__restrict__ target, int64_t rows, int64_t ignore) {
     __shared__ long long part[16];
     long long n = 0;
-    if (mean)
-        for (int64_t i = threadIdx.x; i < rows; i += 1024) n += target[i] != ignore ? 1 : 0;
+    for (int64_t i = threadIdx.x; i < rows; i += 1024) n += target[i] != ignore ? 1 : 0;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        long long all = 0;
-        for (int k = 0; k < 16; ++k) all += part[k];
-        const double share = !mean ? 1.0 : all > 0 ? 1.0 / (double)all : 0.0;
-        scal[kXentShare] = (float)share;
-        scal[kXentGrad] = (float)(share * (double)grad_scale);
-    }
+    long long all = 0;
+    for (int k = 0; k < 16; ++k) all += part[k];
+    return all;
+}
+__device__ __forceinline__ double share_of(long long rows, int mean) {
+    return !mean ? 1.0 : rows > 0 ? 1.0 / (double)rows : 0.0;
 }
 
-// lse = m + log(sum_g s_g exp(m_g - m)), m the largest group maximum: a block
-// of 256 threads takes 64 rows, four threads a row (a quarter of the groups
-// each, joined in a fixed order).  A target outside [0, V) that is not the
-// ignored one makes the row NaN.
-__global__ __launch_bounds__(kThreads) void xent_lse_kernel(const float2 *__restrict__ stats, int64_t ldstat,
-                                                            int groups, const int64_t *__restrict__ target,
-                                                            int64_t ignore, int V, const float *__restrict__ zt,
-                                                            int64_t rows, float *__restrict__ lse,
-                                                            float *__restrict__ row_loss) {
-    __shared__ float pm[4][64], ps[4][64];
-    const int lr = threadIdx.x & 63, part = threadIdx.x >> 6;
-    const int64_t row = blockIdx.x * (int64_t)64 + lr;
+// the gradients' factor
+__global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t *__restrict__ target, int64_t rows,
+                                                          int64_t ignore, int mean, float grad_scale,
+                                                          float *__restrict__ factor) {
+    const long long n = mean ? valid_rows(target, rows, ignore) : 0;
+    if (threadIdx.x == 0) *factor = (float)(share_of(n, mean) * (double)grad_scale);
+}
+
+// (m, s) of two sets of exponentials, s relative to exp(m)
+__device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
+    const float t = fmaxf(m, m2);
+    const float ref = t == -INFINITY ? 0.0f : t;  // (a NaN maximum is left out here and makes the sum NaN)
+    s = s * expf(m - ref) + s2 * expf(m2 - ref);
+    m = t;
+}
+
+// lse = m + log(sum_g s_g exp(m_g - m)), m the largest group maximum.  A block
+// of 1024 threads takes 16 rows, 64 threads a row; each joins every 64th
+// group, eight at a time so that as many loads are in flight, and the 64 join
+// in a fixed order.  A target outside [0, V) that is not the ignored one
+// makes the row NaN.
+__global__ __launch_bounds__(1024) void xent_lse_kernel(const float2 *__restrict__ stats, int64_t ldstat, int groups,
+                                                        const int64_t *__restrict__ target, int64_t ignore, int V,
+                                                        const float *__restrict__ zt, int64_t rows,
+                                                        float *__restrict__ lse, float *__restrict__ row_loss) {
+    __shared__ float pm[16][16], ps[16][16];
+    const int lr = threadIdx.x & 15, part = threadIdx.x >> 4;
+    const int64_t row = blockIdx.x * (int64_t)16 + lr;
+    const bool live = row < rows;
     float m = -INFINITY, s = 0.0f;
-    if (row < rows) {
-        const int g0 = (int)((int64_t)groups * part / 4), g1 = (int)((int64_t)groups * (part + 1) / 4);
-        for (int g = g0; g < g1; ++g) {
-            const float2 v = stats[g * ldstat + row];
-            // (a NaN maximum leaves m, and the sum NaN)
-            const float t = fmaxf(m, v.x);
+    if (live) {
+        const float2 *p = stats + row;
+        for (int g = part; g < groups; g += 512) {
+            float2 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = g + 64 * k < groups ? p[(int64_t)(g + 64 * k) * ldstat] : make_float2(-INFINITY, 0.0f);
+            float t = m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t = fmaxf(t, v[k].x);
             const float ref = t == -INFINITY ? 0.0f : t;
-            s = s * expf(m - ref) + v.y * expf(v.x - ref);
+            s *= expf(m - ref);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k].y * expf(v[k].x - ref);
             m = t;
         }
     }
-    pm[part][lr] = m;
-    ps[part][lr] = s;
-    __syncthreads();
-    if (part != 0 || row >= rows) return;
-    for (int k = 1; k < 4; ++k) {
-        const float t = fmaxf(m, pm[k][lr]);
-        const float ref = t == -INFINITY ? 0.0f : t;
-        s = s * expf(m - ref) + ps[k][lr] * expf(pm[k][lr] - ref);
-        m = t;
+#pragma unroll
+    for (int o = 16; o <= 32; o <<= 1) {
+        const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
+        join(m, s, m2, s2);
     }
+    if ((part & 3) == 0) {
+        pm[part >> 2][lr] = m;
+        ps[part >> 2][lr] = s;
+    }
+    __syncthreads();
+    if (part != 0 || !live) return;
+    for (int k = 1; k < 16; ++k) join(m, s, pm[k][lr], ps[k][lr]);
     const int64_t t = target[row];
     const bool in = t >= 0 && t < V;
     const float ls = logf(s);
@@ -207,8 +228,10 @@ __global__ __launch_bounds__(kThreads) void xent_probs_kernel(uint16_t *__restri
 
 // loss = share * sum of row losses, in double, in a fixed order
 __global__ __launch_bounds__(1024) void xent_total_kernel(const float *__restrict__ row_loss, int64_t rows,
-                                                          const float *__restrict__ scal, float *__restrict__ loss) {
+                                                          const int64_t *__restrict__ target, int64_t ignore,
+                                                          int mean, float *__restrict__ loss) {
     __shared__ double part[16];
+    const long long n = mean ? valid_rows(target, rows, ignore) : 0;
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < rows; i += 1024) s += (double)row_loss[i];
 #pragma unroll
@@ -218,7 +241,7 @@ __global__ __launch_bounds__(1024) void xent_total_kernel(const float *__restric
     if (threadIdx.x == 0) {
         double all = 0.0;
         for (int k = 0; k < 16; ++k) all += part[k];
-        *loss = (float)(all * (double)scal[kXentShare]);
+        *loss = (float)(all * share_of(n, mean));
     }
 }
 
@@ -282,15 +305,16 @@ hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t ro
 }
 
 hipError_t launch_xent_count(const int64_t *target, int64_t rows, int64_t ignore, int32_t mean, float grad_scale,
-                             float *scal, hipStream_t stream) {
-    hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, stream, target, rows, ignore, mean, grad_scale, scal);
+                             float *factor, hipStream_t stream) {
+    hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, stream, target, rows, ignore, mean, grad_scale,
+                       factor);
     return hipGetLastError();
 }
 
 hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups, const int64_t *target, int64_t ignore,
                            int32_t V, const float *zt, int64_t rows, float *lse, float *row_loss, hipStream_t stream) {
-    hipLaunchKernelGGL(xent_lse_kernel, dim3((uint32_t)((rows + 63) / 64)), dim3(kThreads), 0, stream, stats, ldstat,
-                       groups, target, ignore, V, zt, rows, lse, row_loss);
+    hipLaunchKernelGGL(xent_lse_kernel, dim3((uint32_t)((rows + 15) / 16)), dim3(1024), 0, stream, stats, ldstat, groups,
+                       target, ignore, V, zt, rows, lse, row_loss);
     return hipGetLastError();
 }
 
@@ -302,8 +326,9 @@ hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V, 
     return hipGetLastError();
 }
 
-hipError_t launch_xent_total(const float *row_loss, int64_t rows, const float *scal, float *loss, hipStream_t stream) {
-    hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(1024), 0, stream, row_loss, rows, scal, loss);
+hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t *target, int64_t ignore, int32_t mean,
+                             float *loss, hipStream_t stream) {
+    hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(1024), 0, stream, row_loss, rows, target, ignore, mean, loss);
     return hipGetLastError();
 }
 
