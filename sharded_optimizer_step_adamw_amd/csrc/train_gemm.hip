@@ -28,6 +28,9 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBK = 32;  // reduction elements per stage
 
+// output tiles
+enum Tile : int { kTile64 = 64, kTile128 = 128, kTile256x128 = 192, kTile256 = 256 };
+
 // f(0), f(1), ... with the index as a type
 template <int... M, class F>
 __device__ __forceinline__ void for_each(std::integer_sequence<int, M...>, F f) {
@@ -286,57 +289,61 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
     }
 }
 
-// Tiles.  A BM x BM tile per workgroup, its waves BM / WR x 64 each, from
-// 16 x 16 x 32 MFMAs with fp32 accumulators.  WPE: waves per SIMD.
-template <int BM>
+// Tiles.  A BM x BN tile per workgroup, its WR x WC waves BM / WR x 64 each,
+// from 16 x 16 x 32 MFMAs with fp32 accumulators; STAGES LDS buffers; WPE
+// waves per SIMD.
+template <int TILE>
 struct Cfg;
 template <>
-struct Cfg<256> { static constexpr int WR = 2, WC = 4, WPE = 2; };
+struct Cfg<kTile256> { static constexpr int BM = 256, BN = 256, WR = 2, WC = 4, STAGES = 4, WPE = 2; };
 template <>
-struct Cfg<128> { static constexpr int WR = 2, WC = 2, WPE = 2; };
+struct Cfg<kTile256x128> { static constexpr int BM = 256, BN = 128, WR = 2, WC = 2, STAGES = 3, WPE = 2; };
 template <>
-struct Cfg<64> { static constexpr int WR = 4, WC = 1, WPE = 4; };
+struct Cfg<kTile128> { static constexpr int BM = 128, BN = 128, WR = 2, WC = 2, STAGES = 4, WPE = 2; };
+template <>
+struct Cfg<kTile64> { static constexpr int BM = 64, BN = 64, WR = 4, WC = 1, STAGES = 4, WPE = 4; };
 
-constexpr int kStages = 4;
 // s_waitcnt: vmcnt <= n and lgkmcnt = 0 (gfx9 field layout: vmcnt[3:0],
 // expcnt[6:4], lgkmcnt[11:8], vmcnt high bits[15:14])
 #define WAIT_VM_LGKM0(n) ((((n) & 15) | (((n) >> 4) << 14) | (7 << 4)))
 
-// The main loop.  The reduction advances in stages of 32 through four LDS
-// buffers that buffer_load ... lds fills three stages ahead (16 bytes a lane;
+// The main loop.  The reduction advances in stages of 32 through STAGES LDS
+// buffers that buffer_load ... lds fills ahead (16 bytes a lane;
 // a lane outside the operand reads past its descriptor's end, which gives
 // zeros).  A stage's body: barrier (everyone's loads of the next stage have
 // landed and everyone has read this one's fragments) -> loads of the stage
-// four ahead into the buffer just freed -> the next stage's fragments, read
+// STAGES ahead into the buffer just freed -> the next stage's fragments, read
 // between this stage's MFMAs -> wait for those reads and for this wave's
 // loads of the stage after.
 //
 // The kernel is persistent: one round of resident workgroups walks all tiles,
-// and from a tile's last four stages on the loads are those of the
+// and from a tile's last STAGES stages on the loads are those of the
 // workgroup's next tile, so that its operands arrive while this one is
 // finished and stored.  A tile's stages are padded with zero stages to an
 // even number, four at least.
 //
 // LDS layouts: row-major rows of 64 bytes, 16-byte chunk c of row r at slot
-// c ^ ((r >> 1) & 3); k-major rows of 2 BM bytes, 32-byte unit u of row r at
+// c ^ ((r >> 1) & 3); k-major rows of 2 BM (2 BN) bytes, 32-byte unit u of row r at
 // unit u ^ qsw(r), read with ds_read_b64_tr_b16: lane 4 q + p of a 16-lane
 // group addresses row +q, columns 4 p .. 4 p + 3 of a 4 x 16 block, and lane
 // i receives rows +0 .. +3 of column i.  Both spread each read over all
 // banks.  The transposing reads are inline assembly: as ordinary loads the
 // compiler could not tell them from the copies in flight into other buffers
 // and would wait for those.  Each is waited for within the stage's body.
-template <int BM, int EPI, bool AKM, bool BKM>
-__global__ __launch_bounds__(Cfg<BM>::WR *Cfg<BM>::WC * 64)
-__attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
-    constexpr int WR = Cfg<BM>::WR, WC = Cfg<BM>::WC, NW = WR * WC;
+template <int TILE, int EPI, bool AKM, bool BKM>
+__global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64)
+__attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) {
+    using C = Cfg<TILE>;
+    constexpr int BM = C::BM, BN = C::BN, WR = C::WR, WC = C::WC, NW = WR * WC, kStages = C::STAGES;
     constexpr int WTM = BM / WR, FM = WTM / 16, FN = 4;
-    static_assert(BM / WC == 64, "a wave holds 64 columns");
-    constexpr int ROW = 64, OPB = BM * ROW, STAGE = 2 * OPB, LOADS = OPB / 1024 / NW, LPS = 2 * LOADS;
-    static_assert(LOADS >= 1 && LOADS * NW * 1024 == OPB, "whole kilobytes");
-    constexpr int QRB = 2 * BM, QCH = QRB / 16;
+    static_assert(BN / WC == 64, "a wave holds 64 columns");
+    constexpr int ROW = 64, OPA = BM * ROW, OPB = BN * ROW, STAGE = OPA + OPB;
+    constexpr int LA = OPA / 1024 / NW, LB = OPB / 1024 / NW, LPS = LA + LB;  // loads a wave and stage
+    static_assert(LA * NW * 1024 == OPA && LB * NW * 1024 == OPB, "whole kilobytes");
+    constexpr int QRA = 2 * BM, QRB = 2 * BN;  // k-major row bytes
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
     static_assert(!GLU || NW % 4 == 0, "a wave loads rows of the gate or of the up projection");
-    constexpr int BN = GLU ? BM / 2 : BM;  // output columns of a tile
+    constexpr int BO = GLU ? BN / 2 : BN;  // output columns of a tile
     constexpr int kOut = 0x7FFFFFF0;       // a byte offset past every descriptor
     __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * STAGE];
 
@@ -347,8 +354,8 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
     const uint32_t lds_base =
         (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds);
 
-    auto qsw = [](int r) __attribute__((always_inline)) {
-        return BM >= 128 ? (r & 3) | (((r >> 3) & 1) << 2) : ((r >> 1) & 1) | (((r >> 3) & 1) << 1);
+    auto qsw = [](int r, int width) __attribute__((always_inline)) {
+        return width >= 128 ? (r & 3) | (((r >> 3) & 1) << 2) : ((r >> 1) & 1) | (((r >> 3) & 1) << 1);
     };
 
     struct Tile {
@@ -370,12 +377,12 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
         int ti, tj;
         tile_at(t - item * per, L.tiles_m, L.tiles_n, ti, tj);
         T.m0 = ti * BM;
-        T.n0 = tj * BN;
+        T.n0 = tj * BO;
         const TgProblem &P = L.prob[T.prob];
         const int all = P.seg[0].stages + (!GLU && P.nseg > 1 ? P.seg[1].stages : 0);
         T.stage0 = T.split * L.split_stages;
         T.live = all - T.stage0 < L.split_stages ? all - T.stage0 : L.split_stages;
-        T.stages = T.live <= 4 ? 4 : (T.live + 1) & ~1;
+        T.stages = T.live <= 4 ? 4 : (T.live + 1) & ~1;  // (the switch to the next tile is kStages before)
         return true;
     };
     auto seek = [&](int slot, Tile &T) __attribute__((always_inline)) -> int {
@@ -392,7 +399,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
     const uint16_t *pa = nullptr, *pb = nullptr;
     int ka = 0, kb = 0, lda = 0, ldb = 0, ea = 0, eb = 0, seg_left = 0, total_left = 0;
     int sprob = 0, sm0 = 0, sn0 = 0;
-    int va[LOADS], vb[LOADS];
+    int va[LA], vb[LB];
     const int chunk8 = ((lane & 3) ^ ((lane >> 3) & 3)) << 3;  // row-major: the lane's k offset
     auto corner = [&](const TgOperand &o, bool km, int c0, int extent, int k0, const uint16_t *&p, int &k, int &ld,
                       int &e) __attribute__((always_inline)) {
@@ -414,7 +421,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
         corner(S.a, AKM, sm0, BM, k0, pa, ka, lda, ea);
         // gate / up: LDS blocks 0, 1 of each four hold the gate's rows (wave
         // w fills blocks w, w + NW, ...)
-        corner(GLU && (wave & 2) ? P.seg[1].b : S.b, BKM, sn0, BN, k0, pb, kb, ldb, eb);
+        corner(GLU && (wave & 2) ? P.seg[1].b : S.b, BKM, sn0, BO, k0, pb, kb, ldb, eb);
     };
     auto stream = [&](const Tile &T, bool live) __attribute__((always_inline)) {
         total_left = live ? T.live : 0;
@@ -426,28 +433,26 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
             open_segment(1, (T.stage0 - s0) * kBK);
         else
             open_segment(0, T.stage0 * kBK);
+        // k-major: kilobyte `kilo` holds 1024 / (2 width) k rows
+        auto across = [&](int kilo, int width, int ld, int e) __attribute__((always_inline)) -> int {
+            const int per = width / 8, r = kilo * (512 / width) + lane / per, s16 = lane % per;
+            const int col = (((s16 >> 1) ^ qsw(r, width)) << 4) + ((s16 & 1) << 3);
+            return col * 2 < e ? (r * ld + col) * 2 : kOut;
+        };
 #pragma unroll
-        for (int x = 0; x < LOADS; ++x) {
+        for (int x = 0; x < LA; ++x) {
             const int kilo = x * NW + wave;
-            if constexpr (AKM) {
-                const int r = kilo * (1024 / QRB) + lane / QCH, s16 = lane % QCH;
-                const int col = (((s16 >> 1) ^ qsw(r)) << 4) + ((s16 & 1) << 3);
-                va[x] = col * 2 < ea ? (r * lda + col) * 2 : kOut;
-            } else {
-                va[x] = ((kilo * 16 + (lane >> 2)) * lda + chunk8) * 2;
-            }
-            if constexpr (BKM) {
-                const int r = kilo * (1024 / QRB) + lane / QCH, s16 = lane % QCH;
-                const int col = (((s16 >> 1) ^ qsw(r)) << 4) + ((s16 & 1) << 3);
-                vb[x] = col * 2 < eb ? (r * ldb + col) * 2 : kOut;
-            } else {
-                // LDS row n of block `kilo` holds the tile's column 32 (kilo / 2)
-                // + 8 (n / 4) + 4 (kilo % 2) + n % 4; gate / up: of the 32
-                // columns of wave kilo / 4
-                const int n = lane >> 2, sub = 8 * (n >> 2) + 4 * (kilo & 1) + (n & 3);
-                const int row = (GLU ? (kilo >> 2) * 32 : (kilo >> 1) * 32) + sub;
-                vb[x] = (row * ldb + chunk8) * 2;
-            }
+            va[x] = AKM ? across(kilo, BM, lda, ea) : ((kilo * 16 + (lane >> 2)) * lda + chunk8) * 2;
+        }
+#pragma unroll
+        for (int x = 0; x < LB; ++x) {
+            const int kilo = x * NW + wave;
+            // row-major: LDS row n of block `kilo` holds the tile's column
+            // 32 (kilo / 2) + 8 (n / 4) + 4 (kilo % 2) + n % 4; gate / up: of
+            // the 32 columns of wave kilo / 4
+            const int n = lane >> 2, sub = 8 * (n >> 2) + 4 * (kilo & 1) + (n & 3);
+            const int row = (GLU ? (kilo >> 2) * 32 : (kilo >> 1) * 32) + sub;
+            vb[x] = BKM ? across(kilo, BN, ldb, eb) : (row * ldb + chunk8) * 2;
         }
     };
     auto extent = [&](bool km, int k, int ld, int e) __attribute__((always_inline)) -> int {
@@ -455,21 +460,22 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
         if (km) return ((k < kBK ? k : kBK) - 1) * ld * 2 + e;
         return e + k * 2;
     };
-    // load y of a stage: the operands' kilobytes in turn
+    // load y of a stage: A's kilobytes, then B's
     __amdgpu_buffer_rsrc_t ra, rb;
     auto open_stage = [&]() __attribute__((always_inline)) {
         ra = __builtin_amdgcn_make_buffer_rsrc((void *)pa, (short)0, extent(AKM, ka, lda, ea), 0x00020000);
         rb = __builtin_amdgcn_make_buffer_rsrc((void *)pb, (short)0, extent(BKM, kb, ldb, eb), 0x00020000);
     };
     auto gload = [&](int sbase, int y) __attribute__((always_inline)) {
-        const int kilo = (y >> 1) * NW + wave;
         // (a chunk past the row's end would be the next row's)
-        if (y & 1) {
-            const int o = BKM || chunk8 < kb ? vb[y >> 1] : kOut;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_ADDR(&lds[sbase + OPB + kilo * 1024]), 16, o, 0, 0, 0);
-        } else {
-            const int o = AKM || chunk8 < ka ? va[y >> 1] : kOut;
+        if (y < LA) {
+            const int kilo = y * NW + wave;
+            const int o = AKM || chunk8 < ka ? va[y] : kOut;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_ADDR(&lds[sbase + kilo * 1024]), 16, o, 0, 0, 0);
+        } else {
+            const int kilo = (y - LA) * NW + wave;
+            const int o = BKM || chunk8 < kb ? vb[y - LA] : kOut;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_ADDR(&lds[sbase + OPA + kilo * 1024]), 16, o, 0, 0, 0);
         }
     };
     auto close_stage = [&]() __attribute__((always_inline)) {
@@ -486,17 +492,19 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
     const int fr = lane & 15, fh = lane >> 4;
     const int foff = fr * ROW + ((fh ^ ((fr >> 1) & 3)) << 4);
     const int tr = 8 * fh + ((lane >> 2) & 3), tp = lane & 3;
-    const uint32_t toff = lds_base + tr * QRB + ((tp >> 1) << 4) + ((tp & 1) << 3) + (qsw(tr) << 5);
+    const uint32_t tlane = lds_base + ((tp >> 1) << 4) + ((tp & 1) << 3);
+    const uint32_t toffa = tlane + tr * QRA + ((qsw(tr, BM) ^ (wr * FM)) << 5);
+    const uint32_t toffb = tlane + tr * QRB + ((qsw(tr, BN) ^ (wc * FN)) << 5);
     bf16x8 fa[2][FM], fb[2][FN];
     // block `blk` of an operand: unit (first + blk) ^ qsw(row), i.e. the
     // address of block 0 with blk's bits flipped
-    auto tread = [&](uint32_t at, auto BLK) __attribute__((always_inline)) {
+    auto tread = [&](uint32_t at, auto BLK, auto ROWB) __attribute__((always_inline)) {
         tg_u32x2 lo, hi;
         uint32_t t;
         asm volatile(
             "v_xor_b32 %2, %3, %4\n\tds_read_b64_tr_b16 %0, %2\n\tds_read_b64_tr_b16 %1, %2 offset:%5"
             : "=&v"(lo), "=&v"(hi), "=&v"(t)
-            : "i"(decltype(BLK)::value << 5), "v"(at), "i"(4 * QRB));
+            : "i"(decltype(BLK)::value << 5), "v"(at), "i"(4 * decltype(ROWB)::value));
         return __builtin_bit_cast(bf16x8, tg_u32x4{lo.x, lo.y, hi.x, hi.y});
     };
     // fragment y of a stage: A's blocks, then B's
@@ -504,15 +512,16 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
         constexpr int y = decltype(Y)::value;
         if constexpr (y < FM) {
             if constexpr (AKM)
-                fa[buf][y] = tread((toff + sbase) ^ ((wr * FM) << 5), Y);
+                fa[buf][y] = tread(toffa + sbase, Y, std::integral_constant<int, QRA>{});
             else
                 fa[buf][y] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + (wr * WTM + y * 16) * ROW + foff]);
         } else {
             constexpr int j = y - FM;
             if constexpr (BKM)
-                fb[buf][j] = tread((toff + sbase + OPB) ^ ((wc * FN) << 5), std::integral_constant<int, j>{});
+                fb[buf][j] = tread(toffb + sbase + OPA, std::integral_constant<int, j>{},
+                                   std::integral_constant<int, QRB>{});
             else
-                fb[buf][j] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + OPB + (wc * 64 + j * 16) * ROW + foff]);
+                fb[buf][j] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + OPA + (wc * 64 + j * 16) * ROW + foff]);
         }
     };
     // (after a wait: nothing that uses the fragments moves above it)
@@ -545,7 +554,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
     int cur = 0;
     auto body = [&](auto PAR) __attribute__((always_inline)) {
         constexpr int par = decltype(PAR)::value;
-        const int nxt = (cur + 1) & (kStages - 1);
+        const int nxt = cur + 1 == kStages ? 0 : cur + 1;
         __builtin_amdgcn_s_barrier();
         open_stage();
         __builtin_amdgcn_sched_barrier(0);
@@ -585,12 +594,19 @@ __attribute__((amdgpu_waves_per_eu(Cfg<BM>::WPE))) void tg_kernel(TgLaunch L) {
             for (int j = 0; j < FN; ++j) acc[i][j] = tg_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         int kt = 0;
 #pragma clang loop unroll(disable)
-        for (; kt < cu.stages - kStages; kt += 2) {
+        for (; kt + 1 < cu.stages - kStages; kt += 2) {
             body(std::integral_constant<int, 0>{});
             body(std::integral_constant<int, 1>{});
         }
-        // the last four stages load the next tile's first ones (or zeros)
-        stream(more ? nx : cu, more);
+        if constexpr (kStages % 2 == 1) {
+            body(std::integral_constant<int, 0>{});
+            stream(more ? nx : cu, more);
+            body(std::integral_constant<int, 1>{});
+            kt += 2;
+        } else {
+            stream(more ? nx : cu, more);
+        }
+#pragma clang loop unroll(disable)
         for (; kt < cu.stages; kt += 2) {
             body(std::integral_constant<int, 0>{});
             body(std::integral_constant<int, 1>{});
@@ -634,19 +650,20 @@ int compute_units() {
     return cus / 8 * 8;
 }
 
-template <int BM, int EPI, bool AKM, bool BKM>
+template <int TILE, int EPI, bool AKM, bool BKM>
 hipError_t run(TgLaunch &L, hipStream_t stream) {
+    using C = Cfg<TILE>;
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
-    constexpr int BN = GLU ? BM / 2 : BM, threads = Cfg<BM>::WR * Cfg<BM>::WC * 64;
-    L.tiles_m = (L.M + BM - 1) / BM;
-    L.tiles_n = (L.N + BN - 1) / BN;
+    constexpr int BO = GLU ? C::BN / 2 : C::BN, threads = C::WR * C::WC * 64;
+    L.tiles_m = (L.M + C::BM - 1) / C::BM;
+    L.tiles_n = (L.N + BO - 1) / BO;
     const int64_t total = (int64_t)L.tiles_m * L.tiles_n * L.nprob * L.splits;
     if (total > 0x7FFFFF00) return hipErrorInvalidValue;
     L.total = (int32_t)total;
     L.padded = (L.total + 7) / 8 * 8;
-    const int64_t round = (int64_t)compute_units() * (Cfg<BM>::WPE * 4 / (threads / 64));
+    const int64_t round = (int64_t)compute_units() * (C::WPE * 4 / (threads / 64));
     const uint32_t grid = (uint32_t)(L.padded < round ? L.padded : round);
-    hipLaunchKernelGGL((tg_kernel<BM, EPI, AKM, BKM>), dim3(grid), dim3(threads), 0, stream, L);
+    hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM>), dim3(grid), dim3(threads), 0, stream, L);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && EPI == kTgStore && L.splits > 1) {
         const int64_t work = (int64_t)L.M * ((L.N + 3) / 4) * L.nprob;
@@ -659,9 +676,10 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
 
 template <int EPI, bool AKM, bool BKM>
 hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
-    if (L.tile == 256) return run<256, EPI, AKM, BKM>(L, stream);
-    if (L.tile == 128) return run<128, EPI, AKM, BKM>(L, stream);
-    return run<64, EPI, AKM, BKM>(L, stream);
+    if (L.tile == kTile256) return run<kTile256, EPI, AKM, BKM>(L, stream);
+    if (L.tile == kTile256x128) return run<kTile256x128, EPI, AKM, BKM>(L, stream);
+    if (L.tile == kTile128) return run<kTile128, EPI, AKM, BKM>(L, stream);
+    return run<kTile64, EPI, AKM, BKM>(L, stream);
 }
 
 }  // namespace
@@ -680,19 +698,20 @@ hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
 // few microseconds of the best, 5% at most.
 void plan_tg(TgEpilogue epi, TgLaunch &L) {
     struct Figures {
-        int tile, held;
+        int tile, bm, bn, held;
         double alone, full, plain, heavy;
     };
-    static constexpr Figures figures[3] = {
-        {256, 1, 0.66, 0.86, 4.0, 10.0}, {128, 2, 0.27, 0.235, 2.0, 7.0}, {64, 4, 0.17, 0.13, 1.5, 6.0}};
+    static constexpr Figures figures[3] = {{kTile256, 256, 256, 1, 0.66, 0.86, 4.0, 10.0},
+                                           {kTile128, 128, 128, 2, 0.27, 0.25, 2.0, 7.0},
+                                           {kTile64, 64, 64, 4, 0.17, 0.13, 1.5, 6.0}};
     constexpr int64_t cus = 256;
     const bool glu = epi == kTgGlu || epi == kTgGluBack;
     int all = L.prob[0].seg[0].stages;
     if (epi == kTgStore && L.prob[0].nseg > 1) all += L.prob[0].seg[1].stages;
     double best = 0;
     for (const Figures &f : figures) {
-        const int64_t bn = glu ? f.tile / 2 : f.tile;
-        const int64_t tiles = (L.M + f.tile - 1) / f.tile * ((L.N + bn - 1) / bn) * L.nprob;
+        const int64_t bn = glu ? f.bn / 2 : f.bn;
+        const int64_t tiles = (L.M + f.bm - 1) / f.bm * ((L.N + bn - 1) / bn) * L.nprob;
         const bool may = epi == kTgStore && !L.sum_in && !L.sum_out && tiles < 4 * cus;
         for (int split = 1; split <= (may ? 32 : 1); ++split) {
             const int per = (all + split - 1) / split;
