@@ -578,20 +578,23 @@ def _need_rows(t, dtype, rows, cols, name, device=None) -> int:
         raise TypeError(f"{name}: expected a tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, need {dtype}")
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (
-            cols is not None and t.shape[1] != cols):
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (
+            cols is not None and shape[1] != cols):
         want = tuple("any" if s is None else s for s in (rows, cols))
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {want}")
-    if t.device.type != "cuda":
+        raise ValueError(f"{name}: shape {tuple(shape)}, need {want}")
+    dev = t.device
+    if dev.type != "cuda":
         raise ValueError(f"{name}: must be a GPU tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    r, c = t.shape
+    if device is not None and dev != device:
+        raise ValueError(f"{name}: on {dev}, expected {device}")
+    r, c = shape
     if c == 0:
         raise ValueError(f"{name}: rows are empty")
-    if c > 1 and t.stride(1) != 1 or r > 1 and t.stride(0) < c:
-        raise ValueError(f"{name}: strides {t.stride()}, need contiguous rows that do not overlap")
-    return t.stride(0) if r > 1 else c
+    s0, s1 = t.stride()
+    if c > 1 and s1 != 1 or r > 1 and s0 < c:
+        raise ValueError(f"{name}: strides {(s0, s1)}, need contiguous rows that do not overlap")
+    return s0 if r > 1 else c
 
 
 def _need_act8(a, rows, cols, name, device=None) -> None:
@@ -609,14 +612,15 @@ def _ptr(t):
 
 
 class _On:
-    """Where a call's outputs and workspace come from when the caller gives
-    none: memory of the call's own stream, so that the allocator reuses it
-    only after the call."""
+    """The stream of a call, and where its outputs and workspace come from when
+    the caller gives none: memory of the call's own stream, so that the
+    allocator reuses it only after the call."""
 
     def __init__(self, device, stream):
         self.device = device
-        self.handle = _stream(device, stream)
-        self.other = self.handle != torch.cuda.current_stream(device).cuda_stream
+        current = torch._C._cuda_getCurrentRawStream(device.index)
+        self.handle = current if stream is None else _stream(device, stream)
+        self.other = self.handle != current
 
     def empty(self, shape, dtype):
         if not self.other:
@@ -625,31 +629,16 @@ class _On:
             return torch.empty(shape, dtype=dtype, device=self.device)
 
 
-_sizes = {}
-
-
-def _sized(fn, args, pointers, where, on, workspace):
-    """Runs fn(*args, workspace, size, stream) with a workspace of the size
-    that the same call asks for.  That size depends on the arguments but for
-    where the pointers (indices `pointers` of args) point, their alignment
-    apart; it is asked for once per such set of arguments."""
+def _sized(fn, args, where, on, workspace):
+    """Runs fn(*args, workspace, size, stream), with a workspace of the size
+    that the same call asks for if none is given."""
+    size = ctypes.c_size_t(0)
     if workspace is None:
-        key = list(args)
-        for i in pointers:
-            p = key[i]
-            key[i] = None if p is None else p & 15
-        key = (where, *key)
-        need = _sizes.get(key)
-        if need is None:
-            size = ctypes.c_size_t(0)
-            _check(fn(*args, None, ctypes.byref(size), None), f"{where}(workspace query)")
-            if len(_sizes) >= 4096:
-                _sizes.clear()
-            need = _sizes[key] = int(size.value)
-        workspace = on.empty(need, torch.uint8)
+        _check(fn(*args, None, ctypes.byref(size), None), where)
+        workspace = on.empty(size.value, torch.uint8)
     else:
         _need(workspace, torch.uint8, 0, "workspace", on.device)
-    size = ctypes.c_size_t(workspace.numel())
+        size.value = workspace.numel()
     _check(fn(*args, workspace.data_ptr(), ctypes.byref(size), on.handle), where)
 
 
@@ -679,7 +668,7 @@ def _linear_xent(x, w, target, ignore_index, mean, grad_scale, loss, row_loss, d
     # (a tensor of no rows has no address; the call takes NULL for "not wanted")
     args = (T, D, V, _ptr(x), ldx, _ptr(w), ldw, _ptr(target), int(ignore_index), int(mean),
             float(grad_scale), _ptr(loss), _ptr(row_loss), _ptr(dx), lddx, _ptr(dw), lddw)
-    _sized(lib().zopt_linear_xent, args, (3, 5, 7, 11, 12, 13, 15), "zopt_linear_xent", on, workspace)
+    _sized(lib().zopt_linear_xent, args, "zopt_linear_xent", on, workspace)
     return loss, row_loss, dx, dw
 
 
@@ -752,7 +741,7 @@ def act8_wgrad(dy, a: Act8, out: Optional[torch.Tensor] = None,
         out = on.empty((N, D), torch.bfloat16)
     ld = _need_rows(out, torch.bfloat16, N, D, "out", dy.device)
     _sized(lib().zopt_act8_wgrad, (T, N, D, _ptr(dy), lddy, _ptr(a.q), _ptr(a.scale), _ptr(out), ld),
-           (3, 5, 6, 7), "zopt_act8_wgrad", on, workspace)
+           "zopt_act8_wgrad", on, workspace)
     return out
 
 
@@ -799,7 +788,7 @@ def glu_forward(x, w_gate, w_up, act: str = "silu", checkpoint=False,
     c = [None] * 4 if kept is None else [_ptr(t) for a in kept for t in a]
     _sized(lib().zopt_glu_forward, (T, D, F, _ptr(x), ldx, _ptr(w_gate), _ptr(w_up), ldw,
                                     _act_id(act), _ptr(out), ldh, *c),
-           (3, 5, 6, 9, 11, 12, 13, 14), "zopt_glu_forward", on, workspace)
+           "zopt_glu_forward", on, workspace)
     return out if kept is None else (out, kept)
 
 
@@ -842,5 +831,5 @@ def glu_backward(dh, x, w_gate, w_up, act: str = "silu", checkpoint=None,
     _sized(lib().zopt_glu_backward, (T, D, F, _ptr(dh), lddh, *xa, _ptr(w_gate), _ptr(w_up), ldw,
                                      _act_id(act), *c, _ptr(h), ldh, _ptr(dx), lddx, _ptr(dw_gate),
                                      _ptr(dw_up), lddw),
-           (3, 5, 7, 8, 9, 10, 13, 14, 15, 16, 17, 19, 21, 22), "zopt_glu_backward", on, workspace)
+           "zopt_glu_backward", on, workspace)
     return dx, dw_gate, dw_up

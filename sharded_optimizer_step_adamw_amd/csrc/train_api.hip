@@ -100,7 +100,7 @@ struct Product {
     // scratch for the parts of a split reduction
     size_t parts() {
         plan_tg(epi, L);
-        return tg_part_bytes(L);
+        return tg_part_bytes(epi, L);
     }
     hipError_t run(bool a_km, bool b_km, char *part, hipStream_t s) {
         plan_tg(epi, L);
@@ -179,6 +179,7 @@ XentPlan xent_plan(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t l
         const int64_t r0 = k * p.piece, n = T - r0 < p.piece ? T - r0 : p.piece;
         if (n <= 0) break;
         if (k > 0 && r0 + n < T) continue;  // (pieces between are as the first)
+        parts = larger(parts, p.logits(r0, n).parts());
         if (dx) parts = larger(parts, p.dx(nullptr, n).parts());
         if (dw) parts = larger(parts, p.dw(nullptr, r0, n).parts());
     }
@@ -224,14 +225,15 @@ GluPlan glu_plan(int64_t T, int64_t D, int64_t F, const uint16_t *x, int64_t ldx
     if (back) {
         p.dg = c.take(T * p.fp * 2);
         p.du = c.take(T * p.fp * 2);
-        if (T > 0) p.part = c.take(larger(p.dx(nullptr).parts(), p.dw(nullptr).parts()));
+    }
+    if (T > 0) {
+        size_t parts = p.products(back ? kTgGluBack : kTgGlu).parts();
+        if (back) parts = larger(parts, larger(p.dx(nullptr).parts(), p.dw(nullptr).parts()));
+        p.part = c.take(parts);
     }
     p.total = c.total();
     return p;
 }
-
-bool vec8(const void *p, int64_t ld) { return aligned16(p) && (ld & 7) == 0; }
-bool vec4(const void *p, int64_t ld) { return ((uintptr_t)p & 7) == 0 && (ld & 3) == 0; }
 
 }  // namespace
 }  // namespace zopt
@@ -283,7 +285,7 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
         L.ldstat = n;
         L.target = target + r0;
         L.zt = zt;
-        ZOPT_TRY(logits.run(false, false, nullptr, s));
+        ZOPT_TRY(logits.run(false, false, ws + p.part, s));
         ZOPT_TRY(launch_xent_lse(stats, n, p.groups, target + r0, ignore_index, (int32_t)V, zt, n, lse, row + r0, s));
         if (e == nullptr) continue;
         ZOPT_TRY(launch_xent_probs(e, p.lde, n, (int32_t)V, stats, n, lse, row + r0, target + r0,
@@ -292,7 +294,6 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
             Product g = p.dx(ws, n);
             g.L.prob[0].out = dx + r0 * lddx;
             g.L.ldc = lddx;
-            g.L.vec = vec4(dx, lddx);
             g.L.alpha = factor;
             ZOPT_TRY(g.run(false, true, ws + p.part, s));
         }
@@ -301,7 +302,6 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
             g.L.prob[0].out = dw;
             g.L.prob[0].sum = reinterpret_cast<float *>(ws + p.sum);
             g.L.ldc = lddw;
-            g.L.vec = vec4(dw, lddw);
             g.L.alpha = factor;
             ZOPT_TRY(g.run(true, true, ws + p.part, s));
         }
@@ -340,12 +340,11 @@ ZOPT_EXPORT zopt_status zopt_glu_forward(int64_t T, int64_t D, int64_t F, const 
     L.act = act;
     L.h = h;
     L.ldc = ldh;
-    L.vec = vec8(h, ldh);
     L.g8 = g8;
     L.gs = g_scale;
     L.u8 = u8;
     L.us = u_scale;
-    return device(both.run(false, false, nullptr, s));
+    return device(both.run(false, false, ws + p.part, s));
 }
 
 ZOPT_EXPORT zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const uint16_t *dh, int64_t lddh,
@@ -398,25 +397,21 @@ ZOPT_EXPORT zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const
         L.act = act;
         L.h = h;
         L.ldc = ldh;
-        L.vec = vec8(h, ldh);
         L.dh = dh;
         L.lddh = lddh;
-        L.dhvec = vec8(dh, lddh);
         L.dg = dg;
         L.du = du;
         L.lddg = p.fp;
-        ZOPT_TRY(both.run(false, false, nullptr, s));
+        ZOPT_TRY(both.run(false, false, ws + p.part, s));
     }
     Product gx = p.dx(ws);
     gx.L.prob[0].out = dx;
     gx.L.ldc = lddx;
-    gx.L.vec = vec4(dx, lddx);
     ZOPT_TRY(gx.run(false, true, ws + p.part, s));
     Product gw = p.dw(ws);
     gw.L.prob[0].out = dw_gate;
     gw.L.prob[1].out = dw_up;
     gw.L.ldc = lddw;
-    gw.L.vec = vec4(dw_gate, lddw) && vec4(dw_up, lddw);
     return device(gw.run(true, true, ws + p.part, s));
 }
 
@@ -464,6 +459,5 @@ ZOPT_EXPORT zopt_status zopt_act8_wgrad(int64_t T, int64_t N, int64_t D, const u
     g.L.prob[0].seg[0] = segment(across(y, 0, T), across(x, 0, T));
     g.L.prob[0].out = dw;
     g.L.ldc = lddw;
-    g.L.vec = vec4(dw, lddw);
     return device(g.run(true, true, ws + part, s));
 }

@@ -146,7 +146,7 @@ __device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
 // the lanes q = 0 .. 3 of column c: the scale from the largest magnitude of
 // all four, then the lane's eight bytes.
 __device__ __forceinline__ void act8_store(const float (&v)[8], int n, uint8_t *qrow, uint8_t *srow, int col,
-                                           int q, bool live, bool vec) {
+                                           int q, bool live) {
     uint32_t big = 0;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -159,7 +159,7 @@ __device__ __forceinline__ void act8_store(const float (&v)[8], int n, uint8_t *
     big = o > big ? o : big;
     const uint32_t byte = tg_scale_byte(big);
     if (!live) return;
-    if (n > 0) tg_store8b(qrow + col, tg_pack_e4m3(v, byte), n, vec);
+    if (n > 0) tg_store8b(qrow + col, tg_pack_e4m3(v, byte), n);
     if (q == 0) srow[col >> 5] = (uint8_t)byte;
 }
 
@@ -173,7 +173,6 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
     const int col = C0 + q * 8;
     const int n = F - col > 8 ? 8 : F - col < 0 ? 0 : F - col;
     const int64_t blocks = (F + 31) / 32;
-    const bool vec = L.vec != 0, qvec = (F & 7) == 0;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int row = R0 + i * 16 + c;
@@ -187,15 +186,15 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
         if constexpr (!BACK) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) h[k] = tg_act(g[k], L.act).a * u[k];
-            if (live && n > 0) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n, vec);
+            if (live && n > 0) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n);
             if (L.g8 != nullptr) {
-                act8_store(g, n, L.g8 + (int64_t)row * F, L.gs + (int64_t)row * blocks, col, q, live, qvec);
-                act8_store(u, n, L.u8 + (int64_t)row * F, L.us + (int64_t)row * blocks, col, q, live, qvec);
+                act8_store(g, n, L.g8 + (int64_t)row * F, L.gs + (int64_t)row * blocks, col, q, live);
+                act8_store(u, n, L.u8 + (int64_t)row * F, L.us + (int64_t)row * blocks, col, q, live);
             }
         } else {
             if (live && n > 0) {
                 float dh[8], dg[8], du[8];
-                unpack8(tg_load8h(L.dh + (int64_t)row * L.lddh + col, n, L.dhvec != 0), dh);
+                unpack8(tg_load8h(L.dh + (int64_t)row * L.lddh + col, n), dh);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const TgActValue a = tg_act(g[k], L.act);
@@ -206,39 +205,25 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
                 // (the padded row has room for all eight)
                 *reinterpret_cast<tg_u32x4 *>(L.dg + (int64_t)row * L.lddg + col) = pack8(dg);
                 *reinterpret_cast<tg_u32x4 *>(L.du + (int64_t)row * L.lddg + col) = pack8(du);
-                if (L.h != nullptr) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n, vec);
+                if (L.h != nullptr) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n);
             }
         }
     }
 }
 
-// four columns of a row, col .. col + 3, of which those below N exist
-__device__ __forceinline__ void store4(const TgLaunch &L, uint16_t *o, tg_f32x4 v, float alpha, int col) {
-    const tg_u32x2 p{tg_pack_bf16(v[0] * alpha, v[1] * alpha), tg_pack_bf16(v[2] * alpha, v[3] * alpha)};
-    if (L.vec && col + 4 <= L.N) {
-        *reinterpret_cast<tg_u32x2 *>(o) = p;
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (col + k < L.N) o[k] = (uint16_t)((k < 2 ? p.x : p.y) >> (16 * (k & 1)));
-    }
-}
-
-// A tile of sums: alpha * acc to bf16, fp32 sums kept for a later call, or
-// this part of a split reduction in fp32.
+// A tile of sums: alpha * acc to bf16, or fp32 sums kept for a later call.
 // PERM: the column order of a row-major B (eight consecutive per lane).
 template <int FM, int FN, bool PERM>
-__device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProblem &P, int part,
-                                               tg_f32x4 (&acc)[FM][FN], int R0, int C0) {
+__device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProblem &P, tg_f32x4 (&acc)[FM][FN], int R0,
+                                               int C0) {
     const int lane = lane_id(), c = lane & 15, q = lane >> 4;
     const float alpha = L.alpha ? *L.alpha : 1.0f;
     // the lane's first column, and the one of block j
     const int first = C0 + (PERM ? q * 8 : q * 4);
     auto at = [](int j) __attribute__((always_inline)) { return PERM ? (j >> 1) * 32 + (j & 1) * 4 : j * 16; };
     const int rows = L.M - R0 - c, cols = L.N - first;  // what is left from the lane's first place on
-    const bool parts = L.splits > 1, in = L.sum_in != 0;
-    float *s = parts ? L.part + part * L.part_stride : P.sum;
-    s += (int64_t)(R0 + c) * L.ldsum + first;  // (rows of fp32 sums are padded to a multiple of 4)
+    const bool in = L.sum_in != 0;
+    float *s = P.sum + (int64_t)(R0 + c) * L.ldsum + first;  // (rows of fp32 sums are padded to a multiple of 4)
     const int64_t sstep = 16 * L.ldsum;
     auto sum = [&](int i, int j) __attribute__((always_inline)) {
         tg_f32x4 v = acc[i][j];
@@ -247,7 +232,7 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
     };
     uint16_t *o = P.out + (int64_t)(R0 + c) * L.ldc + first;
     const int64_t step = 16 * L.ldc;
-    if (parts || L.sum_out) {
+    if (L.sum_out) {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -256,37 +241,40 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
             s += sstep;
             __builtin_amdgcn_sched_barrier(0);
         }
-    } else if (L.vec && (L.N & 3) == 0) {
+    } else {
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 if (i * 16 < rows && at(j) < cols) {
                     const tg_f32x4 v = sum(i, j) * alpha;
-                    *reinterpret_cast<tg_u32x2 *>(o + at(j)) =
-                        tg_u32x2{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3])};
+                    const tg_u32x2 p{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3])};
+                    if (at(j) + 4 <= cols) {
+                        tg_store(o + at(j), p);
+                    } else {
+                        o[at(j)] = (uint16_t)p.x;
+                        if (at(j) + 1 < cols) o[at(j) + 1] = (uint16_t)(p.x >> 16);
+                        if (at(j) + 2 < cols) o[at(j) + 2] = (uint16_t)p.y;
+                    }
                 }
             }
             o += step;
             s += sstep;
             __builtin_amdgcn_sched_barrier(0);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-#pragma unroll
-            for (int j = 0; j < FN; ++j)
-                if (i * 16 < rows && at(j) < cols) {
-                    const tg_f32x4 v = sum(i, j) * alpha;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (at(j) + k < cols) o[at(j) + k] = (uint16_t)tg_pack_bf16(v[k], 0.0f);
-                }
-            o += step;
-            s += sstep;
-            __builtin_amdgcn_sched_barrier(0);
-        }
     }
+}
+
+// What becomes of a wave's sums, BM / WR rows from R0 and 64 columns (32 of
+// the gate and of the up projection) from C0 on.
+template <int EPI, bool BKM, int FM>
+__device__ __forceinline__ void finish(const TgLaunch &L, int prob, tg_f32x4 (&acc)[FM][4], int R0, int C0) {
+    if constexpr (EPI == kTgXent)
+        xent_epilogue<FM>(L, acc, R0, C0);
+    else if constexpr (EPI == kTgGlu || EPI == kTgGluBack)
+        glu_epilogue<FM, EPI == kTgGluBack>(L, acc, R0, C0);
+    else
+        store_epilogue<FM, 4, !BKM>(L, L.prob[prob], acc, R0, C0);
 }
 
 // Tiles.  A BM x BN tile per workgroup, its WR x WC waves BM / WR x 64 each,
@@ -306,6 +294,21 @@ struct Cfg<kTile64> { static constexpr int BM = 64, BN = 64, WR = 4, WC = 1, STA
 // s_waitcnt: vmcnt <= n and lgkmcnt = 0 (gfx9 field layout: vmcnt[3:0],
 // expcnt[6:4], lgkmcnt[11:8], vmcnt high bits[15:14])
 #define WAIT_VM_LGKM0(n) ((((n) & 15) | (((n) >> 4) << 14) | (7 << 4)))
+
+// A wave's sums of part `split` of split tile t, in register order (16 bytes a
+// lane).
+template <int FM, int NW>
+__device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, int wave, tg_f32x4 (&acc)[FM][4]) {
+    tg_f32x4 *p = reinterpret_cast<tg_f32x4 *>(L.part) +
+                  (((int64_t)t * L.splits + split) * NW + wave) * (FM * 4 * 64) + lane_id();
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[j * 64] = acc[i][j];
+        p += 4 * 64;
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
 
 // The main loop.  The reduction advances in stages of 32 through STAGES LDS
 // buffers that buffer_load ... lds fills ahead (16 bytes a lane;
@@ -359,7 +362,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     };
 
     struct Tile {
-        int prob, split, m0, n0, stage0, live, stages;  // live: real stages; stages: padded
+        int t, prob, split, m0, n0, stage0, live, stages;  // split: -1 whole; live: real stages; stages: padded
     };
     // slot -> tile (false: a padding slot).  Workgroups go to the 8 XCDs in
     // turn; XCD x takes the x-th contiguous eighth of each round of resident
@@ -370,18 +373,25 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         const int rem = L.padded - base < grid ? L.padded - base : grid;
         int t = base + (slot & 7) * (rem >> 3) + ((slot - base) >> 3);
         if (t >= L.total) return false;
+        // (parts of the tiles that are split: all first ones, all second ones, ...)
+        T.split = -1;
+        if (t >= L.whole && L.splits > 1) {
+            const int rest = L.tiles - L.whole;
+            T.split = (t - L.whole) / rest;
+            t -= T.split * rest;
+        }
+        T.t = t;
         const int per = L.tiles_m * L.tiles_n;
-        const int item = t / per;
-        T.prob = item / L.splits;
-        T.split = item - T.prob * L.splits;
+        T.prob = t >= per ? 1 : 0;
         int ti, tj;
-        tile_at(t - item * per, L.tiles_m, L.tiles_n, ti, tj);
+        tile_at(t - T.prob * per, L.tiles_m, L.tiles_n, ti, tj);
         T.m0 = ti * BM;
         T.n0 = tj * BO;
         const TgProblem &P = L.prob[T.prob];
         const int all = P.seg[0].stages + (!GLU && P.nseg > 1 ? P.seg[1].stages : 0);
-        T.stage0 = T.split * L.split_stages;
-        T.live = all - T.stage0 < L.split_stages ? all - T.stage0 : L.split_stages;
+        T.stage0 = T.split < 0 ? 0 : T.split * L.split_stages;
+        T.live = all - T.stage0;
+        if (T.split >= 0 && T.live > L.split_stages) T.live = L.split_stages;
         T.stages = T.live <= 4 ? 4 : (T.live + 1) & ~1;  // (the switch to the next tile is kStages before)
         return true;
     };
@@ -592,33 +602,19 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = tg_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        int kt = 0;
+        // (from stage kStages before the end on, the loads are the next tile's
+        // first ones, or zeros)
 #pragma clang loop unroll(disable)
-        for (; kt + 1 < cu.stages - kStages; kt += 2) {
+        for (int kt = cu.stages; kt > 0; kt -= 2) {
+            if (kStages % 2 == 0 && kt == kStages) stream(more ? nx : cu, more);
             body(std::integral_constant<int, 0>{});
+            if (kStages % 2 == 1 && kt == kStages + 1) stream(more ? nx : cu, more);
             body(std::integral_constant<int, 1>{});
         }
-        if constexpr (kStages % 2 == 1) {
-            body(std::integral_constant<int, 0>{});
-            stream(more ? nx : cu, more);
-            body(std::integral_constant<int, 1>{});
-            kt += 2;
-        } else {
-            stream(more ? nx : cu, more);
-        }
-#pragma clang loop unroll(disable)
-        for (; kt < cu.stages; kt += 2) {
-            body(std::integral_constant<int, 0>{});
-            body(std::integral_constant<int, 1>{});
-        }
-        const TgProblem &P = L.prob[cu.prob];
-        const int R0 = cu.m0 + wr * WTM;
-        if constexpr (EPI == kTgXent)
-            xent_epilogue<FM>(L, acc, R0, cu.n0 + wc * 64);
-        else if constexpr (GLU)
-            glu_epilogue<FM, EPI == kTgGluBack>(L, acc, R0, cu.n0 + wc * 32);
+        if (cu.split >= 0)
+            keep_part<FM, NW>(L, cu.t - L.whole, cu.split, wave, acc);
         else
-            store_epilogue<FM, FN, !BKM>(L, P, cu.prob * L.splits + cu.split, acc, R0, cu.n0 + wc * 64);
+            finish<EPI, BKM, FM>(L, cu.prob, acc, cu.m0 + wr * WTM, cu.n0 + wc * (GLU ? 32 : 64));
         if (!more) break;
         cu = nx;
         slot = nslot;
@@ -627,27 +623,47 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     __builtin_amdgcn_s_waitcnt(0);
 }
 
-// out = bf16(alpha * sum over splits of part), four columns a thread, in
-// split order
-__global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
-    const int64_t per = (L.N + 3) / 4, one = per * L.M, total = one * L.nprob;
-    const float alpha = L.alpha ? *L.alpha : 1.0f;
-    for (int64_t id = blockIdx.x * (int64_t)256 + threadIdx.x; id < total; id += (int64_t)gridDim.x * 256) {
-        const int pi = id >= one ? 1 : 0;
-        const int64_t k = id - pi * one, row = k / per, col = (k - row * per) * 4;
-        const float *p = L.part + (int64_t)pi * L.splits * L.part_stride + row * L.ldsum + col;
-        tg_f32x4 v = *reinterpret_cast<const tg_f32x4 *>(p);
-        for (int s = 1; s < L.splits; ++s) v += *reinterpret_cast<const tg_f32x4 *>(p + s * L.part_stride);
-        store4(L, L.prob[pi].out + row * L.ldc + col, v, alpha, (int)col);
+// The tiles that were split: their parts' sums, added in order, and then what
+// the whole tiles' workgroups do.  One workgroup a tile.
+template <int TILE, int EPI, bool BKM>
+__global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64) void tg_join_kernel(TgLaunch L) {
+    using C = Cfg<TILE>;
+    constexpr int NW = C::WR * C::WC, WTM = C::BM / C::WR, FM = WTM / 16;
+    constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const tg_f32x4 *p = reinterpret_cast<const tg_f32x4 *>(L.part) +
+                        ((int64_t)blockIdx.x * L.splits * NW + wave) * (FM * 4 * 64) + lane;
+    tg_f32x4 acc[FM][4];
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = p[(i * 4 + j) * 64];
+#pragma clang loop unroll(disable)
+    for (int s = 1; s < L.splits; ++s) {
+        p += (int64_t)NW * (FM * 4 * 64);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] += p[(i * 4 + j) * 64];
     }
+    const int t = L.whole + blockIdx.x, per = L.tiles_m * L.tiles_n, prob = t >= per ? 1 : 0;
+    int ti, tj;
+    tile_at(t - prob * per, L.tiles_m, L.tiles_n, ti, tj);
+    finish<EPI, BKM, FM>(L, prob, acc, ti * C::BM + (wave / C::WC) * WTM,
+                         tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64));
 }
 
+// Compute units of the current device (asked for once), a multiple of the 8
+// XCDs.
 int compute_units() {
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess ||
-        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 8)
-        cus = 256;
-    return cus / 8 * 8;
+    static const int cus = [] {
+        int dev = 0, n = 0;
+        if (hipGetDevice(&dev) != hipSuccess ||
+            hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n < 8)
+            n = 256;
+        return n / 8 * 8;
+    }();
+    return cus;
 }
 
 template <int TILE, int EPI, bool AKM, bool BKM>
@@ -657,18 +673,19 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
     constexpr int BO = GLU ? C::BN / 2 : C::BN, threads = C::WR * C::WC * 64;
     L.tiles_m = (L.M + C::BM - 1) / C::BM;
     L.tiles_n = (L.N + BO - 1) / BO;
-    const int64_t total = (int64_t)L.tiles_m * L.tiles_n * L.nprob * L.splits;
-    if (total > 0x7FFFFF00) return hipErrorInvalidValue;
+    const int64_t tiles = (int64_t)L.tiles_m * L.tiles_n * L.nprob;
+    const int64_t total = L.whole + (tiles - L.whole) * L.splits;
+    if (tiles > 0x7FFFFF00 || total > 0x7FFFFF00) return hipErrorInvalidValue;
+    L.tiles = (int32_t)tiles;
     L.total = (int32_t)total;
     L.padded = (L.total + 7) / 8 * 8;
     const int64_t round = (int64_t)compute_units() * (C::WPE * 4 / (threads / 64));
     const uint32_t grid = (uint32_t)(L.padded < round ? L.padded : round);
     hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM>), dim3(grid), dim3(threads), 0, stream, L);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && EPI == kTgStore && L.splits > 1) {
-        const int64_t work = (int64_t)L.M * ((L.N + 3) / 4) * L.nprob;
-        const int64_t blocks = (work + 255) / 256;
-        hipLaunchKernelGGL(tg_join_kernel, dim3((uint32_t)(blocks < 65536 ? blocks : 65536)), dim3(256), 0, stream, L);
+    if (e == hipSuccess && L.splits > 1) {
+        hipLaunchKernelGGL((tg_join_kernel<TILE, EPI, BKM>), dim3((uint32_t)(tiles - L.whole)), dim3(threads), 0,
+                           stream, L);
         e = hipGetLastError();
     }
     return e;
@@ -686,57 +703,60 @@ hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
 
 // Tile and split, by an estimate of the launch's time in microseconds from
 // figures measured on the card (256 CUs):
-//   stage   one workgroup alone on its CU takes 0.66 / 0.27 / 0.17 a stage of
-//           32 on tiles of 256 / 128 / 64, bound by latency; a CU with all it
-//           holds (1 / 2 / 4 of them) 0.86 / 0.47 / 0.52 for all together
-//   tile    its first loads and its epilogue: about 4 / 2 / 1.5 plain, 10 / 7 /
-//           6 with exponentials
+//   stage   one workgroup alone on its CU takes `alone` a stage of 32, bound by
+//           latency; a CU with all it holds (`held` of them) held * full
+//   tile    its first loads and its epilogue: `plain`, or `heavy` with
+//           exponentials
 //   split   a second launch (4) and 8 bytes an output and part at 5 TB/s
-// So a reduction is split where its tiles leave CUs idle: [256, 50304] x
-// [50304, 768] takes 1.05 ms whole on 256 tiles, 0.18 ms in 16 parts on 128
-// ones.  Checked against a sweep of 18 shapes x 3 tiles x 10 splits: within a
-// few microseconds of the best, 5% at most.
+// Full rounds of tiles are computed whole; those left over, which would leave
+// CUs idle, may be split along the reduction: [256, 50304] x [50304, 768]
+// takes 1.05 ms whole on 256 x 256 tiles, 0.18 ms in 16 parts on 128 x 128.
 void plan_tg(TgEpilogue epi, TgLaunch &L) {
     struct Figures {
         int tile, bm, bn, held;
         double alone, full, plain, heavy;
     };
-    static constexpr Figures figures[3] = {{kTile256, 256, 256, 1, 0.66, 0.86, 4.0, 10.0},
+    static constexpr Figures figures[4] = {{kTile256, 256, 256, 1, 0.66, 0.86, 4.0, 10.0},
+                                           {kTile256x128, 256, 128, 2, 0.46, 0.485, 3.0, 8.0},
                                            {kTile128, 128, 128, 2, 0.27, 0.25, 2.0, 7.0},
                                            {kTile64, 64, 64, 4, 0.17, 0.13, 1.5, 6.0}};
     constexpr int64_t cus = 256;
     const bool glu = epi == kTgGlu || epi == kTgGluBack;
     int all = L.prob[0].seg[0].stages;
-    if (epi == kTgStore && L.prob[0].nseg > 1) all += L.prob[0].seg[1].stages;
+    if (!glu && L.prob[0].nseg > 1) all += L.prob[0].seg[1].stages;
     double best = 0;
     for (const Figures &f : figures) {
-        const int64_t bn = glu ? f.bn / 2 : f.bn;
+        const int64_t bn = glu ? f.bn / 2 : f.bn, held = f.held * cus;
         const int64_t tiles = (L.M + f.bm - 1) / f.bm * ((L.N + bn - 1) / bn) * L.nprob;
-        const bool may = epi == kTgStore && !L.sum_in && !L.sum_out && tiles < 4 * cus;
-        for (int split = 1; split <= (may ? 32 : 1); ++split) {
+        const int64_t rounds = tiles / held, rest = tiles % held;
+        const double each = epi == kTgStore ? f.plain : f.heavy;
+        auto load = [&](int64_t n) { return f.alone > n * f.full ? f.alone : n * f.full; };
+        const double whole = rounds * (all * load(f.held) + each);
+        for (int split = 1; split <= 32; ++split) {
             const int per = (all + split - 1) / split;
-            if (split > 1 && per < 8) break;
-            const int parts = (all + per - 1) / per;
-            if (parts != split) continue;
-            const int64_t on = (tiles * parts + cus - 1) / cus, rounds = on / f.held, rest = on % f.held;
-            auto load = [&](double n) { return f.alone > n * f.full ? f.alone : n * f.full; };
-            double t = per * (rounds * load(f.held) + (rest ? load((double)rest) : 0.0)) +
-                       (double)(rounds + (rest ? 1 : 0)) * (epi == kTgStore ? f.plain : f.heavy);
-            if (parts > 1) t += 4.0 + 8.0 * parts * (double)L.M * L.N * L.nprob / 5.0e6;
+            if (split > 1 && (per < 8 || rest == 0)) break;
+            if ((all + per - 1) / per != split) continue;
+            const int64_t on = (rest * split + cus - 1) / cus, full = on / f.held, left = on % f.held;
+            double t = whole + full * (per * load(f.held) + each) + (left ? per * load(left) + each : 0.0);
+            if (split > 1) t += 4.0 + 8.0 * split * (double)(rest * f.bm * f.bn) / 5.0e6;
             if (best == 0 || t < best) {
                 best = t;
                 L.tile = f.tile;
-                L.splits = parts;
+                L.splits = split;
                 L.split_stages = per;
+                L.whole = (int32_t)(split > 1 ? tiles - rest : tiles);
             }
         }
     }
     L.ldsum = (L.N + 3) / 4 * 4;
-    L.part_stride = (int64_t)L.M * L.ldsum;
 }
 
-size_t tg_part_bytes(const TgLaunch &L) {
-    return L.splits > 1 ? (size_t)L.splits * L.nprob * L.part_stride * 4 : 0;
+size_t tg_part_bytes(TgEpilogue epi, const TgLaunch &L) {
+    if (L.splits == 1) return 0;
+    const int64_t bm = L.tile == kTile64 ? 64 : L.tile == kTile128 ? 128 : 256;
+    const int64_t bn = L.tile == kTile256x128 ? 128 : bm, bo = epi == kTgGlu || epi == kTgGluBack ? bn / 2 : bn;
+    const int64_t tiles = (L.M + bm - 1) / bm * ((L.N + bo - 1) / bo) * L.nprob;
+    return (size_t)((tiles - L.whole) * L.splits * bm * bn * 4);
 }
 
 hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStream_t stream) {

@@ -47,13 +47,14 @@ struct TgLaunch {
     TgProblem prob[2];
     int32_t nprob;
     int32_t M, N;             // output sizes (Glu: N = feed-forward width)
-    int32_t tile, tiles_m, tiles_n;  // tile side, grid of output tiles
-    int32_t splits, split_stages;    // kTgStore: the reduction in parts of split_stages stages
-    int32_t total, padded;           // tiles of all problems and parts; rounded up to 8
-    float *part;              // splits > 1: fp32 parts, part_stride each
-    int64_t part_stride;
+    int32_t tile, tiles_m, tiles_n;  // kind of tile, grid of output tiles
+    // Tiles [0, whole) are computed in one go, the others in `splits` parts of
+    // split_stages stages each, kept in `part` (fp32) and joined by a second
+    // launch
+    int32_t whole, splits, split_stages;
+    int32_t tiles, total, padded;  // tiles of all problems; with parts; rounded up to 8
+    float *part;
     int64_t ldc;
-    int32_t vec;              // outputs take vector stores
     // kTgStore
     const float *alpha;       // device scalar, or NULL: 1
     int64_t ldsum;
@@ -74,17 +75,16 @@ struct TgLaunch {
     uint8_t *gs, *us;
     const uint16_t *dh;
     int64_t lddh;
-    int32_t dhvec;
     uint16_t *dg, *du;        // row stride lddg, columns [N, round up to 8) written as zero
     int64_t lddg;
 };
 
 constexpr int kXentGroup = 64;  // columns per statistics group
 
-// Chooses tile and split (sets tile, splits, split_stages, ldsum, part_stride)
-// from the sizes, problems and segments; the parts' fp32 scratch.
+// Chooses tile and split (sets tile, whole, splits, split_stages, ldsum) from
+// the sizes, problems and segments; the parts' fp32 scratch.
 void plan_tg(TgEpilogue epi, TgLaunch &L);
-size_t tg_part_bytes(const TgLaunch &L);
+size_t tg_part_bytes(TgEpilogue epi, const TgLaunch &L);
 
 // a_km / b_km: operand is k-major.  kTgXent and the Glu kinds: both row-major.
 hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStream_t stream);
@@ -209,10 +209,20 @@ __device__ __forceinline__ void tg_unpack_e4m3(tg_u32x2 q, float s, float (&v)[8
     }
 }
 
-// up to 8 bytes / 16-bit values at p, of which the first n (< 8: the others
-// are not touched) exist; vec: p is aligned for one access
-__device__ __forceinline__ tg_u32x2 tg_load8b(const uint8_t *p, int n, bool vec) {
-    if (vec && n >= 8) return *reinterpret_cast<const tg_u32x2 *>(p);
+// 8 and 16 bytes at any address (global memory takes them unaligned)
+template <class V>
+__device__ __forceinline__ V tg_load(const void *p) {
+    V v;
+    __builtin_memcpy(&v, p, sizeof v);
+    return v;
+}
+template <class V>
+__device__ __forceinline__ void tg_store(void *p, V v) {
+    __builtin_memcpy(p, &v, sizeof v);
+}
+// up to 8 bytes / 16-bit values at p, of which the first n exist
+__device__ __forceinline__ tg_u32x2 tg_load8b(const uint8_t *p, int n) {
+    if (n >= 8) return tg_load<tg_u32x2>(p);
     tg_u32x2 r{0, 0};
     for (int k = 0; k < 8; ++k)
         if (k < n) {
@@ -221,25 +231,25 @@ __device__ __forceinline__ tg_u32x2 tg_load8b(const uint8_t *p, int n, bool vec)
         }
     return r;
 }
-__device__ __forceinline__ void tg_store8b(uint8_t *p, tg_u32x2 v, int n, bool vec) {
-    if (vec && n >= 8) {
-        *reinterpret_cast<tg_u32x2 *>(p) = v;
+__device__ __forceinline__ void tg_store8b(uint8_t *p, tg_u32x2 v, int n) {
+    if (n >= 8) {
+        tg_store(p, v);
         return;
     }
     for (int k = 0; k < 8; ++k)
         if (k < n) p[k] = (uint8_t)((k < 4 ? v.x >> (8 * k) : v.y >> (8 * (k - 4))) & 0xFFu);
 }
-__device__ __forceinline__ tg_u32x4 tg_load8h(const uint16_t *p, int n, bool vec) {
-    if (vec && n >= 8) return *reinterpret_cast<const tg_u32x4 *>(p);
+__device__ __forceinline__ tg_u32x4 tg_load8h(const uint16_t *p, int n) {
+    if (n >= 8) return tg_load<tg_u32x4>(p);
     tg_u32x4 r{0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k < n) r[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
     return r;
 }
-__device__ __forceinline__ void tg_store8h(uint16_t *p, tg_u32x4 v, int n, bool vec) {
-    if (vec && n >= 8) {
-        *reinterpret_cast<tg_u32x4 *>(p) = v;
+__device__ __forceinline__ void tg_store8h(uint16_t *p, tg_u32x4 v, int n) {
+    if (n >= 8) {
+        tg_store(p, v);
         return;
     }
 #pragma unroll

@@ -15,7 +15,6 @@ uint32_t blocks_for(int64_t n) {
     const int64_t b = (n + kThreads - 1) / kThreads;
     return (uint32_t)(b < 1 ? 1 : b > (1 << 20) ? (1 << 20) : b);
 }
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 __device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
 #pragma unroll
@@ -34,15 +33,14 @@ __device__ __forceinline__ tg_u32x4 pack8(const float (&v)[8]) {
 __global__ __launch_bounds__(kThreads) void pad_copy_kernel(const uint16_t *__restrict__ src, int64_t ld,
                                                             int64_t rows, int64_t cols, int64_t cp,
                                                             uint16_t *__restrict__ dst,
-                                                            const int64_t *__restrict__ target, int64_t ignore,
-                                                            int vec) {
+                                                            const int64_t *__restrict__ target, int64_t ignore) {
     const int64_t per = cp / 8, total = rows * per;
     for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
         const int64_t r = id / per, c = (id - r * per) * 8;
         const int64_t left = cols - c;
         tg_u32x4 v{0, 0, 0, 0};
         if (target == nullptr || target[r] != ignore)
-            v = tg_load8h(src + r * ld + c, left > 8 ? 8 : (int)left, vec != 0);
+            v = tg_load8h(src + r * ld + c, left > 8 ? 8 : (int)left);
         *reinterpret_cast<tg_u32x4 *>(dst + r * cp + c) = v;
     }
 }
@@ -60,7 +58,7 @@ __global__ __launch_bounds__(kThreads) void fill_zero_kernel(uint16_t *__restric
 // eight each.
 __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__restrict__ x, int64_t ld, int64_t rows,
                                                              int64_t cols, uint8_t *__restrict__ q,
-                                                             uint8_t *__restrict__ scale, int xvec, int qvec) {
+                                                             uint8_t *__restrict__ scale) {
     const int64_t blocks = (cols + 31) / 32, total = rows * blocks * 4;
     // (total is a multiple of 4, so the four threads of a block stay together)
     for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
@@ -68,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__r
         const int64_t c = cb * 32 + (id & 3) * 8, left = cols - c;
         const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
         tg_u32x4 p{0, 0, 0, 0};
-        if (n > 0) p = tg_load8h(x + r * ld + c, n, xvec != 0);
+        if (n > 0) p = tg_load8h(x + r * ld + c, n);
         float v[8];
         unpack8(p, v);
         uint32_t big = 0;
@@ -82,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__r
         o = __shfl_xor(big, 2);
         big = o > big ? o : big;
         const uint32_t byte = tg_scale_byte(big);
-        if (n > 0) tg_store8b(q + r * cols + c, tg_pack_e4m3(v, byte), n, qvec != 0);
+        if (n > 0) tg_store8b(q + r * cols + c, tg_pack_e4m3(v, byte), n);
         if ((id & 3) == 0) scale[b] = (uint8_t)byte;
     }
 }
@@ -90,7 +88,7 @@ __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__r
 __global__ __launch_bounds__(kThreads) void act8_unpack_kernel(const uint8_t *__restrict__ q,
                                                                const uint8_t *__restrict__ scale, int64_t rows,
                                                                int64_t cols, uint16_t *__restrict__ x, int64_t ld,
-                                                               int64_t cols_out, int qvec, int xvec) {
+                                                               int64_t cols_out) {
     const int64_t blocks = (cols + 31) / 32, per = (cols_out + 7) / 8, total = rows * per;
     for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
         const int64_t r = id / per, c = (id - r * per) * 8;
@@ -98,11 +96,11 @@ __global__ __launch_bounds__(kThreads) void act8_unpack_kernel(const uint8_t *__
         const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
         float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         if (n > 0) {
-            tg_unpack_e4m3(tg_load8b(q + r * cols + c, n, qvec != 0), tg_scale_out(scale[r * blocks + (c >> 5)]), v);
+            tg_unpack_e4m3(tg_load8b(q + r * cols + c, n), tg_scale_out(scale[r * blocks + (c >> 5)]), v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = k < n ? v[k] : 0.0f;
         }
-        tg_store8h(x + r * ld + c, pack8(v), lo > 8 ? 8 : (int)lo, xvec != 0);
+        tg_store8h(x + r * ld + c, pack8(v), lo > 8 ? 8 : (int)lo);
     }
 }
 
@@ -249,16 +247,15 @@ __global__ __launch_bounds__(1024) void xent_total_kernel(const float *__restric
 __global__ __launch_bounds__(kThreads) void glu_back_act8_kernel(
     const uint8_t *__restrict__ g8, const uint8_t *__restrict__ gs, const uint8_t *__restrict__ u8,
     const uint8_t *__restrict__ us, const uint16_t *__restrict__ dh, int64_t lddh, int64_t rows, int64_t F, int act,
-    uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int64_t lddg, uint16_t *__restrict__ h, int64_t ldh,
-    int qvec, int dhvec, int hvec) {
+    uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int64_t lddg, uint16_t *__restrict__ h, int64_t ldh) {
     const int64_t blocks = (F + 31) / 32, per = (F + 7) / 8, total = rows * per;
     for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
         const int64_t r = id / per, c = (id - r * per) * 8;
         const int n = F - c > 8 ? 8 : (int)(F - c);
         float g[8], u[8], d[8], og[8], ou[8], oh[8];
-        tg_unpack_e4m3(tg_load8b(g8 + r * F + c, n, qvec != 0), tg_scale_out(gs[r * blocks + (c >> 5)]), g);
-        tg_unpack_e4m3(tg_load8b(u8 + r * F + c, n, qvec != 0), tg_scale_out(us[r * blocks + (c >> 5)]), u);
-        unpack8(tg_load8h(dh + r * lddh + c, n, dhvec != 0), d);
+        tg_unpack_e4m3(tg_load8b(g8 + r * F + c, n), tg_scale_out(gs[r * blocks + (c >> 5)]), g);
+        tg_unpack_e4m3(tg_load8b(u8 + r * F + c, n), tg_scale_out(us[r * blocks + (c >> 5)]), u);
+        unpack8(tg_load8h(dh + r * lddh + c, n), d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const TgActValue a = tg_act(g[k], act);
@@ -268,7 +265,7 @@ __global__ __launch_bounds__(kThreads) void glu_back_act8_kernel(
         }
         *reinterpret_cast<tg_u32x4 *>(dg + r * lddg + c) = pack8(og);
         *reinterpret_cast<tg_u32x4 *>(du + r * lddg + c) = pack8(ou);
-        if (h != nullptr) tg_store8h(h + r * ldh + c, pack8(oh), n, hvec != 0);
+        if (h != nullptr) tg_store8h(h + r * ldh + c, pack8(oh), n);
     }
 }
 
@@ -277,9 +274,8 @@ __global__ __launch_bounds__(kThreads) void glu_back_act8_kernel(
 hipError_t launch_pad_copy(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols, uint16_t *dst,
                            const int64_t *target, int64_t ignore, hipStream_t stream) {
     const int64_t cp = (cols + 7) / 8 * 8;
-    const int vec = aligned(src, 16) && ld % 8 == 0;
     hipLaunchKernelGGL(pad_copy_kernel, dim3(blocks_for(rows * (cp / 8))), dim3(kThreads), 0, stream, src, ld, rows,
-                       cols, cp, dst, target, ignore, vec);
+                       cols, cp, dst, target, ignore);
     return hipGetLastError();
 }
 
@@ -290,17 +286,15 @@ hipError_t launch_fill_zero(uint16_t *dst, int64_t ld, int64_t rows, int64_t col
 
 hipError_t launch_act8_pack(const uint16_t *x, int64_t ld, int64_t rows, int64_t cols, uint8_t *q, uint8_t *scale,
                             hipStream_t stream) {
-    const int xvec = aligned(x, 16) && ld % 8 == 0, qvec = aligned(q, 8) && cols % 8 == 0;
     hipLaunchKernelGGL(act8_pack_kernel, dim3(blocks_for(rows * ((cols + 31) / 32) * 4)), dim3(kThreads), 0, stream, x,
-                       ld, rows, cols, q, scale, xvec, qvec);
+                       ld, rows, cols, q, scale);
     return hipGetLastError();
 }
 
 hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols, uint16_t *x,
                               int64_t ld, int64_t cols_out, hipStream_t stream) {
-    const int xvec = aligned(x, 16) && ld % 8 == 0, qvec = aligned(q, 8) && cols % 8 == 0;
     hipLaunchKernelGGL(act8_unpack_kernel, dim3(blocks_for(rows * ((cols_out + 7) / 8))), dim3(kThreads), 0, stream, q,
-                       scale, rows, cols, x, ld, cols_out, qvec, xvec);
+                       scale, rows, cols, x, ld, cols_out);
     return hipGetLastError();
 }
 
@@ -335,10 +329,8 @@ hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t 
 hipError_t launch_glu_back_act8(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, const uint8_t *us,
                                 const uint16_t *dh, int64_t lddh, int64_t rows, int64_t F, int32_t act, uint16_t *dg,
                                 uint16_t *du, int64_t lddg, uint16_t *h, int64_t ldh, hipStream_t stream) {
-    const int qvec = aligned(g8, 8) && aligned(u8, 8) && F % 8 == 0, dhvec = aligned(dh, 16) && lddh % 8 == 0;
-    const int hvec = aligned(h, 16) && ldh % 8 == 0;
     hipLaunchKernelGGL(glu_back_act8_kernel, dim3(blocks_for(rows * ((F + 7) / 8))), dim3(kThreads), 0, stream, g8, gs,
-                       u8, us, dh, lddh, rows, F, act, dg, du, lddg, h, ldh, qvec, dhvec, hvec);
+                       u8, us, dh, lddh, rows, F, act, dg, du, lddg, h, ldh);
     return hipGetLastError();
 }
 

@@ -175,9 +175,9 @@ def test_no_rows():
 
 
 def test_pieces_equal_one_piece():
-    """More rows than one piece of exponentials holds: the row losses of the
-    pieces' own calls, and dx and dw within the roundings of another order of
-    summation (how a product is divided depends on its sizes)."""
+    """More rows than one piece of exponentials holds: the pieces' own calls
+    give the same within the roundings of another order of summation (how a
+    product is divided depends on its sizes)."""
     t, d, v = 20_000, 64, 131_072
     g = torch.Generator(device=DEV).manual_seed(9)
     x = torch.randn((t, d), generator=g, device=DEV).to(torch.bfloat16)
@@ -185,9 +185,11 @@ def test_pieces_equal_one_piece():
     y = torch.randint(0, v, (t,), generator=g, device=DEV)
     loss, row, dx, dw = z.linear_xent_grad(x, w, y, mean=False)
     parts = [z.linear_xent_grad(x[a:a + 5000], w, y[a:a + 5000], mean=False) for a in range(0, t, 5000)]
-    assert torch.equal(row, torch.cat([p[1] for p in parts]))
     for k, p in enumerate(parts):
         rows = slice(5000 * k, 5000 * (k + 1))
+        size = (x[rows].float().abs() @ w.float().abs().t()).amax(1).double()  # of a row's logits
+        order = 4 * 1.01 * d * HALF_F32 * size + 2.0 ** -20 * (size + math.log(v) + 1)
+        inside(row[rows], p[1].double(), order, f"row_loss of piece {k}")
         terms = torch.softmax(x[rows].float() @ w.float().t(), 1) @ w.float().abs() + w[y[rows]].float().abs()
         order = 2 * 1.01 * v * HALF_F32 * terms.double()
         bound = HALF_BF16 * (dx[rows].double().abs() + p[2].double().abs()) + order
