@@ -63,17 +63,51 @@ __device__ __forceinline__ void tile_at(int t, int tm, int tn, int &ti, int &tj)
     ti = r0 + q0 + t % hh;
 }
 
+// v of the lanes (c, q), (c, q ^ 1) and (c, q), (c, q ^ 2): the two values, in
+// one order on both sides, by gfx950's row and half exchanges
+struct Pair {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Pair across16(uint32_t v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return {r[0], r[1]};
+}
+__device__ __forceinline__ Pair across32(uint32_t v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return {r[0], r[1]};
+}
+// maximum / sum over the four lanes of a row (q = 0 .. 3)
+__device__ __forceinline__ float quad_max(float v) {
+    Pair p = across16(__float_as_uint(v));
+    v = fmaxf(__uint_as_float(p.a), __uint_as_float(p.b));
+    p = across32(__float_as_uint(v));
+    return fmaxf(__uint_as_float(p.a), __uint_as_float(p.b));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    Pair p = across16(__float_as_uint(v));
+    v = __uint_as_float(p.a) + __uint_as_float(p.b);
+    p = across32(__float_as_uint(v));
+    return __uint_as_float(p.a) + __uint_as_float(p.b);
+}
+__device__ __forceinline__ uint32_t quad_umax(uint32_t v) {
+    Pair p = across16(v);
+    v = p.a > p.b ? p.a : p.b;
+    p = across32(v);
+    return p.a > p.b ? p.a : p.b;
+}
+
 // Row statistics and exponentials of a logits tile.  A wave's 64 columns are
 // one statistics group: m = their largest logit, s = the sum of exp(z - m),
 // and e = exp(z - m) in (0, 1] kept in fp16 (11 bits; what is lost below
 // 2^-14 is under 2^-25 of the group's largest).  exp(z - m) is taken as
 // 2^(z log2 e - m log2 e) in one multiply-add, off by 2^-24 of |m| log2 e.
+// target: those of the lane's rows, or -1 (a column that does not exist).
 template <int FM>
-__device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0) {
+__device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0,
+                                              const int (&target)[FM]) {
     const int lane = lane_id(), c = lane & 15, q = lane >> 4;
     if (C0 >= L.N) return;  // (lde - N < 64: no column of e lies in a group past N's last)
     float2 *stats = L.stats + (int64_t)(C0 / kXentGroup) * L.ldstat + R0 + c;
-    const int64_t *target = L.target + R0 + c;
     uint16_t *e = L.e + (int64_t)(R0 + c) * L.lde + C0 + q * 8;
     const int rows = L.M - R0 - c, cols = L.N - C0 - q * 8;
     const bool whole = C0 + 64 <= L.N, keep = L.e != nullptr;
@@ -90,14 +124,12 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
         float m = z[0];
 #pragma unroll
         for (int k = 1; k < 16; ++k) m = fmaxf(m, z[k]);
-        m = fmaxf(m, __shfl_xor(m, 16));
-        m = fmaxf(m, __shfl_xor(m, 32));
+        m = quad_max(m);
         const bool live = i * 16 < rows;
         // the target's logit, where it is one of this lane's columns
-        int64_t rel = -1;
-        if (live) rel = *target - C0 - q * 8;
-        if (rel >= 0 && rel < 40 && (rel & 31) < 8) {
-            const int at = (int)((rel >> 5) * 8 + (rel & 7));
+        const int rel = target[i] - C0 - q * 8;
+        if (live && (rel & ~39) == 0) {
+            const int at = (rel >> 5) * 8 + (rel & 7);
             float v = z[0];
 #pragma unroll
             for (int k = 1; k < 16; ++k) v = at == k ? z[k] : v;
@@ -111,8 +143,7 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
             z[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[k], kLog2e, -ref));
             s += z[k];
         }
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
+        s = quad_sum(s);
         if (live) {
             if (q == 0) *stats = make_float2(m, s);
             if (keep) {
@@ -124,7 +155,6 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
             }
         }
         stats += 16;
-        target += 16;
         e += 16 * L.lde;
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -153,11 +183,7 @@ __device__ __forceinline__ void act8_store(const float (&v)[8], int n, uint8_t *
         const uint32_t b = __float_as_uint(v[k]) & 0x7FFFFFFFu;
         big = k < n && b > big ? b : big;
     }
-    uint32_t o = __shfl_xor(big, 16);
-    big = o > big ? o : big;
-    o = __shfl_xor(big, 32);
-    big = o > big ? o : big;
-    const uint32_t byte = tg_scale_byte(big);
+    const uint32_t byte = tg_scale_byte(quad_umax(big));
     if (!live) return;
     if (n > 0) tg_store8b(qrow + col, tg_pack_e4m3(v, byte), n);
     if (q == 0) srow[col >> 5] = (uint8_t)byte;
@@ -173,6 +199,18 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
     const int col = C0 + q * 8;
     const int n = F - col > 8 ? 8 : F - col < 0 ? 0 : F - col;
     const int64_t blocks = (F + 31) / 32;
+    // (dh is read three row blocks ahead of the stores: loads and stores are
+    // counted in order, so a load behind a store waits for it)
+    constexpr int kAhead = 3;
+    tg_u32x4 ahead[kAhead];
+    auto fetch = [&](int i) __attribute__((always_inline)) {
+        const int row = R0 + i * 16 + c;
+        if (i < FM && row < L.M && n > 0) ahead[i % kAhead] = tg_load8h(L.dh + (int64_t)row * L.lddh + col, n);
+    };
+    if constexpr (BACK) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch(i);
+    }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int row = R0 + i * 16 + c;
@@ -194,7 +232,8 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
         } else {
             if (live && n > 0) {
                 float dh[8], dg[8], du[8];
-                unpack8(tg_load8h(L.dh + (int64_t)row * L.lddh + col, n), dh);
+                unpack8(ahead[i % kAhead], dh);
+                fetch(i + kAhead);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const TgActValue a = tg_act(g[k], L.act);
@@ -208,6 +247,7 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
                 if (L.h != nullptr) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n);
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
@@ -225,52 +265,57 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
     const bool in = L.sum_in != 0;
     float *s = P.sum + (int64_t)(R0 + c) * L.ldsum + first;  // (rows of fp32 sums are padded to a multiple of 4)
     const int64_t sstep = 16 * L.ldsum;
-    auto sum = [&](int i, int j) __attribute__((always_inline)) {
-        tg_f32x4 v = acc[i][j];
-        if (in) v += *reinterpret_cast<const tg_f32x4 *>(s + at(j));
-        return v;
-    };
     uint16_t *o = P.out + (int64_t)(R0 + c) * L.ldc + first;
     const int64_t step = 16 * L.ldc;
-    if (L.sum_out) {
+    // the earlier sums are read a row block ahead of the stores: loads and
+    // stores are counted in order, so a load behind a store waits for it
+    tg_f32x4 ahead[FN];
+    auto fetch = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
+        for (int j = 0; j < FN; ++j)
+            if (i < FM && i * 16 < rows && at(j) < cols)
+                ahead[j] = *reinterpret_cast<const tg_f32x4 *>(s + i * sstep + at(j));
+    };
+    if (in) fetch(0);
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-                if (i * 16 < rows && at(j) < cols) *reinterpret_cast<tg_f32x4 *>(s + at(j)) = sum(i, j);
-            s += sstep;
-            __builtin_amdgcn_sched_barrier(0);
+    for (int i = 0; i < FM; ++i) {
+        tg_f32x4 v[FN];
+#pragma unroll
+        for (int j = 0; j < FN; ++j) v[j] = acc[i][j];
+        if (in) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) v[j] += ahead[j];
+            fetch(i + 1);
         }
-    } else {
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if (i * 16 < rows && at(j) < cols) {
-                    const tg_f32x4 v = sum(i, j) * alpha;
-                    const tg_u32x2 p{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3])};
-                    if (at(j) + 4 <= cols) {
-                        tg_store(o + at(j), p);
-                    } else {
-                        o[at(j)] = (uint16_t)p.x;
-                        if (at(j) + 1 < cols) o[at(j) + 1] = (uint16_t)(p.x >> 16);
-                        if (at(j) + 2 < cols) o[at(j) + 2] = (uint16_t)p.y;
-                    }
-                }
+        for (int j = 0; j < FN; ++j) {
+            if (i * 16 >= rows || at(j) >= cols) continue;
+            if (L.sum_out) {
+                *reinterpret_cast<tg_f32x4 *>(s + i * sstep + at(j)) = v[j];
+                continue;
             }
-            o += step;
-            s += sstep;
-            __builtin_amdgcn_sched_barrier(0);
+            v[j] *= alpha;
+            const tg_u32x2 p{tg_pack_bf16(v[j][0], v[j][1]), tg_pack_bf16(v[j][2], v[j][3])};
+            if (at(j) + 4 <= cols) {
+                tg_store(o + at(j), p);
+            } else {
+                o[at(j)] = (uint16_t)p.x;
+                if (at(j) + 1 < cols) o[at(j) + 1] = (uint16_t)(p.x >> 16);
+                if (at(j) + 2 < cols) o[at(j) + 2] = (uint16_t)p.y;
+            }
         }
+        o += step;
+        __builtin_amdgcn_sched_barrier(0);
     }
 }
 
 // What becomes of a wave's sums, BM / WR rows from R0 and 64 columns (32 of
 // the gate and of the up projection) from C0 on.
 template <int EPI, bool BKM, int FM>
-__device__ __forceinline__ void finish(const TgLaunch &L, int prob, tg_f32x4 (&acc)[FM][4], int R0, int C0) {
+__device__ __forceinline__ void finish(const TgLaunch &L, int prob, tg_f32x4 (&acc)[FM][4], int R0, int C0,
+                                       const int (&target)[FM]) {
     if constexpr (EPI == kTgXent)
-        xent_epilogue<FM>(L, acc, R0, C0);
+        xent_epilogue<FM>(L, acc, R0, C0, target);
     else if constexpr (EPI == kTgGlu || EPI == kTgGluBack)
         glu_epilogue<FM, EPI == kTgGluBack>(L, acc, R0, C0);
     else
@@ -348,7 +393,10 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     static_assert(!GLU || NW % 4 == 0, "a wave loads rows of the gate or of the up projection");
     constexpr int BO = GLU ? BN / 2 : BN;  // output columns of a tile
     constexpr int kOut = 0x7FFFFFF0;       // a byte offset past every descriptor
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * STAGE];
+    // exponentials: the targets of a tile's rows, of this tile and the next
+    constexpr bool XENT = EPI == kTgXent;
+    constexpr int TGB = XENT ? (BM * 8 < 1024 ? 1024 : BM * 8) : 0;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[kStages * STAGE + 2 * TGB];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -576,9 +624,41 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         cur = nxt;
     };
 
+    // the targets of a tile's rows, 128 a wave instruction, straight to LDS
+    auto load_targets = [&](const Tile &T, int which) __attribute__((always_inline)) {
+        if constexpr (XENT) {
+            if (wave * 128 < BM) {
+                const int left = (L.M - T.m0 < BM ? L.M - T.m0 : BM) * 8;
+                const __amdgpu_buffer_rsrc_t rt = __builtin_amdgcn_make_buffer_rsrc(
+                    (void *)(L.target + T.m0), (short)0, left, 0x00020000);
+                const int off = (wave * 64 + lane_id()) * 16;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rt, LDS_ADDR(&lds[kStages * STAGE + which * TGB + wave * 1024]), 16, off, 0, 0, 0);
+            }
+        }
+    };
+    int which = 0;
+    // ... and read back, those of the lane's rows; outside 0 .. 2^31 - 1: -1
+    auto read_targets = [&](int (&target)[FM]) __attribute__((always_inline)) {
+        if constexpr (XENT) {
+            const uint32_t at = lds_base + kStages * STAGE + which * TGB + (wr * WTM + (lane_id() & 15)) * 8;
+            tg_u32x2 v[FM];
+#pragma unroll
+            for (int i = 0; i < FM; ++i)
+                asm volatile("ds_read_b64 %0, %1 offset:%2" : "=v"(v[i]) : "v"(at), "i"(i * 128));
+            __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0(63));
+#pragma unroll
+            for (int i = 0; i < FM; ++i) {
+                asm volatile("" : "+v"(v[i]));
+                target[i] = v[i].y == 0 ? (int)v[i].x : -1;
+            }
+        }
+    };
+
     Tile cu, nx{};
     int slot = seek(blockIdx.x, cu);
     if (slot < 0) return;
+    load_targets(cu, 0);
     stream(cu, true);
 #pragma unroll
     for (int s = 0; s < kStages; ++s) {
@@ -606,15 +686,22 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         // first ones, or zeros)
 #pragma clang loop unroll(disable)
         for (int kt = cu.stages; kt > 0; kt -= 2) {
+            // (past this tile's first barrier: nobody reads the last tile's
+            // targets any more, whose buffer takes the next one's)
+            if (XENT && more && kt == cu.stages - 2) load_targets(nx, which ^ 1);
             if (kStages % 2 == 0 && kt == kStages) stream(more ? nx : cu, more);
             body(std::integral_constant<int, 0>{});
             if (kStages % 2 == 1 && kt == kStages + 1) stream(more ? nx : cu, more);
             body(std::integral_constant<int, 1>{});
         }
-        if (cu.split >= 0)
+        if (cu.split >= 0) {
             keep_part<FM, NW>(L, cu.t - L.whole, cu.split, wave, acc);
-        else
-            finish<EPI, BKM, FM>(L, cu.prob, acc, cu.m0 + wr * WTM, cu.n0 + wc * (GLU ? 32 : 64));
+        } else {
+            int target[FM];
+            read_targets(target);
+            finish<EPI, BKM, FM>(L, cu.prob, acc, cu.m0 + wr * WTM, cu.n0 + wc * (GLU ? 32 : 64), target);
+        }
+        which ^= 1;
         if (!more) break;
         cu = nx;
         slot = nslot;
@@ -649,8 +736,17 @@ __global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64) void tg_join_ker
     const int t = L.whole + blockIdx.x, per = L.tiles_m * L.tiles_n, prob = t >= per ? 1 : 0;
     int ti, tj;
     tile_at(t - prob * per, L.tiles_m, L.tiles_n, ti, tj);
-    finish<EPI, BKM, FM>(L, prob, acc, ti * C::BM + (wave / C::WC) * WTM,
-                         tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64));
+    const int R0 = ti * C::BM + (wave / C::WC) * WTM;
+    int target[FM];
+    if constexpr (EPI == kTgXent) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+            const int row = R0 + i * 16 + (lane & 15);
+            const int64_t v = row < L.M ? L.target[row] : -1;
+            target[i] = v >= 0 && v <= 0x7FFFFFFF ? (int)v : -1;
+        }
+    }
+    finish<EPI, BKM, FM>(L, prob, acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
 }
 
 // Compute units of the current device (asked for once), a multiple of the 8
