@@ -620,7 +620,8 @@ zopt_status zopt_set_ns_form(int32_t form);
  * workspace: device scratch, 256-byte aligned, of at least the size that the
  * call with workspace == NULL writes to *workspace_bytes.  That size depends
  * on the sizes, strides, the alignment of the operands and which optional
- * pointers are NULL, so query with the arguments of the call.
+ * pointers are NULL, so query with the arguments of the call.  Where it is 0
+ * the workspace is not touched: any non-NULL, aligned value will do.
  */
 
 /*

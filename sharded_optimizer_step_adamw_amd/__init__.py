@@ -635,6 +635,9 @@ def _sized(fn, args, where, on, workspace):
     size = ctypes.c_size_t(0)
     if workspace is None:
         _check(fn(*args, None, ctypes.byref(size), None), where)
+        if size.value == 0:  # any address will do
+            _check(fn(*args, 256, ctypes.byref(size), on.handle), where)
+            return
         workspace = on.empty(size.value, torch.uint8)
     else:
         _need(workspace, torch.uint8, 0, "workspace", on.device)

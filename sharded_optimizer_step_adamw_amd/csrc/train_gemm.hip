@@ -148,10 +148,19 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
             if (q == 0) *stats = make_float2(m, s);
             if (keep) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    *reinterpret_cast<tg_u32x4 *>(e + h * 32) =
-                        tg_u32x4{tg_pack_f16(z[8 * h], z[8 * h + 1]), tg_pack_f16(z[8 * h + 2], z[8 * h + 3]),
-                                 tg_pack_f16(z[8 * h + 4], z[8 * h + 5]), tg_pack_f16(z[8 * h + 6], z[8 * h + 7])};
+                for (int h = 0; h < 2; ++h) {
+                    const tg_u32x4 p{tg_pack_f16(z[8 * h], z[8 * h + 1]), tg_pack_f16(z[8 * h + 2], z[8 * h + 3]),
+                                     tg_pack_f16(z[8 * h + 4], z[8 * h + 5]), tg_pack_f16(z[8 * h + 6], z[8 * h + 7])};
+                    // (the markers keep the two from being merged into one
+                    // ordinary store)
+                    if (L.past) {
+                        asm volatile("; past the caches");
+                        tg_store<true>(e + h * 32, p);
+                        asm volatile("; past the caches");
+                    } else {
+                        tg_store<false>(e + h * 32, p);
+                    }
+                }
             }
         }
         stats += 16;
@@ -201,7 +210,7 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
     const int64_t blocks = (F + 31) / 32;
     // (dh is read three row blocks ahead of the stores: loads and stores are
     // counted in order, so a load behind a store waits for it)
-    constexpr int kAhead = 3;
+    constexpr int kAhead = FM < 3 ? FM : 3;
     tg_u32x4 ahead[kAhead];
     auto fetch = [&](int i) __attribute__((always_inline)) {
         const int row = R0 + i * 16 + c;
@@ -711,42 +720,40 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
 }
 
 // The tiles that were split: their parts' sums, added in order, and then what
-// the whole tiles' workgroups do.  One workgroup a tile.
+// the whole tiles' workgroups do.  A wave takes 16 rows of what one wave of
+// the tile held (four a workgroup, each on its own), so that few tiles still
+// fill the GPU.
 template <int TILE, int EPI, bool BKM>
-__global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64) void tg_join_kernel(TgLaunch L) {
+__global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
     using C = Cfg<TILE>;
     constexpr int NW = C::WR * C::WC, WTM = C::BM / C::WR, FM = WTM / 16;
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int lane = threadIdx.x & 63;
+    const int id = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    const int rt = id / (NW * FM), wave = id / FM % NW, i = id % FM;
+    if (rt >= L.tiles - L.whole) return;
     const tg_f32x4 *p = reinterpret_cast<const tg_f32x4 *>(L.part) +
-                        ((int64_t)blockIdx.x * L.splits * NW + wave) * (FM * 4 * 64) + lane;
-    tg_f32x4 acc[FM][4];
+                        (((int64_t)rt * L.splits * NW + wave) * FM + i) * (4 * 64) + lane;
+    tg_f32x4 acc[1][4];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = p[(i * 4 + j) * 64];
-#pragma clang loop unroll(disable)
+    for (int j = 0; j < 4; ++j) acc[0][j] = p[j * 64];
+#pragma unroll 4
     for (int s = 1; s < L.splits; ++s) {
-        p += (int64_t)NW * (FM * 4 * 64);
+        p += (int64_t)NW * FM * (4 * 64);
 #pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] += p[(i * 4 + j) * 64];
+        for (int j = 0; j < 4; ++j) acc[0][j] += p[j * 64];
     }
-    const int t = L.whole + blockIdx.x, per = L.tiles_m * L.tiles_n, prob = t >= per ? 1 : 0;
+    const int t = L.whole + rt, per = L.tiles_m * L.tiles_n, prob = t >= per ? 1 : 0;
     int ti, tj;
     tile_at(t - prob * per, L.tiles_m, L.tiles_n, ti, tj);
-    const int R0 = ti * C::BM + (wave / C::WC) * WTM;
-    int target[FM];
+    const int R0 = ti * C::BM + (wave / C::WC) * WTM + i * 16;
+    int target[1] = {-1};
     if constexpr (EPI == kTgXent) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i) {
-            const int row = R0 + i * 16 + (lane & 15);
-            const int64_t v = row < L.M ? L.target[row] : -1;
-            target[i] = v >= 0 && v <= 0x7FFFFFFF ? (int)v : -1;
-        }
+        const int row = R0 + (lane & 15);
+        const int64_t v = row < L.M ? L.target[row] : -1;
+        if (v >= 0 && v <= 0x7FFFFFFF) target[0] = (int)v;
     }
-    finish<EPI, BKM, FM>(L, prob, acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
+    finish<EPI, BKM, 1>(L, prob, acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
 }
 
 // Compute units of the current device (asked for once), a multiple of the 8
@@ -780,8 +787,8 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
     hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM>), dim3(grid), dim3(threads), 0, stream, L);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && L.splits > 1) {
-        hipLaunchKernelGGL((tg_join_kernel<TILE, EPI, BKM>), dim3((uint32_t)(tiles - L.whole)), dim3(threads), 0,
-                           stream, L);
+        const int64_t waves = (tiles - L.whole) * (C::BM / 16) * C::WC;
+        hipLaunchKernelGGL((tg_join_kernel<TILE, EPI, BKM>), dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, stream, L);
         e = hipGetLastError();
     }
     return e;
@@ -826,7 +833,11 @@ void plan_tg(TgEpilogue epi, TgLaunch &L) {
         const int64_t tiles = (L.M + f.bm - 1) / f.bm * ((L.N + bn - 1) / bn) * L.nprob;
         const int64_t rounds = tiles / held, rest = tiles % held;
         const double each = epi == kTgStore ? f.plain : f.heavy;
-        auto load = [&](int64_t n) { return f.alone > n * f.full ? f.alone : n * f.full; };
+        auto load = [&](int64_t n) {
+            // (one on each of few CUs is not held up by the others)
+            const bool few = n == 1 && (f.held > 1 || tiles < cus / 2);
+            return few || f.alone > n * f.full ? f.alone : n * f.full;
+        };
         const double whole = rounds * (all * load(f.held) + each);
         for (int split = 1; split <= 32; ++split) {
             const int per = (all + split - 1) / split;

@@ -64,6 +64,7 @@ struct TgLaunch {
     // target's logit to zt
     uint16_t *e;
     int64_t lde;
+    int32_t past;             // e is written past the caches
     float2 *stats;
     int64_t ldstat;
     const int64_t *target;
@@ -91,23 +92,49 @@ hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStrea
 
 // ------------------------------------------------------------- row passes
 
-// dst [rows, round8(cols)] = src [rows, cols], zero beyond cols and in rows
-// whose target is `ignore` (target NULL: none).
-hipError_t launch_pad_copy(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols,
-                           uint16_t *dst, const int64_t *target, int64_t ignore,
-                           hipStream_t stream);
+// The memory-side cache of 256 MiB serves a pass what the pass before wrote if
+// that fits it.  Where a matrix does not, or would push out what the next
+// pass needs, its accesses go past the caches.
+constexpr int64_t kCacheBytes = (int64_t)256 << 20;
+
+// What a call does to its operands before its products, all in one launch:
+//   kPrepCopy    dst [rows, round8(cols)] = src [rows, cols] (row stride ld), zero
+//                beyond cols and in rows whose target is `ignore` (target NULL: none)
+//   kPrepUnpack  dst [rows, round8(cols)] = the values of the checkpoint q, scale
+//   kPrepBack    dst = dg, dst2 = du (row stride dst_ld, zero in columns [cols,
+//                round8(cols))) and h (or NULL, row stride h_ld) from the
+//                checkpoint q, scale of g and q2, scale2 of u and from src = dh
+//   kPrepCount   *factor = grad_scale, or (mean) grad_scale / rows that take part (0
+//                if none)
+enum TgPrepKind : int { kPrepCopy = 0, kPrepUnpack = 1, kPrepBack = 2, kPrepCount = 3 };
+struct TgPrep {
+    int32_t kind, act, mean;
+    uint32_t blocks;          // set by the launch
+    int64_t rows, cols;
+    const uint16_t *src;
+    int64_t ld;
+    const uint8_t *q, *scale, *q2, *scale2;
+    uint16_t *dst, *dst2, *h;
+    int64_t dst_ld, h_ld;
+    const int64_t *target;
+    int64_t ignore;
+    float grad_scale;
+    float *factor;
+};
+constexpr int kMaxPreps = 4;
+struct TgPrepList {
+    TgPrep job[kMaxPreps];
+    int32_t n;
+};
+hipError_t launch_prep(TgPrepList &list, hipStream_t stream);
 hipError_t launch_fill_zero(uint16_t *dst, int64_t ld, int64_t rows, int64_t cols,
                             hipStream_t stream);
 
 hipError_t launch_act8_pack(const uint16_t *x, int64_t ld, int64_t rows, int64_t cols, uint8_t *q,
                             uint8_t *scale, hipStream_t stream);
-// columns [cols, cols_out) are written as zero
 hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
-                              uint16_t *x, int64_t ld, int64_t cols_out, hipStream_t stream);
+                              uint16_t *x, int64_t ld, hipStream_t stream);
 
-// *factor = grad_scale, or grad_scale / rows that take part (0 if none)
-hipError_t launch_xent_count(const int64_t *target, int64_t rows, int64_t ignore, int32_t mean,
-                             float grad_scale, float *factor, hipStream_t stream);
 // lse and row loss of rows [0, rows) from the group statistics
 hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups,
                            const int64_t *target, int64_t ignore, int32_t V, const float *zt,
@@ -115,17 +142,10 @@ hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups,
 // e (fp16 exponentials) -> P = softmax - onehot (bf16), in place, columns [V, lde) zero
 hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V,
                              const float2 *stats, int64_t ldstat, const float *lse,
-                             const float *row_loss, const int64_t *target, int64_t ignore,
+                             const float *row_loss, const int64_t *target, int64_t ignore, int32_t past,
                              hipStream_t stream);
 hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t *target,
                              int64_t ignore, int32_t mean, float *loss, hipStream_t stream);
-
-// dg, du (row stride lddg, zero in columns [F, round8(F))) and h (or NULL)
-// from a checkpoint of g and u and from dh
-hipError_t launch_glu_back_act8(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8,
-                                const uint8_t *us, const uint16_t *dh, int64_t lddh, int64_t rows,
-                                int64_t F, int32_t act, uint16_t *dg, uint16_t *du, int64_t lddg,
-                                uint16_t *h, int64_t ldh, hipStream_t stream);
 
 // ---------------------------------------------------------- device helpers
 
@@ -220,6 +240,24 @@ template <class V>
 __device__ __forceinline__ void tg_store(void *p, V v) {
     __builtin_memcpy(p, &v, sizeof v);
 }
+// ... past the caches (PAST), for data that is not met again before the
+// memory-side cache has seen more than it holds
+template <class V, bool PAST>
+__device__ __forceinline__ V tg_load(const void *p) {
+    typedef V U __attribute__((aligned(1)));
+    if constexpr (PAST)
+        return __builtin_nontemporal_load(reinterpret_cast<const U *>(p));
+    else
+        return tg_load<V>(p);
+}
+template <bool PAST, class V>
+__device__ __forceinline__ void tg_store(void *p, V v) {
+    typedef V U __attribute__((aligned(1)));
+    if constexpr (PAST)
+        __builtin_nontemporal_store(v, reinterpret_cast<U *>(p));
+    else
+        tg_store(p, v);
+}
 // up to 8 bytes / 16-bit values at p, of which the first n exist
 __device__ __forceinline__ tg_u32x2 tg_load8b(const uint8_t *p, int n) {
     if (n >= 8) return tg_load<tg_u32x2>(p);
@@ -239,17 +277,19 @@ __device__ __forceinline__ void tg_store8b(uint8_t *p, tg_u32x2 v, int n) {
     for (int k = 0; k < 8; ++k)
         if (k < n) p[k] = (uint8_t)((k < 4 ? v.x >> (8 * k) : v.y >> (8 * (k - 4))) & 0xFFu);
 }
+template <bool PAST = false>
 __device__ __forceinline__ tg_u32x4 tg_load8h(const uint16_t *p, int n) {
-    if (n >= 8) return tg_load<tg_u32x4>(p);
+    if (n >= 8) return tg_load<tg_u32x4, PAST>(p);
     tg_u32x4 r{0, 0, 0, 0};
 #pragma unroll
     for (int k = 0; k < 8; ++k)
         if (k < n) r[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
     return r;
 }
+template <bool PAST = false>
 __device__ __forceinline__ void tg_store8h(uint16_t *p, tg_u32x4 v, int n) {
     if (n >= 8) {
-        tg_store(p, v);
+        tg_store<PAST>(p, v);
         return;
     }
 #pragma unroll

@@ -16,6 +16,12 @@ uint32_t blocks_for(int64_t n) {
     return (uint32_t)(b < 1 ? 1 : b > (1 << 20) ? (1 << 20) : b);
 }
 
+// The 16-bit side of an 8-bit checkpoint goes past the caches where it fills
+// more than half of the memory-side one, and leaves that to the 8-bit side: a
+// [8192, 14336] matrix packed and read back takes 120 us so, 139 us otherwise
+// (a [8192, 4096] one 41 and 39).
+bool past_half(int64_t bytes) { return bytes > kCacheBytes / 2; }
+
 __device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -26,23 +32,6 @@ __device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
 __device__ __forceinline__ tg_u32x4 pack8(const float (&v)[8]) {
     return tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
                     tg_pack_bf16(v[6], v[7])};
-}
-
-// dst [rows, cp] = src [rows, cols], zero in [cols, cp) and in rows whose
-// target is the ignored one (target != NULL); one thread an eight
-__global__ __launch_bounds__(kThreads) void pad_copy_kernel(const uint16_t *__restrict__ src, int64_t ld,
-                                                            int64_t rows, int64_t cols, int64_t cp,
-                                                            uint16_t *__restrict__ dst,
-                                                            const int64_t *__restrict__ target, int64_t ignore) {
-    const int64_t per = cp / 8, total = rows * per;
-    for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = id / per, c = (id - r * per) * 8;
-        const int64_t left = cols - c;
-        tg_u32x4 v{0, 0, 0, 0};
-        if (target == nullptr || target[r] != ignore)
-            v = tg_load8h(src + r * ld + c, left > 8 ? 8 : (int)left);
-        *reinterpret_cast<tg_u32x4 *>(dst + r * cp + c) = v;
-    }
 }
 
 __global__ __launch_bounds__(kThreads) void fill_zero_kernel(uint16_t *__restrict__ dst, int64_t ld, int64_t rows,
@@ -56,6 +45,7 @@ __global__ __launch_bounds__(kThreads) void fill_zero_kernel(uint16_t *__restric
 
 // 8-bit checkpoints: four neighbouring threads hold a block of 32 values,
 // eight each.
+template <bool PAST>
 __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__restrict__ x, int64_t ld, int64_t rows,
                                                              int64_t cols, uint8_t *__restrict__ q,
                                                              uint8_t *__restrict__ scale) {
@@ -66,7 +56,7 @@ __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__r
         const int64_t c = cb * 32 + (id & 3) * 8, left = cols - c;
         const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
         tg_u32x4 p{0, 0, 0, 0};
-        if (n > 0) p = tg_load8h(x + r * ld + c, n);
+        if (n > 0) p = tg_load8h<PAST>(x + r * ld + c, n);
         float v[8];
         unpack8(p, v);
         uint32_t big = 0;
@@ -85,48 +75,43 @@ __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__r
     }
 }
 
+// eight values of row r from column c on
+__device__ __forceinline__ void act8_values(const uint8_t *q, const uint8_t *scale, int64_t r, int64_t c, int64_t cols,
+                                            int64_t blocks, int n, float (&v)[8]) {
+    tg_unpack_e4m3(tg_load8b(q + r * cols + c, n), tg_scale_out(scale[r * blocks + (c >> 5)]), v);
+}
+
+template <bool PAST>
 __global__ __launch_bounds__(kThreads) void act8_unpack_kernel(const uint8_t *__restrict__ q,
                                                                const uint8_t *__restrict__ scale, int64_t rows,
-                                                               int64_t cols, uint16_t *__restrict__ x, int64_t ld,
-                                                               int64_t cols_out) {
-    const int64_t blocks = (cols + 31) / 32, per = (cols_out + 7) / 8, total = rows * per;
+                                                               int64_t cols, uint16_t *__restrict__ x, int64_t ld) {
+    const int64_t blocks = (cols + 31) / 32, per = (cols + 7) / 8, total = rows * per;
     for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
         const int64_t r = id / per, c = (id - r * per) * 8;
-        const int64_t left = cols - c, lo = cols_out - c;
-        const int n = left > 8 ? 8 : left < 0 ? 0 : (int)left;
-        float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (n > 0) {
-            tg_unpack_e4m3(tg_load8b(q + r * cols + c, n), tg_scale_out(scale[r * blocks + (c >> 5)]), v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = k < n ? v[k] : 0.0f;
-        }
-        tg_store8h(x + r * ld + c, pack8(v), lo > 8 ? 8 : (int)lo);
+        const int n = cols - c > 8 ? 8 : (int)(cols - c);
+        float v[8];
+        act8_values(q, scale, r, c, cols, blocks, n, v);
+        tg_store8h<PAST>(x + r * ld + c, pack8(v), n);
     }
 }
 
-// The number of rows that take part, summed over a block of 1024 threads.
+// The number of rows that take part, summed over a block of N threads.
+template <int N>
 __device__ __forceinline__ long long valid_rows(const int64_t *__restrict__ target, int64_t rows, int64_t ignore) {
-    __shared__ long long part[16];
+    __shared__ long long part[N / 64];
     long long n = 0;
-    for (int64_t i = threadIdx.x; i < rows; i += 1024) n += target[i] != ignore ? 1 : 0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < rows; i += N) n += target[i] != ignore ? 1 : 0;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
     __syncthreads();
     long long all = 0;
-    for (int k = 0; k < 16; ++k) all += part[k];
+    for (int k = 0; k < N / 64; ++k) all += part[k];
     return all;
 }
 __device__ __forceinline__ double share_of(long long rows, int mean) {
     return !mean ? 1.0 : rows > 0 ? 1.0 / (double)rows : 0.0;
-}
-
-// the gradients' factor
-__global__ __launch_bounds__(1024) void xent_count_kernel(const int64_t *__restrict__ target, int64_t rows,
-                                                          int64_t ignore, int mean, float grad_scale,
-                                                          float *__restrict__ factor) {
-    const long long n = mean ? valid_rows(target, rows, ignore) : 0;
-    if (threadIdx.x == 0) *factor = (float)(share_of(n, mean) * (double)grad_scale);
 }
 
 // (m, s) of two sets of exponentials, s relative to exp(m)
@@ -191,6 +176,7 @@ __global__ __launch_bounds__(1024) void xent_lse_kernel(const float2 *__restrict
 // rows.  The target's own entry, softmax - 1, comes from the row's loss,
 // expm1(-row_loss): where the model is sure of the target the difference is
 // small, and e's 11 bits would be most of it.
+template <bool PAST>
 __global__ __launch_bounds__(kThreads) void xent_probs_kernel(uint16_t *__restrict__ e, int64_t lde, int64_t rows,
                                                               int V, const float2 *__restrict__ stats, int64_t ldstat,
                                                               const float *__restrict__ lse,
@@ -203,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void xent_probs_kernel(uint16_t *__restri
         const int64_t t = target[r];
         tg_u32x4 out{0, 0, 0, 0};
         if (t != ignore && c < V) {
-            const tg_u32x4 in = *p;
+            const tg_u32x4 in = tg_load<tg_u32x4, PAST>(p);
             const float f = expf(stats[(c / kXentGroup) * ldstat + r].x - lse[r]);
             const int64_t rel = t - c;
             float v[8];
@@ -220,7 +206,7 @@ __global__ __launch_bounds__(kThreads) void xent_probs_kernel(uint16_t *__restri
             }
             out = pack8(v);
         }
-        *p = out;
+        tg_store<PAST>(p, out);
     }
 }
 
@@ -229,7 +215,7 @@ __global__ __launch_bounds__(1024) void xent_total_kernel(const float *__restric
                                                           const int64_t *__restrict__ target, int64_t ignore,
                                                           int mean, float *__restrict__ loss) {
     __shared__ double part[16];
-    const long long n = mean ? valid_rows(target, rows, ignore) : 0;
+    const long long n = mean ? valid_rows<1024>(target, rows, ignore) : 0;
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < rows; i += 1024) s += (double)row_loss[i];
 #pragma unroll
@@ -243,39 +229,83 @@ __global__ __launch_bounds__(1024) void xent_total_kernel(const float *__restric
     }
 }
 
-// dg = dh u act'(g), du = dh act(g), h = act(g) u, eight columns a thread
-__global__ __launch_bounds__(kThreads) void glu_back_act8_kernel(
-    const uint8_t *__restrict__ g8, const uint8_t *__restrict__ gs, const uint8_t *__restrict__ u8,
-    const uint8_t *__restrict__ us, const uint16_t *__restrict__ dh, int64_t lddh, int64_t rows, int64_t F, int act,
-    uint16_t *__restrict__ dg, uint16_t *__restrict__ du, int64_t lddg, uint16_t *__restrict__ h, int64_t ldh) {
-    const int64_t blocks = (F + 31) / 32, per = (F + 7) / 8, total = rows * per;
-    for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
+// The jobs before a call's products, each on blocks of its own; eight columns
+// a thread.  One launch for all: each of them alone takes 3 to 5 us on small
+// operands, most of it a launch's.
+__device__ __forceinline__ void prep_copy(const TgPrep &j, int64_t block) {
+    const int64_t per = (j.cols + 7) / 8, total = j.rows * per;
+    for (int64_t id = block * kThreads + threadIdx.x; id < total; id += (int64_t)j.blocks * kThreads) {
+        const int64_t r = id / per, c = (id - r * per) * 8, left = j.cols - c;
+        tg_u32x4 v{0, 0, 0, 0};
+        if (j.target == nullptr || j.target[r] != j.ignore)
+            v = tg_load8h(j.src + r * j.ld + c, left > 8 ? 8 : (int)left);
+        *reinterpret_cast<tg_u32x4 *>(j.dst + id * 8) = v;
+    }
+}
+__device__ __forceinline__ void prep_unpack(const TgPrep &j, int64_t block) {
+    const int64_t blocks = (j.cols + 31) / 32, per = (j.cols + 7) / 8, total = j.rows * per;
+    for (int64_t id = block * kThreads + threadIdx.x; id < total; id += (int64_t)j.blocks * kThreads) {
         const int64_t r = id / per, c = (id - r * per) * 8;
-        const int n = F - c > 8 ? 8 : (int)(F - c);
+        const int n = j.cols - c > 8 ? 8 : (int)(j.cols - c);
+        float v[8];
+        act8_values(j.q, j.scale, r, c, j.cols, blocks, n, v);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < n ? v[k] : 0.0f;
+        *reinterpret_cast<tg_u32x4 *>(j.dst + id * 8) = pack8(v);
+    }
+}
+// dg = dh u act'(g), du = dh act(g), h = act(g) u
+__device__ __forceinline__ void prep_back(const TgPrep &j, int64_t block) {
+    const int64_t blocks = (j.cols + 31) / 32, per = (j.cols + 7) / 8, total = j.rows * per;
+    for (int64_t id = block * kThreads + threadIdx.x; id < total; id += (int64_t)j.blocks * kThreads) {
+        const int64_t r = id / per, c = (id - r * per) * 8;
+        const int n = j.cols - c > 8 ? 8 : (int)(j.cols - c);
         float g[8], u[8], d[8], og[8], ou[8], oh[8];
-        tg_unpack_e4m3(tg_load8b(g8 + r * F + c, n), tg_scale_out(gs[r * blocks + (c >> 5)]), g);
-        tg_unpack_e4m3(tg_load8b(u8 + r * F + c, n), tg_scale_out(us[r * blocks + (c >> 5)]), u);
-        unpack8(tg_load8h(dh + r * lddh + c, n), d);
+        act8_values(j.q, j.scale, r, c, j.cols, blocks, n, g);
+        act8_values(j.q2, j.scale2, r, c, j.cols, blocks, n, u);
+        unpack8(tg_load8h(j.src + r * j.ld + c, n), d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const TgActValue a = tg_act(g[k], act);
+            const TgActValue a = tg_act(g[k], j.act);
             og[k] = k < n ? d[k] * u[k] * a.da : 0.0f;
             ou[k] = k < n ? d[k] * a.a : 0.0f;
             oh[k] = a.a * u[k];
         }
-        *reinterpret_cast<tg_u32x4 *>(dg + r * lddg + c) = pack8(og);
-        *reinterpret_cast<tg_u32x4 *>(du + r * lddg + c) = pack8(ou);
-        if (h != nullptr) tg_store8h(h + r * ldh + c, pack8(oh), n);
+        *reinterpret_cast<tg_u32x4 *>(j.dst + r * j.dst_ld + c) = pack8(og);
+        *reinterpret_cast<tg_u32x4 *>(j.dst2 + r * j.dst_ld + c) = pack8(ou);
+        if (j.h != nullptr) tg_store8h(j.h + r * j.h_ld + c, pack8(oh), n);
     }
+}
+__device__ __forceinline__ void prep_count(const TgPrep &j) {
+    const long long n = j.mean ? valid_rows<kThreads>(j.target, j.rows, j.ignore) : 0;
+    if (threadIdx.x == 0) *j.factor = (float)(share_of(n, j.mean) * (double)j.grad_scale);
+}
+__global__ __launch_bounds__(kThreads) void prep_kernel(TgPrepList list) {
+    uint32_t block = blockIdx.x;
+    int k = 0;
+    while (k + 1 < list.n && block >= list.job[k].blocks) block -= list.job[k++].blocks;
+    const TgPrep &j = list.job[k];
+    if (j.kind == kPrepCopy)
+        prep_copy(j, block);
+    else if (j.kind == kPrepUnpack)
+        prep_unpack(j, block);
+    else if (j.kind == kPrepBack)
+        prep_back(j, block);
+    else
+        prep_count(j);
 }
 
 }  // namespace
 
-hipError_t launch_pad_copy(const uint16_t *src, int64_t ld, int64_t rows, int64_t cols, uint16_t *dst,
-                           const int64_t *target, int64_t ignore, hipStream_t stream) {
-    const int64_t cp = (cols + 7) / 8 * 8;
-    hipLaunchKernelGGL(pad_copy_kernel, dim3(blocks_for(rows * (cp / 8))), dim3(kThreads), 0, stream, src, ld, rows,
-                       cols, cp, dst, target, ignore);
+hipError_t launch_prep(TgPrepList &list, hipStream_t stream) {
+    if (list.n == 0) return hipSuccess;
+    uint32_t total = 0;
+    for (int k = 0; k < list.n; ++k) {
+        TgPrep &j = list.job[k];
+        j.blocks = j.kind == kPrepCount ? 1 : blocks_for(j.rows * ((j.cols + 7) / 8));
+        total += j.blocks;
+    }
+    hipLaunchKernelGGL(prep_kernel, dim3(total), dim3(kThreads), 0, stream, list);
     return hipGetLastError();
 }
 
@@ -286,22 +316,17 @@ hipError_t launch_fill_zero(uint16_t *dst, int64_t ld, int64_t rows, int64_t col
 
 hipError_t launch_act8_pack(const uint16_t *x, int64_t ld, int64_t rows, int64_t cols, uint8_t *q, uint8_t *scale,
                             hipStream_t stream) {
-    hipLaunchKernelGGL(act8_pack_kernel, dim3(blocks_for(rows * ((cols + 31) / 32) * 4)), dim3(kThreads), 0, stream, x,
-                       ld, rows, cols, q, scale);
+    const auto kernel = past_half(rows * cols * 2) ? act8_pack_kernel<true> : act8_pack_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3(blocks_for(rows * ((cols + 31) / 32) * 4)), dim3(kThreads), 0, stream, x, ld, rows,
+                       cols, q, scale);
     return hipGetLastError();
 }
 
 hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols, uint16_t *x,
-                              int64_t ld, int64_t cols_out, hipStream_t stream) {
-    hipLaunchKernelGGL(act8_unpack_kernel, dim3(blocks_for(rows * ((cols_out + 7) / 8))), dim3(kThreads), 0, stream, q,
-                       scale, rows, cols, x, ld, cols_out);
-    return hipGetLastError();
-}
-
-hipError_t launch_xent_count(const int64_t *target, int64_t rows, int64_t ignore, int32_t mean, float grad_scale,
-                             float *factor, hipStream_t stream) {
-    hipLaunchKernelGGL(xent_count_kernel, dim3(1), dim3(1024), 0, stream, target, rows, ignore, mean, grad_scale,
-                       factor);
+                              int64_t ld, hipStream_t stream) {
+    const auto kernel = past_half(rows * cols * 2) ? act8_unpack_kernel<true> : act8_unpack_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3(blocks_for(rows * ((cols + 7) / 8))), dim3(kThreads), 0, stream, q, scale, rows,
+                       cols, x, ld);
     return hipGetLastError();
 }
 
@@ -313,24 +338,17 @@ hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups, 
 }
 
 hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V, const float2 *stats, int64_t ldstat,
-                             const float *lse, const float *row_loss, const int64_t *target, int64_t ignore,
+                             const float *lse, const float *row_loss, const int64_t *target, int64_t ignore, int32_t past,
                              hipStream_t stream) {
-    hipLaunchKernelGGL(xent_probs_kernel, dim3(blocks_for(rows * (lde / 8))), dim3(kThreads), 0, stream, e, lde, rows,
-                       V, stats, ldstat, lse, row_loss, target, ignore);
+    const auto kernel = past ? xent_probs_kernel<true> : xent_probs_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3(blocks_for(rows * (lde / 8))), dim3(kThreads), 0, stream, e, lde, rows, V, stats,
+                       ldstat, lse, row_loss, target, ignore);
     return hipGetLastError();
 }
 
 hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t *target, int64_t ignore, int32_t mean,
                              float *loss, hipStream_t stream) {
     hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(1024), 0, stream, row_loss, rows, target, ignore, mean, loss);
-    return hipGetLastError();
-}
-
-hipError_t launch_glu_back_act8(const uint8_t *g8, const uint8_t *gs, const uint8_t *u8, const uint8_t *us,
-                                const uint16_t *dh, int64_t lddh, int64_t rows, int64_t F, int32_t act, uint16_t *dg,
-                                uint16_t *du, int64_t lddg, uint16_t *h, int64_t ldh, hipStream_t stream) {
-    hipLaunchKernelGGL(glu_back_act8_kernel, dim3(blocks_for(rows * ((F + 7) / 8))), dim3(kThreads), 0, stream, g8, gs,
-                       u8, us, dh, lddh, rows, F, act, dg, du, lddg, h, ldh);
     return hipGetLastError();
 }
 

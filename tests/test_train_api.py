@@ -78,8 +78,10 @@ def test_act8_pack_and_unpack_reject_and_empty_is_a_noop():
 def test_workspace_is_sized_and_checked(name, args):
     fn = getattr(z.lib(), name)
     st, need = call(fn, args.values(), ws=None, size=0)
-    assert st == z.ZOPT_OK and need >= 256 and need % 256 == 0
-    assert call(fn, args.values(), size=need - 1)[0] == z.ZOPT_ERR_WORKSPACE
+    assert st == z.ZOPT_OK and need % 256 == 0
+    assert (need == 0) == (name == "zopt_glu_forward")  # aligned operands, one launch
+    if need:
+        assert call(fn, args.values(), size=need - 1)[0] == z.ZOPT_ERR_WORKSPACE
     assert call(fn, args.values(), ws=FAKE + 128, size=need)[0] == z.ZOPT_ERR_WORKSPACE
     assert fn(*args.values(), FAKE, None, None) == NULL
 
