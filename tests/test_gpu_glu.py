@@ -32,7 +32,7 @@ def check_h(h, g, u, ge, ue, kind, what):
     a, _ = act(g, kind)
     ref = a * u
     b = 1.13 * ge * (u.abs() + ue) + a.abs() * ue + FAST * (a.abs() + g.abs() * 2.0 ** -4) * u.abs()
-    inside(h.cpu(), ref, HALF_BF16 * ref.abs() + 1.01 * b + 1e-38, what)
+    inside(h.to(ref.device), ref, HALF_BF16 * ref.abs() + 1.01 * b + 1e-38, what)
 
 
 def check_back(got, dh, X, g, u, ge, ue, wg, wu, kind, what):
@@ -48,12 +48,12 @@ def check_back(got, dh, X, g, u, ge, ue, wg, wu, kind, what):
     t, f = D.shape
     ref = dg @ G + du @ U
     terms = dg.abs() @ G.abs() + du.abs() @ U.abs()
-    inside(dx.cpu(), ref, HALF_BF16 * ref.abs() + 1.02 * (dge @ G.abs() + due @ U.abs() + 2 * f * HALF_F32 * terms)
+    inside(dx.to(ref.device), ref, HALF_BF16 * ref.abs() + 1.02 * (dge @ G.abs() + due @ U.abs() + 2 * f * HALF_F32 * terms)
            + 1e-38, f"{what} dx")
     for name, got_w, v, ve in (("dw_gate", dwg, dg, dge), ("dw_up", dwu, du, due)):
         ref = v.t() @ X
         b = ve.t() @ X.abs() + t * HALF_F32 * (v.abs().t() @ X.abs())
-        inside(got_w.cpu(), ref, HALF_BF16 * ref.abs() + 1.02 * b + 1e-38, f"{what} {name}")
+        inside(got_w.to(ref.device), ref, HALF_BF16 * ref.abs() + 1.02 * b + 1e-38, f"{what} {name}")
 
 
 SHAPES = [(1, 1, 1), (1, 8, 8), (2, 5, 3), (16, 64, 32), (33, 40, 31), (65, 64, 65), (64, 96, 96), (128, 128, 128),

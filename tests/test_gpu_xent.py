@@ -42,18 +42,18 @@ def check(x, w, y, mean, scale, got, what):
     big = (X @ W.t()).abs().amax(1)
     # exponentials and logarithms of the hardware: 2^-21 of values of the logits' size, and of log v
     rbound = 2 * zerr[:, 0] + 2.0 ** -21 * (big + math.log(v) + 1)
-    inside(row.cpu(), rr, rbound, f"{what} row_loss")
+    inside(row.to(X.device), rr, rbound, f"{what} row_loss")
     keep = (y != IGN).double()
     share = c / scale
-    inside(loss.cpu()[0], rl, (rbound * keep).sum() * share + HALF_F32 * rl.abs() * 4, f"{what} loss")
+    inside(loss.to(X.device)[0], rl, (rbound * keep).sum() * share + HALF_F32 * rl.abs() * 4, f"{what} loss")
     q = torch.exp(X @ W.t() - torch.logsumexp(X @ W.t(), 1, keepdim=True)) * keep.unsqueeze(1)
     perr = HALF_BF16 * 1.01 * p.abs() + (HALF_F16 * 1.01 + 2 * rbound.unsqueeze(1)) * q + 2.0 ** -25 * keep.unsqueeze(1)
     if dx is not None:
         b = c * (perr @ W.abs() + 1.01 * v * HALF_F32 * (p.abs() @ W.abs()))
-        inside(dx.cpu(), rdx, HALF_BF16 * rdx.abs() + 1.01 * b + 1e-38, f"{what} dx")
+        inside(dx.to(X.device), rdx, HALF_BF16 * rdx.abs() + 1.01 * b + 1e-38, f"{what} dx")
     if dw is not None:
         b = c * (perr.t() @ X.abs() + 1.01 * t * HALF_F32 * (p.abs().t() @ X.abs()))
-        inside(dw.cpu(), rdw, HALF_BF16 * rdw.abs() + 1.01 * b + 1e-38, f"{what} dw")
+        inside(dw.to(X.device), rdw, HALF_BF16 * rdw.abs() + 1.01 * b + 1e-38, f"{what} dw")
 
 
 SHAPES = [(1, 1, 1), (1, 8, 2), (2, 3, 5), (1, 64, 1000), (17, 33, 63), (64, 64, 64), (65, 40, 65), (127, 96, 129),
