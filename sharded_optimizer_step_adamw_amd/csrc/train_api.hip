@@ -157,7 +157,7 @@ struct XentPlan {
     int64_t piece;   // rows of a piece
     int32_t pieces, groups;
     int64_t lde;     // row stride of the exponentials
-    size_t e, stats, zt, lse, row, factor, sum, part, total;
+    size_t e, stats, zt, row, factor, sum, part, total;
     Input probs(char *ws, int64_t n) const {
         return Input{reinterpret_cast<const uint16_t *>(ws + e), lde, n, w.rows, false, 0};
     }
@@ -168,7 +168,8 @@ struct XentPlan {
         return Product(kTgStore, n, w.cols, segment(along(probs(ws, n), 0, n), across(w, 0, w.rows)));
     }
     Product dw(char *ws, int64_t r0, int64_t n) const {
-        Product p(kTgStore, w.rows, w.cols, segment(across(probs(ws, n), 0, n), across(x, r0, n)));
+        Product p(pieces > 1 ? kTgSum : kTgStore, w.rows, w.cols,
+                  segment(across(probs(ws, n), 0, n), across(x, r0, n)));
         p.L.sum_in = r0 > 0;
         p.L.sum_out = r0 + n < x.rows;
         return p;
@@ -192,7 +193,6 @@ XentPlan xent_plan(int64_t T, int64_t D, int64_t V, const uint16_t *x, int64_t l
     if (dx || dw) p.e = c.take(p.piece * p.lde * 2);
     p.stats = c.take(p.piece * p.groups * (int64_t)sizeof(float2));
     p.zt = c.take(p.piece * 4);
-    p.lse = c.take(p.piece * 4);
     p.row = c.take(T * 4);
     p.factor = c.take(4);
     if (dw && p.pieces > 1) p.sum = c.take(V * up(D, 4) * 4);
@@ -285,7 +285,7 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
     float *factor = reinterpret_cast<float *>(ws + p.factor);
     float *row = row_loss != nullptr ? row_loss : reinterpret_cast<float *>(ws + p.row);
     if (T == 0) {
-        ZOPT_TRY(launch_xent_total(row, 0, target, ignore_index, mean, loss, s));
+        ZOPT_TRY(launch_xent_total(TgTotal{row, target, 0, ignore_index, mean, loss}, s));
         if (dw != nullptr) ZOPT_TRY(launch_fill_zero(dw, lddw, V, D, s));
         return ZOPT_OK;
     }
@@ -303,7 +303,8 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
     ZOPT_TRY(preps.run(s));
     uint16_t *e = dx != nullptr || dw != nullptr ? reinterpret_cast<uint16_t *>(ws + p.e) : nullptr;
     float2 *stats = reinterpret_cast<float2 *>(ws + p.stats);
-    float *zt = reinterpret_cast<float *>(ws + p.zt), *lse = reinterpret_cast<float *>(ws + p.lse);
+    float *zt = reinterpret_cast<float *>(ws + p.zt);
+    const TgTotal total{row, target, T, ignore_index, mean, loss};
     // Exponentials beyond twice the memory-side cache go past the caches: for
     // [8192, 768] x 50304 (824 MB) the pass that makes them takes 51 us less of
     // 790 so, the one that turns them into probabilities 23 us less of 350.
@@ -317,19 +318,20 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
         L.lde = e != nullptr ? p.lde : 0;
         L.past = past;
         L.stats = stats;
-        L.ldstat = n;
+        L.ldstat = p.groups;
         L.target = target + r0;
         L.zt = zt;
         ZOPT_TRY(logits.run(false, false, ws + p.part, s));
-        ZOPT_TRY(launch_xent_lse(stats, n, p.groups, target + r0, ignore_index, (int32_t)V, zt, n, lse, row + r0, s));
-        if (e == nullptr) continue;
-        ZOPT_TRY(launch_xent_probs(e, p.lde, n, (int32_t)V, stats, n, lse, row + r0, target + r0,
-                                   ignore_index, past, s));
+        ZOPT_TRY(launch_xent_rows(stats, p.groups, target + r0, ignore_index, (int32_t)V, zt, n, row + r0, e, p.lde, past,
+                                  s));
+        // (the last product's launch also forms the loss)
+        const bool last = r0 + n == T;
         if (dx != nullptr) {
             Product g = p.dx(ws, n);
             g.L.prob[0].out = dx + r0 * lddx;
             g.L.ldc = lddx;
             g.L.alpha = factor;
+            if (last && dw == nullptr) g.L.sum_up = total;
             ZOPT_TRY(g.run(false, true, ws + p.part, s));
         }
         if (dw != nullptr) {
@@ -338,10 +340,11 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
             g.L.prob[0].sum = reinterpret_cast<float *>(ws + p.sum);
             g.L.ldc = lddw;
             g.L.alpha = factor;
+            if (last) g.L.sum_up = total;
             ZOPT_TRY(g.run(true, true, ws + p.part, s));
         }
     }
-    ZOPT_TRY(launch_xent_total(row, T, target, ignore_index, mean, loss, s));
+    if (e == nullptr) ZOPT_TRY(launch_xent_total(total, s));
     return ZOPT_OK;
 }
 

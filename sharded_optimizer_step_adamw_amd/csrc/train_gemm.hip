@@ -107,7 +107,7 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
                                               const int (&target)[FM]) {
     const int lane = lane_id(), c = lane & 15, q = lane >> 4;
     if (C0 >= L.N) return;  // (lde - N < 64: no column of e lies in a group past N's last)
-    float2 *stats = L.stats + (int64_t)(C0 / kXentGroup) * L.ldstat + R0 + c;
+    float2 *stats = L.stats + (int64_t)(R0 + c) * L.ldstat + C0 / kXentGroup;
     uint16_t *e = L.e + (int64_t)(R0 + c) * L.lde + C0 + q * 8;
     const int rows = L.M - R0 - c, cols = L.N - C0 - q * 8;
     const bool whole = C0 + 64 <= L.N, keep = L.e != nullptr;
@@ -163,7 +163,7 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
                 }
             }
         }
-        stats += 16;
+        stats += 16 * L.ldstat;
         e += 16 * L.lde;
         __builtin_amdgcn_sched_barrier(0);
     }
@@ -260,18 +260,18 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
     }
 }
 
-// A tile of sums: alpha * acc to bf16, or fp32 sums kept for a later call.
+// A tile of sums: alpha * acc to bf16; SUM: plus earlier fp32 sums, or kept as
+// such for a later call.
 // PERM: the column order of a row-major B (eight consecutive per lane).
-template <int FM, int FN, bool PERM>
-__device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProblem &P, tg_f32x4 (&acc)[FM][FN], int R0,
-                                               int C0) {
+template <int FM, int FN, bool PERM, bool SUM>
+__device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProblem &P, float alpha,
+                                               tg_f32x4 (&acc)[FM][FN], int R0, int C0) {
     const int lane = lane_id(), c = lane & 15, q = lane >> 4;
-    const float alpha = L.alpha ? *L.alpha : 1.0f;
     // the lane's first column, and the one of block j
     const int first = C0 + (PERM ? q * 8 : q * 4);
     auto at = [](int j) __attribute__((always_inline)) { return PERM ? (j >> 1) * 32 + (j & 1) * 4 : j * 16; };
     const int rows = L.M - R0 - c, cols = L.N - first;  // what is left from the lane's first place on
-    const bool in = L.sum_in != 0;
+    const bool in = SUM && L.sum_in != 0;
     float *s = P.sum + (int64_t)(R0 + c) * L.ldsum + first;  // (rows of fp32 sums are padded to a multiple of 4)
     const int64_t sstep = 16 * L.ldsum;
     uint16_t *o = P.out + (int64_t)(R0 + c) * L.ldc + first;
@@ -298,19 +298,20 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
         }
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            if (i * 16 >= rows || at(j) >= cols) continue;
-            if (L.sum_out) {
-                *reinterpret_cast<tg_f32x4 *>(s + i * sstep + at(j)) = v[j];
-                continue;
-            }
-            v[j] *= alpha;
-            const tg_u32x2 p{tg_pack_bf16(v[j][0], v[j][1]), tg_pack_bf16(v[j][2], v[j][3])};
-            if (at(j) + 4 <= cols) {
-                tg_store(o + at(j), p);
-            } else {
-                o[at(j)] = (uint16_t)p.x;
-                if (at(j) + 1 < cols) o[at(j) + 1] = (uint16_t)(p.x >> 16);
-                if (at(j) + 2 < cols) o[at(j) + 2] = (uint16_t)p.y;
+            if (i * 16 < rows && at(j) < cols) {
+                if (SUM && L.sum_out) {
+                    *reinterpret_cast<tg_f32x4 *>(s + i * sstep + at(j)) = v[j];
+                } else {
+                    const tg_f32x4 x = v[j] * alpha;
+                    const tg_u32x2 p{tg_pack_bf16(x[0], x[1]), tg_pack_bf16(x[2], x[3])};
+                    if (at(j) + 4 <= cols) {
+                        tg_store(o + at(j), p);
+                    } else {
+                        o[at(j)] = (uint16_t)p.x;
+                        if (at(j) + 1 < cols) o[at(j) + 1] = (uint16_t)(p.x >> 16);
+                        if (at(j) + 2 < cols) o[at(j) + 2] = (uint16_t)p.y;
+                    }
+                }
             }
         }
         o += step;
@@ -318,17 +319,25 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
     }
 }
 
+// The factor of the outputs, in a scalar register: read once, before the main
+// loop (a load among the stores would wait for the operands in flight).
+__device__ __forceinline__ float read_alpha(const TgLaunch &L) {
+    float a = 1.0f;
+    if (L.alpha != nullptr) a = *L.alpha;
+    return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(a)));
+}
+
 // What becomes of a wave's sums, BM / WR rows from R0 and 64 columns (32 of
 // the gate and of the up projection) from C0 on.
 template <int EPI, bool BKM, int FM>
-__device__ __forceinline__ void finish(const TgLaunch &L, int prob, tg_f32x4 (&acc)[FM][4], int R0, int C0,
-                                       const int (&target)[FM]) {
+__device__ __forceinline__ void finish(const TgLaunch &L, int prob, float alpha, tg_f32x4 (&acc)[FM][4], int R0,
+                                       int C0, const int (&target)[FM]) {
     if constexpr (EPI == kTgXent)
         xent_epilogue<FM>(L, acc, R0, C0, target);
     else if constexpr (EPI == kTgGlu || EPI == kTgGluBack)
         glu_epilogue<FM, EPI == kTgGluBack>(L, acc, R0, C0);
     else
-        store_epilogue<FM, 4, !BKM>(L, L.prob[prob], acc, R0, C0);
+        store_epilogue<FM, 4, !BKM, EPI == kTgSum>(L, L.prob[prob], alpha, acc, R0, C0);
 }
 
 // Tiles.  A BM x BN tile per workgroup, its WR x WC waves BM / WR x 64 each,
@@ -384,9 +393,9 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, i
 // unit u ^ qsw(r), read with ds_read_b64_tr_b16: lane 4 q + p of a 16-lane
 // group addresses row +q, columns 4 p .. 4 p + 3 of a 4 x 16 block, and lane
 // i receives rows +0 .. +3 of column i.  Both spread each read over all
-// banks.  The transposing reads are inline assembly: as ordinary loads the
-// compiler could not tell them from the copies in flight into other buffers
-// and would wait for those.  Each is waited for within the stage's body.
+// banks.  The reads are inline assembly: as ordinary loads the compiler cannot
+// tell them from the copies in flight into other buffers and may wait for
+// those.  Each is waited for within the stage's body.
 template <int TILE, int EPI, bool AKM, bool BKM>
 __global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64)
 __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) {
@@ -410,7 +419,14 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / WC, wc = wave % WC;
-    const int grid = gridDim.x;
+    constexpr bool PLAIN = EPI == kTgStore || EPI == kTgSum;
+    const int grid = gridDim.x - (PLAIN && L.sum_up.loss != nullptr ? 1 : 0);
+    if constexpr (PLAIN) {
+        if ((int)blockIdx.x == grid) {
+            tg_total<NW * 64>(L.sum_up);
+            return;
+        }
+    }
     const uint32_t lds_base =
         (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) uint8_t *)lds);
 
@@ -574,6 +590,12 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
             : "i"(decltype(BLK)::value << 5), "v"(at), "i"(4 * decltype(ROWB)::value));
         return __builtin_bit_cast(bf16x8, tg_u32x4{lo.x, lo.y, hi.x, hi.y});
     };
+    auto rread = [&](uint32_t at, auto BLK) __attribute__((always_inline)) {
+        tg_u32x4 v;
+        asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(at), "i"(decltype(BLK)::value * 16 * ROW));
+        return __builtin_bit_cast(bf16x8, v);
+    };
+    const uint32_t roffa = lds_base + wr * WTM * ROW + foff, roffb = lds_base + OPA + wc * 64 * ROW + foff;
     // fragment y of a stage: A's blocks, then B's
     auto read = [&](int buf, int sbase, auto Y) __attribute__((always_inline)) {
         constexpr int y = decltype(Y)::value;
@@ -581,24 +603,22 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
             if constexpr (AKM)
                 fa[buf][y] = tread(toffa + sbase, Y, std::integral_constant<int, QRA>{});
             else
-                fa[buf][y] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + (wr * WTM + y * 16) * ROW + foff]);
+                fa[buf][y] = rread(roffa + sbase, Y);
         } else {
             constexpr int j = y - FM;
             if constexpr (BKM)
                 fb[buf][j] = tread(toffb + sbase + OPA, std::integral_constant<int, j>{},
                                    std::integral_constant<int, QRB>{});
             else
-                fb[buf][j] = *reinterpret_cast<const bf16x8 *>(&lds[sbase + OPA + (wc * 64 + j * 16) * ROW + foff]);
+                fb[buf][j] = rread(roffb + sbase, std::integral_constant<int, j>{});
         }
     };
     // (after a wait: nothing that uses the fragments moves above it)
     auto tie = [&](int buf) __attribute__((always_inline)) {
-        if constexpr (AKM)
 #pragma unroll
-            for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(fa[buf][i]));
-        if constexpr (BKM)
+        for (int i = 0; i < FM; ++i) asm volatile("" : "+v"(fa[buf][i]));
 #pragma unroll
-            for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(fb[buf][j]));
+        for (int j = 0; j < FN; ++j) asm volatile("" : "+v"(fb[buf][j]));
     };
     tg_f32x4 acc[FM][FN];
     // steps of a stage's body: product m, then one load or fragment read
@@ -664,6 +684,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         }
     };
 
+    const float alpha = PLAIN ? read_alpha(L) : 1.0f;
     Tile cu, nx{};
     int slot = seek(blockIdx.x, cu);
     if (slot < 0) return;
@@ -708,7 +729,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         } else {
             int target[FM];
             read_targets(target);
-            finish<EPI, BKM, FM>(L, cu.prob, acc, cu.m0 + wr * WTM, cu.n0 + wc * (GLU ? 32 : 64), target);
+            finish<EPI, BKM, FM>(L, cu.prob, alpha, acc, cu.m0 + wr * WTM, cu.n0 + wc * (GLU ? 32 : 64), target);
         }
         which ^= 1;
         if (!more) break;
@@ -753,7 +774,7 @@ __global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
         const int64_t v = row < L.M ? L.target[row] : -1;
         if (v >= 0 && v <= 0x7FFFFFFF) target[0] = (int)v;
     }
-    finish<EPI, BKM, 1>(L, prob, acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
+    finish<EPI, BKM, 1>(L, prob, read_alpha(L), acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
 }
 
 // Compute units of the current device (asked for once), a multiple of the 8
@@ -784,7 +805,8 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
     L.padded = (L.total + 7) / 8 * 8;
     const int64_t round = (int64_t)compute_units() * (C::WPE * 4 / (threads / 64));
     const uint32_t grid = (uint32_t)(L.padded < round ? L.padded : round);
-    hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM>), dim3(grid), dim3(threads), 0, stream, L);
+    hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM>), dim3(grid + ((EPI == kTgStore || EPI == kTgSum) && L.sum_up.loss != nullptr ? 1 : 0)),
+                       dim3(threads), 0, stream, L);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && L.splits > 1) {
         const int64_t waves = (tiles - L.whole) * (C::BM / 16) * C::WC;
@@ -832,7 +854,7 @@ void plan_tg(TgEpilogue epi, TgLaunch &L) {
         const int64_t bn = glu ? f.bn / 2 : f.bn, held = f.held * cus;
         const int64_t tiles = (L.M + f.bm - 1) / f.bm * ((L.N + bn - 1) / bn) * L.nprob;
         const int64_t rounds = tiles / held, rest = tiles % held;
-        const double each = epi == kTgStore ? f.plain : f.heavy;
+        const double each = epi == kTgStore || epi == kTgSum ? f.plain : f.heavy;
         auto load = [&](int64_t n) {
             // (one on each of few CUs is not held up by the others)
             const bool few = n == 1 && (f.held > 1 || tiles < cus / 2);
@@ -870,7 +892,8 @@ hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStrea
     if (epi == kTgXent) return run_tile<kTgXent, false, false>(L, stream);
     if (epi == kTgGlu) return run_tile<kTgGlu, false, false>(L, stream);
     if (epi == kTgGluBack) return run_tile<kTgGluBack, false, false>(L, stream);
-    if (!b_km) return hipErrorInvalidValue;
+    if (!b_km || (epi == kTgSum && !a_km)) return hipErrorInvalidValue;
+    if (epi == kTgSum) return run_tile<kTgSum, true, true>(L, stream);
     return a_km ? run_tile<kTgStore, true, true>(L, stream) : run_tile<kTgStore, false, true>(L, stream);
 }
 

@@ -28,11 +28,12 @@ struct TgSegment {
 };
 
 // What becomes of a tile:
-//   kTgStore    alpha * sum -> bf16 (or fp32 sums, see below)
+//   kTgStore    alpha * sum -> bf16
+//   kTgSum      the same with fp32 sums kept between calls (see below)
 //   kTgXent     exponentials and row statistics of a piece of logits
 //   kTgGlu      act(g) u from interleaved gate / up columns, with checkpoints
 //   kTgGluBack  dg, du (and h) from g, u and dh
-enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3 };
+enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3, kTgSum = 4 };
 
 enum TgAct : int { kActSilu = 0, kActGelu = 1 };
 
@@ -41,6 +42,16 @@ struct TgProblem {
     int32_t nseg;
     uint16_t *out;     // bf16 [M, N], row stride ldc
     float *sum;        // fp32 [M, N] (row stride ldsum), or NULL
+};
+
+// The loss from its rows: share * sum, share = 1 or (mean) 1 / the rows whose
+// target is not `ignore` (0 if none).
+struct TgTotal {
+    const float *row_loss;
+    const int64_t *target;
+    int64_t rows, ignore;
+    int32_t mean;
+    float *loss;
 };
 
 struct TgLaunch {
@@ -55,13 +66,15 @@ struct TgLaunch {
     int32_t tiles, total, padded;  // tiles of all problems; with parts; rounded up to 8
     float *part;
     int64_t ldc;
-    // kTgStore
+    // kTgStore, kTgSum
     const float *alpha;       // device scalar, or NULL: 1
+    // kTgSum
     int64_t ldsum;
     int32_t sum_in, sum_out;  // add prob.sum first; write fp32 to prob.sum (else bf16 to out)
-    // kTgXent: e [M, lde] fp16 (NULL: statistics only), per 64-column group g
-    // and row r stats[g * ldstat + r] = (max, sum of exponentials); the
-    // target's logit to zt
+    TgTotal sum_up;           // loss not NULL: one more workgroup forms it
+    // kTgXent: e [M, lde] fp16 (NULL: statistics only), per row r and 64-column
+    // group g stats[r * ldstat + g] = (max, sum of exponentials); the target's
+    // logit to zt
     uint16_t *e;
     int64_t lde;
     int32_t past;             // e is written past the caches
@@ -87,7 +100,8 @@ constexpr int kXentGroup = 64;  // columns per statistics group
 void plan_tg(TgEpilogue epi, TgLaunch &L);
 size_t tg_part_bytes(TgEpilogue epi, const TgLaunch &L);
 
-// a_km / b_km: operand is k-major.  kTgXent and the Glu kinds: both row-major.
+// a_km / b_km: operand is k-major.  kTgXent and the Glu kinds: both row-major;
+// kTgSum: both k-major; kTgStore: b k-major.
 hipError_t launch_tg(TgEpilogue epi, bool a_km, bool b_km, TgLaunch &L, hipStream_t stream);
 
 // ------------------------------------------------------------- row passes
@@ -135,19 +149,54 @@ hipError_t launch_act8_pack(const uint16_t *x, int64_t ld, int64_t rows, int64_t
 hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t rows, int64_t cols,
                               uint16_t *x, int64_t ld, hipStream_t stream);
 
-// lse and row loss of rows [0, rows) from the group statistics
-hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups,
-                           const int64_t *target, int64_t ignore, int32_t V, const float *zt,
-                           int64_t rows, float *lse, float *row_loss, hipStream_t stream);
-// e (fp16 exponentials) -> P = softmax - onehot (bf16), in place, columns [V, lde) zero
-hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V,
-                             const float2 *stats, int64_t ldstat, const float *lse,
-                             const float *row_loss, const int64_t *target, int64_t ignore, int32_t past,
-                             hipStream_t stream);
-hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t *target,
-                             int64_t ignore, int32_t mean, float *loss, hipStream_t stream);
+// Rows [0, rows): row losses from the group statistics [rows, groups] and the
+// targets' logits; with e (fp16 exponentials, row stride lde) also P = softmax
+// - onehot (bf16) in its place, columns [V, lde) zero.
+hipError_t launch_xent_rows(const float2 *stats, int32_t groups, const int64_t *target,
+                            int64_t ignore, int32_t V, const float *zt, int64_t rows,
+                            float *row_loss, uint16_t *e, int64_t lde, bool past,
+                            hipStream_t stream);
+hipError_t launch_xent_total(const TgTotal &t, hipStream_t stream);
 
 // ---------------------------------------------------------- device helpers
+
+// The number of rows that take part, summed over a block of N threads.
+template <int N>
+__device__ __forceinline__ long long tg_valid_rows(const int64_t *__restrict__ target, int64_t rows,
+                                                   int64_t ignore) {
+    __shared__ long long part[N / 64];
+    long long n = 0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < rows; i += N) n += target[i] != ignore ? 1 : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
+    __syncthreads();
+    long long all = 0;
+    for (int k = 0; k < N / 64; ++k) all += part[k];
+    return all;
+}
+__device__ __forceinline__ double tg_share(long long rows, int mean) {
+    return !mean ? 1.0 : rows > 0 ? 1.0 / (double)rows : 0.0;
+}
+// the loss from its rows by a block of N threads: in double, in a fixed order
+template <int N>
+__device__ __forceinline__ void tg_total(const TgTotal &t) {
+    __shared__ double part[N / 64];
+    const long long n = t.mean ? tg_valid_rows<N>(t.target, t.rows, t.ignore) : 0;
+    double s = 0.0;
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < t.rows; i += N) s += (double)t.row_loss[i];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double all = 0.0;
+        for (int k = 0; k < N / 64; ++k) all += part[k];
+        *t.loss = (float)(all * tg_share(n, t.mean));
+    }
+}
 
 // two fp32 -> two bf16 / fp16, round to nearest even, one instruction each; a
 // NaN stays a NaN

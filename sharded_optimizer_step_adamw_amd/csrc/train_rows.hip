@@ -95,25 +95,6 @@ __global__ __launch_bounds__(kThreads) void act8_unpack_kernel(const uint8_t *__
     }
 }
 
-// The number of rows that take part, summed over a block of N threads.
-template <int N>
-__device__ __forceinline__ long long valid_rows(const int64_t *__restrict__ target, int64_t rows, int64_t ignore) {
-    __shared__ long long part[N / 64];
-    long long n = 0;
-#pragma unroll 8
-    for (int64_t i = threadIdx.x; i < rows; i += N) n += target[i] != ignore ? 1 : 0;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = n;
-    __syncthreads();
-    long long all = 0;
-    for (int k = 0; k < N / 64; ++k) all += part[k];
-    return all;
-}
-__device__ __forceinline__ double share_of(long long rows, int mean) {
-    return !mean ? 1.0 : rows > 0 ? 1.0 / (double)rows : 0.0;
-}
-
 // (m, s) of two sets of exponentials, s relative to exp(m)
 __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     const float t = fmaxf(m, m2);
@@ -122,112 +103,89 @@ __device__ __forceinline__ void join(float &m, float &s, float m2, float s2) {
     m = t;
 }
 
-// lse = m + log(sum_g s_g exp(m_g - m)), m the largest group maximum.  A block
-// of 1024 threads takes 16 rows, 64 threads a row; each joins every 64th
-// group, eight at a time so that as many loads are in flight, and the 64 join
-// in a fixed order.  A target outside [0, V) that is not the ignored one
-// makes the row NaN.
-__global__ __launch_bounds__(1024) void xent_lse_kernel(const float2 *__restrict__ stats, int64_t ldstat, int groups,
-                                                        const int64_t *__restrict__ target, int64_t ignore, int V,
-                                                        const float *__restrict__ zt, int64_t rows,
-                                                        float *__restrict__ lse, float *__restrict__ row_loss) {
-    __shared__ float pm[16][16], ps[16][16];
-    const int lr = threadIdx.x & 15, part = threadIdx.x >> 4;
-    const int64_t row = blockIdx.x * (int64_t)16 + lr;
-    const bool live = row < rows;
-    float m = -INFINITY, s = 0.0f;
-    if (live) {
-        const float2 *p = stats + row;
-        for (int g = part; g < groups; g += 512) {
-            float2 v[8];
+// One row a block: its loss from the group statistics,
+//   lse = m + log(sum_g s_g exp(m_g - m)), m the largest group maximum,
+//   row loss = lse - the target's logit,
+// and, if e is wanted, its exponentials turned into P = softmax - onehot in
+// place: exp(m_group - lse) e, 0 in columns [V, lde) and for ignored rows.
+// The target's own entry, softmax - 1, comes from the row's loss,
+// expm1(-row loss): where the model is sure of the target the difference is
+// small, and e's 11 bits would be most of it.  A target outside [0, V) that
+// is not the ignored one makes the row NaN.  Everything is joined in a fixed
+// order.  Bound by HBM: e is read and written once (4 bytes a logit).
+template <bool PAST>
+__global__ __launch_bounds__(kThreads) void xent_rows_kernel(const float2 *__restrict__ stats, int groups,
+                                                             const int64_t *__restrict__ target, int64_t ignore, int V,
+                                                             const float *__restrict__ zt, int64_t rows,
+                                                             float *__restrict__ row_loss, uint16_t *__restrict__ e,
+                                                             int64_t lde) {
+    __shared__ float pm[kThreads / 64], ps[kThreads / 64];
+    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+        const float2 *p = stats + row * groups;
+        float m = -INFINITY, s = 0.0f;
+        for (int g = threadIdx.x; g < groups; g += 4 * kThreads) {
+            float2 v[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = g + 64 * k < groups ? p[(int64_t)(g + 64 * k) * ldstat] : make_float2(-INFINITY, 0.0f);
+            for (int k = 0; k < 4; ++k)
+                v[k] = g + k * kThreads < groups ? p[g + k * kThreads] : make_float2(-INFINITY, 0.0f);
             float t = m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t = fmaxf(t, v[k].x);
-            const float ref = t == -INFINITY ? 0.0f : t;
+            for (int k = 0; k < 4; ++k) t = fmaxf(t, v[k].x);
+            const float ref = t == -INFINITY ? 0.0f : t;  // (a NaN maximum is left out and makes the sum NaN)
             s *= expf(m - ref);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) s += v[k].y * expf(v[k].x - ref);
+            for (int k = 0; k < 4; ++k) s += v[k].y * expf(v[k].x - ref);
             m = t;
         }
-    }
 #pragma unroll
-    for (int o = 16; o <= 32; o <<= 1) {
-        const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
-        join(m, s, m2, s2);
-    }
-    if ((part & 3) == 0) {
-        pm[part >> 2][lr] = m;
-        ps[part >> 2][lr] = s;
-    }
-    __syncthreads();
-    if (part != 0 || !live) return;
-    for (int k = 1; k < 16; ++k) join(m, s, pm[k][lr], ps[k][lr]);
-    const int64_t t = target[row];
-    const bool in = t >= 0 && t < V;
-    const float ls = logf(s);
-    lse[row] = in || t == ignore ? m + ls : NAN;
-    row_loss[row] = t == ignore ? 0.0f : in ? ls + (m - zt[row]) : NAN;
-}
-
-// e -> P in place, eight columns a thread: exp(m_group - lse) e, 0 for ignored
-// rows.  The target's own entry, softmax - 1, comes from the row's loss,
-// expm1(-row_loss): where the model is sure of the target the difference is
-// small, and e's 11 bits would be most of it.
-template <bool PAST>
-__global__ __launch_bounds__(kThreads) void xent_probs_kernel(uint16_t *__restrict__ e, int64_t lde, int64_t rows,
-                                                              int V, const float2 *__restrict__ stats, int64_t ldstat,
-                                                              const float *__restrict__ lse,
-                                                              const float *__restrict__ row_loss,
-                                                              const int64_t *__restrict__ target, int64_t ignore) {
-    const int64_t per = lde / 8, total = rows * per;
-    for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
-        const int64_t r = id / per, c = (id - r * per) * 8;
-        tg_u32x4 *p = reinterpret_cast<tg_u32x4 *>(e + r * lde + c);
-        const int64_t t = target[r];
-        tg_u32x4 out{0, 0, 0, 0};
-        if (t != ignore && c < V) {
-            const tg_u32x4 in = tg_load<tg_u32x4, PAST>(p);
-            const float f = expf(stats[(c / kXentGroup) * ldstat + r].x - lse[r]);
-            const int64_t rel = t - c;
-            float v[8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const tg_f16x2 h = __builtin_bit_cast(tg_f16x2, (uint32_t)in[k]);
-                v[2 * k] = (float)h.x * f;
-                v[2 * k + 1] = (float)h.y * f;
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (rel == k) v[k] = expm1f(-row_loss[r]);
-                if (c + k >= V) v[k] = 0.0f;
-            }
-            out = pack8(v);
+        for (int o = 1; o < 64; o <<= 1) {
+            const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o);
+            join(m, s, m2, s2);
         }
-        tg_store<PAST>(p, out);
+        __syncthreads();  // (the last row's values have been read)
+        if ((threadIdx.x & 63) == 0) {
+            pm[threadIdx.x >> 6] = m;
+            ps[threadIdx.x >> 6] = s;
+        }
+        __syncthreads();
+        m = pm[0];
+        s = ps[0];
+#pragma unroll
+        for (int k = 1; k < kThreads / 64; ++k) join(m, s, pm[k], ps[k]);
+        const int64_t t = target[row];
+        const bool in = t >= 0 && t < V, used = t != ignore;
+        const float ls = logf(s), lse = in ? m + ls : NAN;
+        const float loss = !used ? 0.0f : in ? ls + (m - zt[row]) : NAN;
+        if (threadIdx.x == 0) row_loss[row] = loss;
+        if (e == nullptr) continue;
+        for (int64_t c = threadIdx.x * 8; c < lde; c += kThreads * 8) {
+            tg_u32x4 *at = reinterpret_cast<tg_u32x4 *>(e + row * lde + c);
+            tg_u32x4 out{0, 0, 0, 0};
+            if (used && c < V) {
+                const tg_u32x4 raw = tg_load<tg_u32x4, PAST>(at);
+                const float f = expf(p[c / kXentGroup].x - lse);
+                const int64_t rel = t - c;
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const tg_f16x2 h = __builtin_bit_cast(tg_f16x2, (uint32_t)raw[k]);
+                    v[2 * k] = (float)h.x * f;
+                    v[2 * k + 1] = (float)h.y * f;
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (rel == k) v[k] = expm1f(-loss);
+                    if (c + k >= V) v[k] = 0.0f;
+                }
+                out = pack8(v);
+            }
+            tg_store<PAST>(at, out);
+        }
     }
 }
 
 // loss = share * sum of row losses, in double, in a fixed order
-__global__ __launch_bounds__(1024) void xent_total_kernel(const float *__restrict__ row_loss, int64_t rows,
-                                                          const int64_t *__restrict__ target, int64_t ignore,
-                                                          int mean, float *__restrict__ loss) {
-    __shared__ double part[16];
-    const long long n = mean ? valid_rows<1024>(target, rows, ignore) : 0;
-    double s = 0.0;
-    for (int64_t i = threadIdx.x; i < rows; i += 1024) s += (double)row_loss[i];
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        double all = 0.0;
-        for (int k = 0; k < 16; ++k) all += part[k];
-        *loss = (float)(all * share_of(n, mean));
-    }
-}
+__global__ __launch_bounds__(1024) void xent_total_kernel(TgTotal t) { tg_total<1024>(t); }
 
 // The jobs before a call's products, each on blocks of its own; eight columns
 // a thread.  One launch for all: each of them alone takes 3 to 5 us on small
@@ -277,8 +235,8 @@ __device__ __forceinline__ void prep_back(const TgPrep &j, int64_t block) {
     }
 }
 __device__ __forceinline__ void prep_count(const TgPrep &j) {
-    const long long n = j.mean ? valid_rows<kThreads>(j.target, j.rows, j.ignore) : 0;
-    if (threadIdx.x == 0) *j.factor = (float)(share_of(n, j.mean) * (double)j.grad_scale);
+    const long long n = j.mean ? tg_valid_rows<kThreads>(j.target, j.rows, j.ignore) : 0;
+    if (threadIdx.x == 0) *j.factor = (float)(tg_share(n, j.mean) * (double)j.grad_scale);
 }
 __global__ __launch_bounds__(kThreads) void prep_kernel(TgPrepList list) {
     uint32_t block = blockIdx.x;
@@ -330,25 +288,17 @@ hipError_t launch_act8_unpack(const uint8_t *q, const uint8_t *scale, int64_t ro
     return hipGetLastError();
 }
 
-hipError_t launch_xent_lse(const float2 *stats, int64_t ldstat, int32_t groups, const int64_t *target, int64_t ignore,
-                           int32_t V, const float *zt, int64_t rows, float *lse, float *row_loss, hipStream_t stream) {
-    hipLaunchKernelGGL(xent_lse_kernel, dim3((uint32_t)((rows + 15) / 16)), dim3(1024), 0, stream, stats, ldstat, groups,
-                       target, ignore, V, zt, rows, lse, row_loss);
+hipError_t launch_xent_rows(const float2 *stats, int32_t groups, const int64_t *target, int64_t ignore, int32_t V,
+                            const float *zt, int64_t rows, float *row_loss, uint16_t *e, int64_t lde, bool past,
+                            hipStream_t stream) {
+    const auto kernel = past ? xent_rows_kernel<true> : xent_rows_kernel<false>;
+    hipLaunchKernelGGL(kernel, dim3((uint32_t)(rows < (1 << 20) ? rows : 1 << 20)), dim3(kThreads), 0, stream, stats,
+                       groups, target, ignore, V, zt, rows, row_loss, e, lde);
     return hipGetLastError();
 }
 
-hipError_t launch_xent_probs(uint16_t *e, int64_t lde, int64_t rows, int32_t V, const float2 *stats, int64_t ldstat,
-                             const float *lse, const float *row_loss, const int64_t *target, int64_t ignore, int32_t past,
-                             hipStream_t stream) {
-    const auto kernel = past ? xent_probs_kernel<true> : xent_probs_kernel<false>;
-    hipLaunchKernelGGL(kernel, dim3(blocks_for(rows * (lde / 8))), dim3(kThreads), 0, stream, e, lde, rows, V, stats,
-                       ldstat, lse, row_loss, target, ignore);
-    return hipGetLastError();
-}
-
-hipError_t launch_xent_total(const float *row_loss, int64_t rows, const int64_t *target, int64_t ignore, int32_t mean,
-                             float *loss, hipStream_t stream) {
-    hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(1024), 0, stream, row_loss, rows, target, ignore, mean, loss);
+hipError_t launch_xent_total(const TgTotal &t, hipStream_t stream) {
+    hipLaunchKernelGGL(xent_total_kernel, dim3(1), dim3(1024), 0, stream, t);
     return hipGetLastError();
 }
 
