@@ -58,8 +58,9 @@
  *    is rounded to bf16, bitwise the unsharded trainer's copy of the master
  *    into the bf16 weights].
  *  - Per-step scalars derived from the hyperparameters are formed in double
- *    on the host and rounded once to binary32; the elementwise arithmetic is
- *    binary32 with no fused multiply-adds, in the order stated below.
+ *    on the host and rounded once to binary32; the optimizers' elementwise
+ *    arithmetic is binary32 with no fused multiply-adds, in the order stated
+ *    below.
  */
 #ifndef ZOPT_H
 #define ZOPT_H
