@@ -100,7 +100,7 @@ TgOperand across(const Input &in, int64_t r0, int64_t n) {
 }
 TgSegment segment(const TgOperand &a, const TgOperand &b) {
     const int32_t k = a.k > b.k ? a.k : b.k;
-    return TgSegment{a, b, (k + 31) / 32};
+    return TgSegment{a, b, (k + 63) / 64 * 2};
 }
 
 // A product's launch over one or two problems of the same sizes.

@@ -385,14 +385,24 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, i
 // between this stage's MFMAs -> wait for those reads and for this wave's
 // loads of the stage after.
 //
+// A row-major operand's rows then come in pieces of 64 bytes, half a cache
+// line, and every line is asked for twice.  So with four buffers and A
+// row-major they hold two PAIRS of stages: all loads of a pair, 128 bytes a
+// row, go out in the body of an odd stage, past its barrier, and are waited for
+// at the end of the next body, which needs no barrier.  Measured: the products
+// of two row-major operands 5 to 8% faster ([8192, 4096] x [4096, 28672] 1.42 ms
+// for 1.52), with B k-major 1 to 2% on 256 x 256 tiles, 7% slower on the smaller
+// ones; with both k-major 3% slower (nothing to gain, and the loads are one
+// stage closer to their use), so neither takes it.
+//
 // The kernel is persistent: one round of resident workgroups walks all tiles,
 // and from a tile's last STAGES stages on the loads are those of the
 // workgroup's next tile, so that its operands arrive while this one is
-// finished and stored.  A tile's stages are padded with zero stages to an
-// even number, four at least.
+// finished and stored.  Segments and parts are of whole pairs of stages, tiles
+// padded with zero stages to four at least.
 //
 // LDS layouts: row-major rows of 64 bytes, 16-byte chunk c of row r at slot
-// c ^ ((r >> 1) & 3); k-major rows of 2 BM (2 BN) bytes, 32-byte unit u of row r at
+// c ^ ((r >> 1) & 3), in pairs 128 bytes and c ^ (r & 7); k-major rows of 2 BM (2 BN) bytes, 32-byte unit u of row r at
 // unit u ^ qsw(r), read with ds_read_b64_tr_b16: lane 4 q + p of a 16-lane
 // group addresses row +q, columns 4 p .. 4 p + 3 of a 4 x 16 block, and lane
 // i receives rows +0 .. +3 of column i.  Both spread each read over all
@@ -417,9 +427,11 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     constexpr int BM = C::BM, BN = C::BN, WR = C::WR, WC = C::WC, NW = WR * WC, kStages = C::STAGES;
     constexpr int WTM = BM / WR, FM = WTM / 16, FN = 4;
     static_assert(BN / WC == 64, "a wave holds 64 columns");
-    constexpr int ROW = 64, OPA = BM * ROW, OPB = BN * ROW, STAGE = OPA + OPB;
-    constexpr int LA = OPA / 1024 / NW, LB = OPB / 1024 / NW, LPS = LA + LB;  // loads a wave and stage
-    static_assert(LA * NW * 1024 == OPA && LB * NW * 1024 == OPB, "whole kilobytes");
+    constexpr int OPA = BM * kBK * 2, OPB = BN * kBK * 2, STAGE = OPA + OPB;
+    constexpr bool PAIRS = !AKM && kStages == 4 && (!BKM || TILE == kTile256);  // (see above)
+    constexpr int SPL = PAIRS ? 2 : 1, ROW = 64 * SPL;  // stages a load; bytes of a row-major row
+    constexpr int LA = SPL * OPA / 1024 / NW, LB = SPL * OPB / 1024 / NW, LPS = LA + LB;  // of a wave, each SPL stages
+    static_assert(LA * NW * 1024 == SPL * OPA && LB * NW * 1024 == SPL * OPB, "whole kilobytes");
     constexpr int QRA = 2 * BM, QRB = 2 * BN;  // k-major row bytes
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack;
     static_assert(!GLU || NW % 4 == 0, "a wave loads rows of the gate or of the up projection");
@@ -475,11 +487,11 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         T.m0 = ti * BM;
         T.n0 = tj * BO;
         const TgProblem &P = L.prob[T.prob];
-        const int all = P.seg[0].stages + (!GLU && P.nseg > 1 ? P.seg[1].stages : 0);
+        const int all = P.seg[0].stages + (PLAIN && P.nseg > 1 ? P.seg[1].stages : 0);
         T.stage0 = T.split < 0 ? 0 : T.split * L.split_stages;
         T.live = all - T.stage0;
         if (T.split >= 0 && T.live > L.split_stages) T.live = L.split_stages;
-        T.stages = T.live <= 4 ? 4 : (T.live + 1) & ~1;  // (the switch to the next tile is kStages before)
+        T.stages = T.live < 4 ? 4 : T.live;  // (the switch to the next tile is kStages before)
         return true;
     };
     auto seek = [&](int slot, Tile &T) __attribute__((always_inline)) -> int {
@@ -496,8 +508,31 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     const uint16_t *pa = nullptr, *pb = nullptr;
     int ka = 0, kb = 0, lda = 0, ldb = 0, ea = 0, eb = 0, seg_left = 0, total_left = 0;
     int sprob = 0, sm0 = 0, sn0 = 0;
-    int va[LA], vb[LB];
-    const int chunk8 = ((lane & 3) ^ ((lane >> 3) & 3)) << 3;  // row-major: the lane's k offset
+    int va[PAIRS ? 1 : LA], vb[PAIRS ? 1 : LB];
+    // row-major: the lane's row of a kilobyte's and its k offset
+    const int krow = PAIRS ? lane >> 3 : lane >> 2;
+    const int chunk8 = (PAIRS ? (lane & 7) ^ (lane >> 3) : (lane & 3) ^ ((lane >> 3) & 3)) << 3;
+    // The wave's x-th kilobyte of an operand is number first + kx(x), such that
+    // its offset differs from that of the first by whole rows.  (k-major, 512-byte
+    // rows: kilobytes of the same swizzle; row-major pairs: a wave's LDS blocks
+    // of B are 0, 1 of each four or 2, 3.)  With pairs a lane keeps the first's
+    // offset, for registers, and adds the rows (kOut stays past every
+    // descriptor: less than 2^32 in all); else it keeps all, 1% faster.
+    constexpr bool spread_a = AKM ? BM == 256 : PAIRS, spread_b = BKM ? BN == 256 : PAIRS;
+    static_assert((!spread_a || LA % 2 == 0) && (!spread_b || LB % 2 == 0), "kx runs over all kilobytes");
+    auto kx = [](bool spread, int x) constexpr { return spread ? (x >> 1) * 2 * NW + (x & 1) * 2 : x * NW; };
+    const int first_a = spread_a ? (wave >> 1) * 4 + (wave & 1) : wave;
+    const int first_b = spread_b ? (wave >> 1) * 4 + (wave & 1) : wave;
+    auto rows_a = [&](int x) __attribute__((always_inline)) -> int {
+        return kx(spread_a, x) * (AKM ? 512 / BM : 16 / SPL);
+    };
+    auto rows_b = [&](int x) __attribute__((always_inline)) -> int {
+        if (BKM) return kx(spread_b, x) * (512 / BN);
+        return PAIRS ? (x >> 1) * (GLU ? NW / 4 : NW / 2) * 32 + (x & 1) * 4 : x * (GLU ? NW / 4 : NW / 2) * 32;
+    };
+    auto plus = [](int offset, int elements) __attribute__((always_inline)) -> int {
+        return (int)((uint32_t)offset + (uint32_t)elements * 2u);
+    };
     auto corner = [&](const TgOperand &o, bool km, int c0, int extent, int k0, const uint16_t *&p, int &k, int &ld,
                       int &e) __attribute__((always_inline)) {
         ld = (int)o.ld;
@@ -526,7 +561,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         sm0 = T.m0;
         sn0 = T.n0;
         const int s0 = L.prob[T.prob].seg[0].stages;
-        if (!GLU && T.stage0 >= s0)
+        if (PLAIN && T.stage0 >= s0)
             open_segment(1, (T.stage0 - s0) * kBK);
         else
             open_segment(0, T.stage0 * kBK);
@@ -536,28 +571,24 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
             const int col = (((s16 >> 1) ^ qsw(r, width)) << 4) + ((s16 & 1) << 3);
             return col * 2 < e ? (r * ld + col) * 2 : kOut;
         };
+        const int base_a = AKM ? across(first_a, BM, lda, ea) : ((first_a * (16 / SPL) + krow) * lda + chunk8) * 2;
+        // row-major: LDS row n of 16-row block `blk` holds the tile's column
+        // 32 (blk / 2) + 8 (n / 4) + 4 (blk % 2) + n % 4; gate / up: of the 32
+        // columns of wave blk / 4
+        const int blk = first_b / SPL, n = (first_b & (SPL - 1)) * 8 + krow;
+        const int row = (GLU ? blk >> 2 : blk >> 1) * 32 + 8 * (n >> 2) + 4 * (blk & 1) + (n & 3);
+        const int base_b = BKM ? across(first_b, BN, ldb, eb) : (row * ldb + chunk8) * 2;
 #pragma unroll
-        for (int x = 0; x < LA; ++x) {
-            const int kilo = x * NW + wave;
-            va[x] = AKM ? across(kilo, BM, lda, ea) : ((kilo * 16 + (lane >> 2)) * lda + chunk8) * 2;
-        }
+        for (int x = 0; x < (PAIRS ? 1 : LA); ++x) va[x] = plus(base_a, rows_a(x) * lda);
 #pragma unroll
-        for (int x = 0; x < LB; ++x) {
-            const int kilo = x * NW + wave;
-            // row-major: LDS row n of block `kilo` holds the tile's column
-            // 32 (kilo / 2) + 8 (n / 4) + 4 (kilo % 2) + n % 4; gate / up: of
-            // the 32 columns of wave kilo / 4
-            const int n = lane >> 2, sub = 8 * (n >> 2) + 4 * (kilo & 1) + (n & 3);
-            const int row = (GLU ? (kilo >> 2) * 32 : (kilo >> 1) * 32) + sub;
-            vb[x] = BKM ? across(kilo, BN, ldb, eb) : (row * ldb + chunk8) * 2;
-        }
+        for (int x = 0; x < (PAIRS ? 1 : LB); ++x) vb[x] = plus(base_b, rows_b(x) * ldb);
     };
     auto extent = [&](bool km, int k, int ld, int e) __attribute__((always_inline)) -> int {
         if (total_left <= 0 || k <= 0) return 0;
-        if (km) return ((k < kBK ? k : kBK) - 1) * ld * 2 + e;
+        if (km) return ((k < kBK * SPL ? k : kBK * SPL) - 1) * ld * 2 + e;
         return e + k * 2;
     };
-    // load y of a stage: A's kilobytes, then B's
+    // load y: A's kilobytes, then B's
     __amdgpu_buffer_rsrc_t ra, rb;
     auto open_stage = [&]() __attribute__((always_inline)) {
         ra = __builtin_amdgcn_make_buffer_rsrc((void *)pa, (short)0, extent(AKM, ka, lda, ea), 0x00020000);
@@ -566,28 +597,30 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     auto gload = [&](int sbase, int y) __attribute__((always_inline)) {
         // (a chunk past the row's end would be the next row's)
         if (y < LA) {
-            const int kilo = y * NW + wave;
-            const int o = AKM || chunk8 < ka ? va[y] : kOut;
+            const int kilo = first_a + kx(spread_a, y);
+            const int first = AKM || chunk8 < ka ? va[PAIRS ? 0 : y] : kOut;
+            const int o = PAIRS ? plus(first, rows_a(y) * lda) : first;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_ADDR(&lds[sbase + kilo * 1024]), 16, o, 0, 0, 0);
         } else {
-            const int kilo = (y - LA) * NW + wave;
-            const int o = BKM || chunk8 < kb ? vb[y - LA] : kOut;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_ADDR(&lds[sbase + OPA + kilo * 1024]), 16, o, 0, 0, 0);
+            const int x = y - LA, kilo = first_b + kx(spread_b, x);
+            const int first = BKM || chunk8 < kb ? vb[PAIRS ? 0 : x] : kOut;
+            const int o = PAIRS ? plus(first, rows_b(x) * ldb) : first;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, LDS_ADDR(&lds[sbase + SPL * OPA + kilo * 1024]), 16, o, 0, 0, 0);
         }
     };
     auto close_stage = [&]() __attribute__((always_inline)) {
-        pa += AKM ? (int64_t)kBK * lda : kBK;
-        pb += BKM ? (int64_t)kBK * ldb : kBK;
-        ka -= kBK;
-        kb -= kBK;
-        --total_left;
+        pa += AKM ? (int64_t)kBK * SPL * lda : kBK * SPL;
+        pb += BKM ? (int64_t)kBK * SPL * ldb : kBK * SPL;
+        ka -= kBK * SPL;
+        kb -= kBK * SPL;
+        total_left -= SPL;
         // (real stages left after a segment's last: there is a second one)
-        if (!GLU && --seg_left == 0 && total_left > 0) open_segment(1, 0);
+        if (PLAIN && (seg_left -= SPL) == 0 && total_left > 0) open_segment(1, 0);
     };
 
     // -------------------------------------------------- fragments and products
     const int fr = lane & 15, fh = lane >> 4;
-    const int foff = fr * ROW + ((fh ^ ((fr >> 1) & 3)) << 4);
+    const int foff = fr * ROW + ((fh ^ (PAIRS ? fr & 7 : (fr >> 1) & 3)) << 4);
     const int tr = 8 * fh + ((lane >> 2) & 3), tp = lane & 3;
     const uint32_t tlane = lds_base + ((tp >> 1) << 4) + ((tp & 1) << 3);
     const uint32_t toffa = tlane + tr * QRA + ((qsw(tr, BM) ^ (wr * FM)) << 5);
@@ -609,22 +642,22 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(at), "i"(decltype(BLK)::value * 16 * ROW));
         return __builtin_bit_cast(bf16x8, v);
     };
-    const uint32_t roffa = lds_base + wr * WTM * ROW + foff, roffb = lds_base + OPA + wc * 64 * ROW + foff;
+    const uint32_t roffa = lds_base + wr * WTM * ROW + foff, roffb = lds_base + SPL * OPA + wc * 64 * ROW + foff;
     // fragment y of a stage: A's blocks, then B's
     auto read = [&](int buf, int sbase, auto Y) __attribute__((always_inline)) {
         constexpr int y = decltype(Y)::value;
         if constexpr (y < FM) {
             if constexpr (AKM)
-                fa[buf][y] = tread(toffa + sbase, Y, std::integral_constant<int, QRA>{});
+                fa[buf][y] = tread(toffa + sbase + (PAIRS ? buf * OPA : 0), Y, std::integral_constant<int, QRA>{});
             else
-                fa[buf][y] = rread(roffa + sbase, Y);
+                fa[buf][y] = rread((PAIRS ? roffa ^ (buf << 6) : roffa) + sbase, Y);
         } else {
             constexpr int j = y - FM;
             if constexpr (BKM)
-                fb[buf][j] = tread(toffb + sbase + OPA, std::integral_constant<int, j>{},
+                fb[buf][j] = tread(toffb + sbase + SPL * OPA + (PAIRS ? buf * OPB : 0), std::integral_constant<int, j>{},
                                    std::integral_constant<int, QRB>{});
             else
-                fb[buf][j] = rread(roffb + sbase, std::integral_constant<int, j>{});
+                fb[buf][j] = rread((PAIRS ? roffb ^ (buf << 6) : roffb) + sbase, std::integral_constant<int, j>{});
         }
     };
     // (after a wait: nothing that uses the fragments moves above it)
@@ -637,24 +670,42 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     tg_f32x4 acc[FM][FN];
     // steps of a stage's body: product m, then one load or fragment read
     auto steps = [&](auto PAR, int cbase, int nbase) __attribute__((always_inline)) {
-        constexpr int par = decltype(PAR)::value;
-        constexpr int kSteps = FM * FN > LPS + FM + FN ? FM * FN : LPS + FM + FN;
+        constexpr int par = decltype(PAR)::value, loads = PAIRS && par == 0 ? 0 : LPS;
+        constexpr int kSteps = FM * FN > loads + FM + FN ? FM * FN : loads + FM + FN;
         for_each(std::make_integer_sequence<int, kSteps>{}, [&](auto MM) __attribute__((always_inline)) {
             constexpr int m = decltype(MM)::value;
             if constexpr (m < FM * FN) {
                 constexpr int i = m / FN, j = m % FN;
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[par][j], fa[par][i], acc[i][j], 0, 0, 0);
             }
-            if constexpr (m < LPS)
+            if constexpr (m < loads)
                 gload(cbase, m);
-            else if constexpr (m - LPS < FM + FN)
-                read(par ^ 1, nbase, std::integral_constant<int, m - LPS>{});
+            else if constexpr (m - loads < FM + FN)
+                read(par ^ 1, nbase, std::integral_constant<int, m - loads>{});
             __builtin_amdgcn_sched_barrier(0);
         });
     };
     int cur = 0;
     auto body = [&](auto PAR) __attribute__((always_inline)) {
         constexpr int par = decltype(PAR)::value;
+        if constexpr (PAIRS) {
+            const int other = cur ^ (2 * STAGE);
+            if constexpr (par == 0) {
+                steps(PAR, 0, cur);
+                __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0(0));
+            } else {
+                __builtin_amdgcn_s_barrier();
+                open_stage();
+                __builtin_amdgcn_sched_barrier(0);
+                steps(PAR, cur, other);
+                close_stage();
+                __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0(63));
+                cur = other;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            tie(par ^ 1);
+            return;
+        }
         const int nxt = cur + 1 == kStages ? 0 : cur + 1;
         __builtin_amdgcn_s_barrier();
         open_stage();
@@ -705,13 +756,13 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     load_targets(cu, 0);
     stream(cu, true);
 #pragma unroll
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kStages; s += SPL) {
         open_stage();
 #pragma unroll
         for (int y = 0; y < LPS; ++y) gload(s * STAGE, y);
         close_stage();
     }
-    __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0((kStages - 1) * LPS));
+    __builtin_amdgcn_s_waitcnt(WAIT_VM_LGKM0(kStages / SPL * LPS - LPS));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     for_each(std::make_integer_sequence<int, FM + FN>{},
@@ -882,7 +933,7 @@ void plan_tg(TgEpilogue epi, TgLaunch &L) {
         };
         const double whole = rounds * (all * load(f.held) + each);
         for (int split = 1; split <= 32; ++split) {
-            const int per = (all + split - 1) / split;
+            const int per = (all / 2 + split - 1) / split * 2;
             if (split > 1 && (per < 8 || rest == 0)) break;
             if ((all + per - 1) / per != split) continue;
             const int64_t on = (rest * split + cus - 1) / cus, full = on / f.held, left = on % f.held;

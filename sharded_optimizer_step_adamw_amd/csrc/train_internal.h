@@ -24,7 +24,7 @@ struct TgOperand {
 
 struct TgSegment {
     TgOperand a, b;
-    int32_t stages;    // ceil(max(a.k, b.k) / 32)
+    int32_t stages;    // max(a.k, b.k) / 32, up to an even number
 };
 
 // What becomes of a tile:
