@@ -895,26 +895,26 @@ hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
 // figures measured on the card (256 CUs):
 //   stage   one workgroup alone on its CU takes `alone` a stage of 32, bound by
 //           latency; a CU with all it holds (`held` of them) held * across, or
-//           held * along with both operands row-major: their rows come in 64
-//           byte pieces, half a cache line each, which is what the smaller
-//           tiles' loads are bound by then
+//           held * along with both operands row-major (256 x 128 tiles, whose
+//           three buffers hold no pairs of stages, load halves of lines then)
 //   tile    its first loads and its epilogue: `plain`, or `heavy` with
 //           exponentials
 //   split   a second launch (4) and 8 bytes an output and part at 5 TB/s
 // Full rounds of tiles are computed whole; those left over, which would leave
 // CUs idle, may be split along the reduction: [256, 50304] x [50304, 768]
 // takes 1.05 ms whole on 256 x 256 tiles, 0.18 ms in 16 parts on 128 x 128.
-// Over 60 calls of drawn sizes each forced to one kind of tile, the choice took
-// at most 5% longer than the best of the four but for two (10%).
+// Over 70 calls of drawn sizes each forced to one kind of tile, the choice took
+// at most 5% longer than the best of the four but for six (6 to 13%, all but
+// one of them under 100 us).
 void plan_tg(TgEpilogue epi, TgLaunch &L) {
     struct Figures {
         int tile, bm, bn, held;
         double alone, across, along, plain, heavy;
     };
-    static constexpr Figures figures[4] = {{kTile256, 256, 256, 1, 0.66, 0.86, 0.86, 4.0, 10.0},
-                                           {kTile256x128, 256, 128, 2, 0.46, 0.485, 0.55, 3.0, 8.0},
-                                           {kTile128, 128, 128, 2, 0.27, 0.25, 0.33, 2.0, 7.0},
-                                           {kTile64, 64, 64, 4, 0.17, 0.13, 0.13, 1.5, 6.0}};
+    static constexpr Figures figures[4] = {{kTile256, 256, 256, 1, 0.66, 0.86, 0.80, 4.0, 10.0},
+                                           {kTile256x128, 256, 128, 2, 0.46, 0.485, 0.60, 3.0, 8.0},
+                                           {kTile128, 128, 128, 2, 0.27, 0.25, 0.28, 2.0, 7.0},
+                                           {kTile64, 64, 64, 4, 0.17, 0.13, 0.12, 1.5, 6.0}};
     constexpr int64_t cus = 256;
     const bool glu = epi == kTgGlu || epi == kTgGluBack;
     int all = L.prob[0].seg[0].stages;
@@ -927,8 +927,9 @@ void plan_tg(TgEpilogue epi, TgLaunch &L) {
         const bool plain = epi == kTgStore || epi == kTgSum;
         const double each = plain ? f.plain : f.heavy, busy = plain ? f.across : f.along;
         auto load = [&](int64_t n) {
-            // (one on each of few CUs is not held up by the others)
-            const bool few = n == 1 && (f.held > 1 || tiles < cus / 2);
+            // (one on each of few CUs is not held up by the others; nor, across
+            // lines, one where two would fit)
+            const bool few = n == 1 && ((plain && f.held > 1) || tiles < cus / 2);
             return few || f.alone > n * busy ? f.alone : n * busy;
         };
         const double whole = rounds * (all * load(f.held) + each);
