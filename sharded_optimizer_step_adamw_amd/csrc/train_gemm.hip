@@ -412,8 +412,8 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, i
 //
 // Bound by the matrix cores and by a stage's synchronisation: measured on the
 // 8192-token products of a 4096 x 14336 block, 256 x 256 tiles run at 1.27
-// PFLOP/s with both operands k-major (1.51 ms), 1.35 with B alone (1.42 ms), 1.20
-// with the gate's epilogue and checkpoints (1.60 ms); matrix cores 66% busy at
+// PFLOP/s with both operands k-major (1.51 ms), 1.35 with B alone (1.42 ms), 1.30
+// with the gate's epilogue and checkpoints (1.48 ms); matrix cores 66% busy at
 // 1.95 GHz, LDS 25%, no bank conflicts.  A library product of the same sizes
 // reaches 1.17, 1.38 and (alone, without an epilogue) 1.53.  Measured without
 // gain: fragment reads late, early or opposite in the two waves of a SIMD (all
