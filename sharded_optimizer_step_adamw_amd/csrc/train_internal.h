@@ -222,9 +222,11 @@ struct TgActValue {
 __device__ __forceinline__ TgActValue tg_act(float g, int32_t act) {
     float y = g, dy = 1.0f;
     if (act == kActGelu) {
-        const float k = 1.5957691216057308f;
-        const float g2 = g * g;
-        y = k * (g + 0.044715f * (g2 * g));
+        // (beyond +-16 s is 1 or 0 to every bit and s (1 - s) is 0; the polynomials
+        // end there, since an infinite dy times that 0 would be NaN)
+        const float k = 1.5957691216057308f, b = __builtin_amdgcn_fmed3f(g, -16.0f, 16.0f);
+        const float g2 = b * b;
+        y = k * (b + 0.044715f * (g2 * b));
         dy = k * (1.0f + 0.134145f * g2);
     }
     const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-y));
