@@ -625,7 +625,11 @@ class _On:
     def empty(self, shape, dtype):
         if not self.other:
             return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(torch.cuda.ExternalStream(self.handle, device=self.device)):
+        # (the default stream's handle is 0, and an ExternalStream of 0 is a new
+        # stream of torch's own pool, whose memory the call does not order)
+        stream = (torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else
+                  torch.cuda.default_stream(self.device))
+        with torch.cuda.stream(stream):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
 
