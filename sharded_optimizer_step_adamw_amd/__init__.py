@@ -622,15 +622,21 @@ class _On:
         self.handle = current if stream is None else _stream(device, stream)
         self.other = self.handle != current
 
-    def empty(self, shape, dtype):
+    def empty(self, shape, dtype, ld=None):
+        """(ld: the row stride of a matrix, its width if not given)"""
         if not self.other:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return self._empty(shape, dtype, ld)
         # (the default stream's handle is 0, and an ExternalStream of 0 is a new
         # stream of torch's own pool, whose memory the call does not order)
         stream = (torch.cuda.ExternalStream(self.handle, device=self.device) if self.handle else
                   torch.cuda.default_stream(self.device))
         with torch.cuda.stream(stream):
+            return self._empty(shape, dtype, ld)
+
+    def _empty(self, shape, dtype, ld):
+        if ld is None or ld == shape[1]:
             return torch.empty(shape, dtype=dtype, device=self.device)
+        return torch.empty_strided(shape, (ld, 1), dtype=dtype, device=self.device)
 
 
 def _sized(fn, args, where, on, workspace):
@@ -825,13 +831,16 @@ def glu_backward(dh, x, w_gate, w_up, act: str = "silu", checkpoint=None,
     on = _On(dev, stream)
     if dx is None:
         dx = on.empty((T, D), torch.bfloat16)
+    # (the weight gradients have one row stride; one that is not given takes the other's)
+    lddw = D
+    for t, name in ((dw_up, "dw_up"), (dw_gate, "dw_gate")):
+        if t is not None:
+            lddw = _need_rows(t, torch.bfloat16, F, D, name, dev)
     if dw_gate is None:
-        dw_gate = on.empty((F, D), torch.bfloat16)
+        dw_gate = on.empty((F, D), torch.bfloat16, lddw)
     if dw_up is None:
-        dw_up = torch.empty_strided(dw_gate.shape, dw_gate.stride(), dtype=torch.bfloat16,
-                                    device=dev) if not on.other else on.empty((F, D), torch.bfloat16)
+        dw_up = on.empty((F, D), torch.bfloat16, lddw)
     lddx = _need_rows(dx, torch.bfloat16, T, D, "dx", dev)
-    lddw = _need_rows(dw_gate, torch.bfloat16, F, D, "dw_gate", dev)
     if _need_rows(dw_up, torch.bfloat16, F, D, "dw_up", dev) != lddw:
         raise ValueError("dw_up: row stride differs from dw_gate's")
     ldh = F if h is None else _need_rows(h, torch.bfloat16, T, F, "h", dev)
