@@ -553,9 +553,13 @@ def muon_groups_output_view(workspace: torch.Tensor, shapes: Sequence[tuple], ns
     return workspace.view(torch.bfloat16).as_strided((rows, cols), (ld.value, 1), off // 2)
 
 
-__all__ = ["adamw_shard_step", "muon_step", "muon_workspace_bytes", "muon_output_view",
-           "muon_step_groups", "muon_groups_workspace_bytes", "muon_groups_output_view",
-           "round_bf16", "shard_len", "lib", "ZoptError", "LIB_PATH", "MAX_BATCH", "MAX_GROUPS"]
+__all__ = ["adamw_shard_step", "adamw_shard_step_clipped", "grad_sq_norm", "grad_sq_norm_noalloc",
+           "grad_sq_norm_workspace_bytes", "grad_clip_stats", "muon_step", "muon_workspace_bytes",
+           "muon_output_view", "muon_step_groups", "muon_groups_workspace_bytes",
+           "muon_groups_output_view", "MuonGraph", "set_ns_workgroup_limit", "set_ns_form",
+           "linear_xent_loss", "linear_xent_grad", "glu_forward", "glu_backward", "act8_pack",
+           "act8_unpack", "act8_wgrad", "Act8", "ACTIVATIONS", "round_bf16", "shard_len", "lib",
+           "ZoptError", "LIB_PATH", "MAX_BATCH", "MAX_GROUPS"]
 
 
 # ------------------------------------------------------ operators of the gradients
