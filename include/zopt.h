@@ -21,8 +21,8 @@
  *    taking its gradient scale from them in device memory;
  *
  * and the operators that produce its gradients where memory is shortest:
- * zopt_linear_xent (a vocabulary projection's loss and gradients without the
- * logits), zopt_glu_forward / zopt_glu_backward (the gated feed-forward) and
+ * zopt_linear_xent (a vocabulary projection's loss and gradients; the caller
+ * holds no logits), zopt_glu_forward / zopt_glu_backward (the gated feed-forward) and
  * zopt_act8_* (activation checkpoints in 8 bits).
  *
  * Conventions common to every call
@@ -627,17 +627,20 @@ zopt_status zopt_set_ns_form(int32_t form);
 
 /*
  * zopt_linear_xent -- softmax cross entropy of a vocabulary projection, with
- * its gradients, without the logits:
+ * its gradients, from x and w (the caller forms and holds no logits):
  *   z_tv  = sum_d x_td w_vd                         (fp32, never stored)
  *   row_t = log sum_v exp(z_tv) - z_t,target        (0 for ignored rows)
  *   loss  = s sum_t row_t,   s = 1, or 1 / (rows not ignored) with mean = 1
  *                            (0 where every row is ignored)
  *   P_tv  = softmax(z_t)_v - [v = target_t]         (0 for ignored rows)
  *   dx    = s grad_scale P w,   dw = s grad_scale P^T x
- * Rows are taken in pieces whose exponentials fill at most 2 GiB of the
- * workspace; they are kept there in 16 bits (fp16, relative to the largest of
- * 64 neighbouring logits), so that each of the call's three products is
- * computed once.  P is rounded to bf16 for the last two.
+ * With a gradient the workspace holds an exponential for every logit of a
+ * piece of rows, in 16 bits (fp16, relative to the largest of 64 neighbouring
+ * logits): as much as the piece's logits in bf16 would take, at most 2 GiB, so
+ * that each of the call's three products is computed once.  The loss alone
+ * keeps none.  P is rounded to bf16 for the last two products; the error of dx
+ * and dw is about 1.2 times that of one rounding to bf16.  No row's loss is
+ * negative.
  *
  * Arguments
  *   x       bf16 [T, D], row stride ldx.     w   bf16 [V, D], row stride ldw.

@@ -24,9 +24,12 @@ Entry points (same names as the C ABI in include/zopt.h):
   grad_clip_stats    clip statistics (device scalars) from summed squares
   adamw_shard_step_clipped   AdamW taking grad_scale from the clip statistics
   linear_xent_loss / linear_xent_grad   cross entropy of a vocabulary projection,
-                     alone or with its gradients, without the logits (zopt_linear_xent)
+                     alone or with its gradients, from x and w (zopt_linear_xent)
   glu_forward / glu_backward   the gated feed-forward block's gate / up part
   act8_pack / act8_unpack / act8_wgrad   activation checkpoints in 8 bits (Act8)
+
+Every entry point stands outside autograd: it records nothing, whatever
+requires_grad says of its arguments, and the caller passes gradients on.
 """
 from __future__ import annotations
 
@@ -783,7 +786,7 @@ def glu_forward(x, w_gate, w_up, act: str = "silu", checkpoint=False,
                 stream=None):
     """h = act(x w_gate^T) * (x w_up^T), bf16 [T, F] (zopt_glu_forward): x bf16
     [T, D], w_gate and w_up bf16 [F, D] with one row stride, act "silu" or
-    "gelu" (tanh form).  With checkpoint=True, or a pair of Act8 to fill,
+    "gelu" (the tanh form, torch's approximate="tanh").  With checkpoint=True, or a pair of Act8 to fill,
     returns (h, (g, u)) with the two products kept in 8 bits for
     glu_backward."""
     ldx = _need_rows(x, torch.bfloat16, None, None, "x")

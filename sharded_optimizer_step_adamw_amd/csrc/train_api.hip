@@ -20,9 +20,10 @@ constexpr int64_t kMaxSide = 1 << 21;          // D, F, V: a 256-row panel stays
 constexpr int64_t kMaxRows = 1 << 30;          // T
 constexpr int64_t kMaxStride = (1 << 22) - 8;  // of an operand read in place
 // Exponentials of the logits held at once (2 GiB, under 1% of the 288 GB).
-// Rows are taken in as few pieces as that allows: every piece after the first
-// reads and writes the fp32 sums of dW once (8 V D bytes), and 8192 rows of a
-// 131072-word vocabulary are one piece.
+// Rows are taken in as few pieces as that allows, since every piece after the
+// first reads and writes the fp32 sums of dW once (8 V D bytes) and reads w
+// again: [16384, 4096] x 131072 words takes 42.5 ms in two pieces, half of its rows
+// 21.0 in one; [8192, 4096] x 262144 words 43.7 in two, half of its rows 21.3.
 constexpr int64_t kPieceBytes = (int64_t)1 << 31;
 
 inline int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -306,8 +307,9 @@ ZOPT_EXPORT zopt_status zopt_linear_xent(int64_t T, int64_t D, int64_t V, const 
     float *zt = reinterpret_cast<float *>(ws + p.zt);
     const TgTotal total{row, target, T, ignore_index, mean, loss};
     // Exponentials beyond twice the memory-side cache go past the caches: for
-    // [8192, 768] x 50304 (824 MB) the pass that makes them takes 51 us less of
-    // 790 so, the one that turns them into probabilities 23 us less of 350.
+    // [8192, 768] x 50304 (824 MB) the pass that turns them into probabilities
+    // takes 320 us so and 372 otherwise, the product after it 528 and 556, the one
+    // that makes them 682 and 685.
     const int32_t past = p.piece * p.lde * 2 > 2 * kCacheBytes;
     for (int32_t k = 0; k < p.pieces; ++k) {
         const int64_t r0 = k * p.piece, n = T - r0 < p.piece ? T - r0 : p.piece;

@@ -105,8 +105,8 @@ __device__ __forceinline__ uint32_t quad_umax(uint32_t v) {
 // with |m| (a multiply-add z log2 e - m log2 e, one operation less, is off by
 // 2^-24 of |m| log2 e: losses of sure rows down to -8e-5 at |m| = 2048).
 // Bound by the vector units and the stores: on [8192, 768] x [768, 50304] the
-// products alone take 0.50 ms, the statistics 0.09 more (half of it the
-// exponentials, at a quarter of the rate), the 824 MB of e 0.08 to 0.14.
+// products alone take 0.46 ms, the statistics 0.09 more (half of it the
+// exponentials, at a quarter of the rate), the 824 MB of e 0.12.
 // target: those of the lane's rows, or -1 (a column that does not exist).
 template <int FM>
 __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[FM][4], int R0, int C0,
@@ -414,11 +414,12 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, i
 // those.  Each is waited for within the stage's body.
 //
 // Bound by the matrix cores and by a stage's synchronisation: measured on the
-// 8192-token products of a 4096 x 14336 block, 256 x 256 tiles run at 1.27
-// PFLOP/s with both operands k-major (1.51 ms), 1.35 with B alone (1.42 ms), 1.30
-// with the gate's epilogue and checkpoints (1.48 ms); matrix cores 66% busy at
-// 1.95 GHz, LDS 25%, no bank conflicts.  A library product of the same sizes
-// reaches 1.17, 1.38 and (alone, without an epilogue) 1.53.  Measured without
+// 8192-token products of a 4096 x 14336 block, 256 x 256 tiles run at 1.29
+// PFLOP/s with both operands k-major (1.50 ms), 1.37 with B alone (1.41 ms), 1.32
+// with the gate's epilogue and checkpoints (1.45 ms); by counters the matrix cores
+// are 63%, 67% and 64% busy at 2.0 to 2.1 GHz, LDS 24 to 25%, no bank conflicts.
+// A library product of the same sizes reaches 1.20, 1.41 and (alone, without an
+// epilogue) 1.57.  Measured without
 // gain: fragment reads late, early or opposite in the two waves of a SIMD (all
 // within 1%), XCDs started at different times, two 256 x 128 workgroups a CU
 // for large products (1.5 times the operand traffic: 9.0 ms for 7.0 on
@@ -905,7 +906,8 @@ hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
 //   split   a second launch (4) and 8 bytes an output and part at 5 TB/s
 // Full rounds of tiles are computed whole; those left over, which would leave
 // CUs idle, may be split along the reduction: [256, 50304] x [50304, 768]
-// takes 1.05 ms whole on 256 x 256 tiles, 0.18 ms in 16 parts on 128 x 128.
+// takes 937 us whole on 256 x 256 tiles, 54 us in 16 parts on 128 x 128, 39 us in
+// the 21 parts that this chooses.
 // Over 70 calls of drawn sizes each forced to one kind of tile, the choice took
 // at most 5% longer than the best of the four but for six (6 to 13%, all but
 // one of them under 100 us).
@@ -918,7 +920,7 @@ void plan_tg(TgEpilogue epi, TgLaunch &L) {
                                            {kTile256x128, 256, 128, 2, 0.46, 0.485, 0.60, 3.0, 8.0},
                                            {kTile128, 128, 128, 2, 0.27, 0.25, 0.28, 2.0, 7.0},
                                            {kTile64, 64, 64, 4, 0.17, 0.13, 0.12, 1.5, 6.0}};
-    constexpr int64_t cus = 256;
+    constexpr int64_t cus = 256;  // (the figures' card; a launch takes the device's own count)
     const bool glu = epi == kTgGlu || epi == kTgGluBack;
     int all = L.prob[0].seg[0].stages;
     if (!glu && L.prob[0].nseg > 1) all += L.prob[0].seg[1].stages;

@@ -44,8 +44,8 @@ __global__ __launch_bounds__(kThreads) void fill_zero_kernel(uint16_t *__restric
 }
 
 // 8-bit checkpoints: four neighbouring threads hold a block of 32 values,
-// eight each.  Bound by HBM: 5.5 TB/s on [8192, 14336] (65 us); reading back,
-// with the 8-bit side still cached, 55 us.
+// eight each.  Bound by HBM: 5.2 to 5.5 TB/s on [8192, 14336] (64 to 69 us);
+// reading back, with the 8-bit side still cached, 55 us.
 template <bool PAST>
 __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__restrict__ x, int64_t ld, int64_t rows,
                                                              int64_t cols, uint8_t *__restrict__ q,
