@@ -235,11 +235,11 @@ def grad_sq_norm(grad, n, bucket, world, rank, out: Optional[torch.Tensor] = Non
     dev = grad.device
     _need(grad, torch.bfloat16, n, "grad")
     if out is None:
-        out = torch.empty(1, dtype=torch.float64, device=dev)
+        out = _On(dev, stream).empty(1, torch.float64)
     _need(out, torch.float64, 1, "out", dev)
     need = grad_sq_norm_workspace_bytes(n, bucket, world, rank)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _On(dev, stream).empty(need, torch.uint8)
     _need(workspace, torch.uint8, need, "workspace", dev)
     size = ctypes.c_size_t(workspace.numel())
     st = lib().zopt_grad_sq_norm(grad.data_ptr(), n, bucket, world, rank,
@@ -272,7 +272,7 @@ def grad_clip_stats(sq: torch.Tensor, max_norm: float, inv_scale: float = 1.0,
     dev = sq.device
     _need(sq, torch.float64, 1, "sq")
     if out is None:
-        out = torch.empty(CLIP_STATS, dtype=torch.float32, device=dev)
+        out = _On(dev, stream).empty(CLIP_STATS, torch.float32)
     _need(out, torch.float32, CLIP_STATS, "out", dev)
     st = lib().zopt_grad_clip_stats(sq.data_ptr(), sq.numel(), max_norm, inv_scale,
                                     out.data_ptr(), _stream(dev, stream))
@@ -359,7 +359,7 @@ def muon_step(master: Sequence[torch.Tensor], momentum: Sequence[torch.Tensor],
                     shape, dev)
     need = muon_workspace_bytes(batch, rows, cols)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _On(dev, stream).empty(need, torch.uint8)
     _need(workspace, torch.uint8, need, "workspace", dev)
     size = ctypes.c_size_t(workspace.numel())
     a, b, c = (float(x) for x in ns_coeffs)
@@ -426,7 +426,7 @@ def muon_step_groups(groups: Sequence[tuple], lr: float, momentum_beta: float = 
     shapes, M, Mo, G, W, with_w, dev = _muon_group_tables(groups)
     need = muon_groups_workspace_bytes(shapes)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = _On(dev, stream).empty(need, torch.uint8)
     _need(workspace, torch.uint8, need, "workspace", dev)
     n, b, r, c = _shape_arrays(shapes)
     size = ctypes.c_size_t(workspace.numel())
