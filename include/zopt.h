@@ -23,7 +23,9 @@
  * and the operators that produce its gradients where memory is shortest:
  * zopt_linear_xent (a vocabulary projection's loss and gradients; the caller
  * holds no logits), zopt_glu_forward / zopt_glu_backward (the gated feed-forward) and
- * zopt_act8_* (activation checkpoints in 8 bits).
+ * zopt_act8_* (activation checkpoints in 8 bits); zopt_qk_norm_rope (norms and
+ * rotation of queries and keys) and zopt_moe_* (routing to experts and the
+ * experts' gated feed-forward), forward and backward.
  *
  * Conventions common to every call
  * --------------------------------
@@ -748,6 +750,204 @@ zopt_status zopt_glu_backward(int64_t T, int64_t D, int64_t F, const uint16_t *d
                               const uint8_t *g_scale, const uint8_t *u8, const uint8_t *u_scale,
                               uint16_t *h, int64_t ldh, uint16_t *dx, int64_t lddx,
                               uint16_t *dw_gate, uint16_t *dw_up, int64_t lddw, void *workspace,
+                              size_t *workspace_bytes, void *stream);
+
+/*
+ * A decoder layer's other operators: norms and rotation of queries and keys,
+ * and a feed-forward of experts.  The conventions of the gradient operators
+ * above hold, but for what is said here.
+ */
+
+/* Which elements of a head turn together. */
+enum {
+    ZOPT_ROPE_HALF = 0, /* i and i + rot / 2, i < rot / 2 */
+    ZOPT_ROPE_PAIRS = 1 /* 2 i and 2 i + 1                */
+};
+
+/*
+ * zopt_rope_table -- the cosines and sines of the angles
+ *   angle(p, i) = p base^(-2 i / rot),   p < positions, i < rot / 2
+ * formed in 64 bits: table, float [positions, rot / 2, 2], written.  A program
+ * makes it once; any other table of that layout (scaled angles, say) will do.
+ * positions 0 .. 2^30 (0 enqueues nothing); rot even, 2 .. 512; base > 0.
+ * Errors: ZOPT_ERR_SIZE; ZOPT_ERR_HYPER (base); ZOPT_ERR_NULL; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_rope_table(int64_t positions, int32_t rot, double base, float *table,
+                            void *stream);
+
+/*
+ * zopt_qk_norm_rope -- the norm of every head of the queries and keys, and the
+ * rotation of its first `rot` elements to its token's position, in one pass:
+ *   n = x / sqrt(mean(x^2) + eps),   y = n w
+ *   (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)
+ * for each pair (a, b) of ZOPT_ROPE_*, (c, s) its angle's cosine and sine.
+ *   T         tokens, 0 .. 2^30 (0 enqueues nothing).
+ *   heads_q, heads_k   1 .. 65536 and 0 .. 65536 heads of `width` elements,
+ *             1 .. 512; 0: no keys, and k, yk are not looked at.
+ *   rot       even, 0 .. width; 0: the norm alone.
+ *   q, k      bf16 [T, heads, width]; *_token and *_head are the strides
+ *             between tokens and between heads, 0 .. 2^40, so that both may be
+ *             views of one projection [T, (heads_q + 2 heads_k) width], or lie
+ *             head by head.
+ *   table     float [positions, rot / 2, 2].
+ *   position  int64 [T], device; NULL: token t has position t.  A row with a
+ *             negative position takes no part: its output is zero.  One with a
+ *             position that the table does not hold is NaN.
+ *   w_q, w_k  bf16 [width], one for all heads of a kind; NULL: 1.
+ *   eps       finite, >= 0.     style   ZOPT_ROPE_*.
+ *   yq, yk    bf16 [T, heads, width], written; their heads may not overlap.
+ *             yq may be q, with the same strides, and yk k.
+ * Norms and sums are held in fp32; the only rounding to bf16 is the output's.
+ * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE (sizes, strides); ZOPT_ERR_HYPER (eps,
+ * style); ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_qk_norm_rope(int64_t T, int32_t heads_q, int32_t heads_k, int32_t width,
+                              int32_t rot, const uint16_t *q, int64_t q_token, int64_t q_head,
+                              const uint16_t *k, int64_t k_token, int64_t k_head,
+                              const float *table, int64_t positions, const int64_t *position,
+                              const uint16_t *w_q, const uint16_t *w_k, float eps,
+                              int32_t style, uint16_t *yq, int64_t yq_token, int64_t yq_head,
+                              uint16_t *yk, int64_t yk_token, int64_t yk_head, void *stream);
+
+/*
+ * zopt_qk_norm_rope_backward -- its gradients, from those of yq and yk and from
+ * the forward's inputs:
+ *   g = dy turned back,   dw = sum over tokens and heads of g n
+ *   dx = (g w - n mean(g w n)) / sqrt(mean(x^2) + eps)
+ *   dyq, dyk  bf16 [T, heads, width].    dq, dk   the same, written; dq may be
+ *             dyq or q with the same strides, dk dyk or k.
+ *   dw_q, dw_k  bf16 [width], written (zero for T = 0); NULL: not wanted.
+ * Rows without a position get zero gradients and no share of dw.
+ * Errors: as zopt_qk_norm_rope, dw_k without keys being ZOPT_ERR_NULL;
+ * ZOPT_ERR_WORKSPACE.
+ */
+zopt_status zopt_qk_norm_rope_backward(
+    int64_t T, int32_t heads_q, int32_t heads_k, int32_t width, int32_t rot, const uint16_t *dyq,
+    int64_t dyq_token, int64_t dyq_head, const uint16_t *dyk, int64_t dyk_token,
+    int64_t dyk_head, const uint16_t *q, int64_t q_token, int64_t q_head, const uint16_t *k,
+    int64_t k_token, int64_t k_head, const float *table, int64_t positions,
+    const int64_t *position, const uint16_t *w_q, const uint16_t *w_k, float eps, int32_t style,
+    uint16_t *dq, int64_t dq_token, int64_t dq_head, uint16_t *dk, int64_t dk_token,
+    int64_t dk_head, uint16_t *dw_q, uint16_t *dw_k, void *workspace, size_t *workspace_bytes,
+    void *stream);
+
+/* What a router's logits are made into. */
+enum {
+    ZOPT_SCORE_SOFTMAX = 0, /* softmax over the experts   */
+    ZOPT_SCORE_SIGMOID = 1  /* the logistic of each logit */
+};
+
+/*
+ * zopt_moe_route -- from a router's logits to each token's experts and weights,
+ * and to the order in which the experts read the tokens.
+ *   s = score(logits);  an expert ranks by s + bias (by its logit, which ranks
+ *   the same, without a bias and groups), of equal ones the lower first
+ *   with groups > 1 the experts lie in `groups` equal ranges, a range ranks by
+ *   the sum of its two best, and only the best `top_groups` are chosen from
+ *   weight = scale s, or (renormalise) scale s / (sum of s over the chosen);
+ *   the bias has no part in it
+ * An expert whose logit or bias is -inf is not there: where fewer than `top`
+ * are, a token's last experts are -1 with weight 0 (a row of -inf: all of them),
+ * and the token takes no part in the products there.  A NaN ranks behind every
+ * number.  Ranks are settled in 64 bits.
+ *   T         tokens, 0 .. 2^30, with T top <= 2^30.
+ *   experts   1 .. 1024.      top   1 .. min(experts, 32).
+ *   logits    fp32 (bf16 = 0) or bf16 (1) [T, experts], row stride ld.
+ *   score     ZOPT_SCORE_*.   bias   float [experts], or NULL.
+ *   groups    1 .. 64, a divisor of experts; top_groups 1 .. groups, with at
+ *             least `top` experts in them.
+ *   renormalise   0 or 1.     scale   finite.
+ *   chosen, weights   int32 and float [T, top], written, the best first.
+ *   offsets   int32 [experts + 1], written: a slot is one of a token's `top`,
+ *             number t top + j; the slots of expert e are order[offsets[e]] ..
+ *             order[offsets[e + 1] - 1], in order.
+ *   order     int32 [T top], written; -1 from offsets[experts] on.
+ *   place     int32 [T, top], written: where a slot is in order, or -1.
+ * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE; ZOPT_ERR_HYPER (bf16, score,
+ * renormalise, scale); ZOPT_ERR_WORKSPACE; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_moe_route(int64_t T, int32_t experts, int32_t top, const void *logits,
+                           int64_t ld, int32_t bf16, int32_t score, const float *bias,
+                           int32_t groups, int32_t top_groups, int32_t renormalise, float scale,
+                           int32_t *chosen, float *weights, int32_t *offsets, int32_t *order,
+                           int32_t *place, void *workspace, size_t *workspace_bytes,
+                           void *stream);
+
+/*
+ * zopt_moe_plan -- offsets, order and place of zopt_moe_route for experts that
+ * the caller chose: chosen, int32 [T, top], any number outside [0, experts)
+ * standing for none, the same expert more than once in a row counting as often.
+ * Other arguments and errors as there, but top may be more than experts.
+ */
+zopt_status zopt_moe_plan(int64_t T, int32_t experts, int32_t top, const int32_t *chosen,
+                          int32_t *offsets, int32_t *order, int32_t *place, void *workspace,
+                          size_t *workspace_bytes, void *stream);
+
+/*
+ * zopt_moe_route_backward -- the gradient of the logits from that of the
+ * weights, dweights float [T, top] (entries of slots without an expert are not
+ * looked at).  logits, ld, bf16, score, renormalise and scale as the forward
+ * had them, chosen as it wrote them; dlogits, in the logits' type, row stride
+ * lddl, written whole.  Choice and bias have no gradient.
+ * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE; ZOPT_ERR_HYPER; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_moe_route_backward(int64_t T, int32_t experts, int32_t top,
+                                    const float *dweights, const void *logits, int64_t ld,
+                                    int32_t bf16, int32_t score, int32_t renormalise,
+                                    float scale, const int32_t *chosen, void *dlogits,
+                                    int64_t lddl, void *stream);
+
+/*
+ * zopt_moe_forward -- the experts' gated feed-forward:
+ *   h_s = act(x_t w_gate[e]^T) (x_t w_up[e]^T)      for slot s of token t, expert e
+ *   y_t = sum over t's slots of weight_s (h_s w_down[e]^T)
+ *   x             bf16 [T, D], row stride ldx.  Rows of tokens without an expert
+ *                 are not read; their y is zero.
+ *   w_gate, w_up  bf16 [experts, F, D], both with row stride ldw and w_expert
+ *                 elements between experts (which do not overlap).
+ *   w_down        bf16 [experts, D, F], ldd and wd_expert.
+ *   act           ZOPT_ACT_*.
+ *   weights       float [T, top];  offsets, order, place   as zopt_moe_route or
+ *                 zopt_moe_plan wrote them for T, experts and top <= 32.
+ *                 (Others give wrong sums, but no access outside the buffers.)
+ *   y             bf16 [T, D], row stride ldy, written.
+ * The sizes of the experts' shares stay on the device: nothing waits for them.
+ * h and a slot's row of y are rounded to bf16 (8 bits: as a dense layer's h and
+ * output are), sums are fp32.
+ * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE; ZOPT_ERR_HYPER (act);
+ * ZOPT_ERR_WORKSPACE; ZOPT_ERR_DEVICE.
+ */
+zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_t experts, int32_t top,
+                             const uint16_t *x, int64_t ldx, const uint16_t *w_gate,
+                             const uint16_t *w_up, int64_t ldw, int64_t w_expert,
+                             const uint16_t *w_down, int64_t ldd, int64_t wd_expert, int32_t act,
+                             const float *weights, const int32_t *offsets, const int32_t *order,
+                             const int32_t *place, uint16_t *y, int64_t ldy, void *workspace,
+                             size_t *workspace_bytes, void *stream);
+
+/*
+ * zopt_moe_backward -- gradients of zopt_moe_forward from dy, bf16 [T, D], row
+ * stride lddy; g, u and h are computed again from x:
+ *   dx            bf16 [T, D], row stride lddx (zero for tokens without an expert).
+ *   dw_gate, dw_up   bf16 [experts, F, D], row stride lddw, dw_expert elements
+ *                 between experts;  dw_down   bf16 [experts, D, F], lddd and
+ *                 dwd_expert; zero for experts without a token.
+ *   dweights      float [T, top], 0 for slots without an expert.
+ * All are written.  A row of x and of dy whose token has no expert reaches
+ * none of them.  dg, du, weight h and a slot's row of dx are rounded to bf16
+ * between the products; dy w_down, and with it dweights, is kept in fp32.
+ * Other arguments and errors as zopt_moe_forward.
+ */
+zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32_t experts, int32_t top,
+                              const uint16_t *dy, int64_t lddy, const uint16_t *x, int64_t ldx,
+                              const uint16_t *w_gate, const uint16_t *w_up, int64_t ldw,
+                              int64_t w_expert, const uint16_t *w_down, int64_t ldd,
+                              int64_t wd_expert, int32_t act, const float *weights,
+                              const int32_t *offsets, const int32_t *order,
+                              const int32_t *place, uint16_t *dx, int64_t lddx,
+                              uint16_t *dw_gate, uint16_t *dw_up, int64_t lddw,
+                              int64_t dw_expert, uint16_t *dw_down, int64_t lddd,
+                              int64_t dwd_expert, float *dweights, void *workspace,
                               size_t *workspace_bytes, void *stream);
 
 #ifdef __cplusplus

@@ -27,6 +27,11 @@ Entry points (same names as the C ABI in include/zopt.h):
                      alone or with its gradients, from x and w (zopt_linear_xent)
   glu_forward / glu_backward   the gated feed-forward block's gate / up part
   act8_pack / act8_unpack / act8_wgrad   activation checkpoints in 8 bits (Act8)
+  qk_norm_rope / qk_norm_rope_backward   norms of queries and keys for each head with
+                     the rotation to their positions
+  rope_table         the rotation's cosines and sines (zopt_rope_table)
+  moe_route / moe_route_backward / moe_plan   routing of tokens to experts (Route)
+  moe_forward / moe_backward   the experts' gated feed-forward
 
 Every entry point stands outside autograd: it records nothing, whatever
 requires_grad says of its arguments, and the caller passes gradients on.
@@ -131,6 +136,25 @@ def _lib_or_raise() -> ctypes.CDLL:
         L.zopt_glu_backward.argtypes = [i64, i64, i64, vp, i64, vp, i64, vp, vp, vp, vp, i64, i32,
                                         vp, vp, vp, vp, vp, i64, vp, i64, vp, vp, i64, vp, size_p,
                                         vp]
+        L.zopt_rope_table.argtypes = [i64, i32, ctypes.c_double, vp, vp]
+        heads = [vp, i64, i64]
+        rope = [vp, i64, vp, vp, vp, f32, i32]
+        L.zopt_qk_norm_rope.argtypes = [i64, i32, i32, i32, i32, *heads * 2, *rope, *heads * 2, vp]
+        L.zopt_qk_norm_rope_backward.argtypes = [i64, i32, i32, i32, i32, *heads * 4, *rope,
+                                                 *heads * 2, vp, vp, vp, size_p, vp]
+        L.zopt_moe_route.argtypes = [i64, i32, i32, vp, i64, i32, i32, vp, i32, i32, i32, f32, vp, vp,
+                                     vp, vp, vp, vp, size_p, vp]
+        L.zopt_moe_plan.argtypes = [i64, i32, i32, vp, vp, vp, vp, vp, size_p, vp]
+        L.zopt_moe_route_backward.argtypes = [i64, i32, i32, vp, vp, i64, i32, i32, i32, f32, vp, vp,
+                                              i64, vp]
+        moe = [vp, i64, vp, vp, i64, i64, vp, i64, i64, i32, vp, vp, vp, vp]
+        L.zopt_moe_forward.argtypes = [i64, i64, i64, i32, i32, *moe, vp, i64, vp, size_p, vp]
+        L.zopt_moe_backward.argtypes = [i64, i64, i64, i32, i32, vp, i64, *moe, vp, i64, vp, vp, i64,
+                                        i64, vp, i64, i64, vp, vp, size_p, vp]
+        for f in (L.zopt_rope_table, L.zopt_qk_norm_rope, L.zopt_qk_norm_rope_backward,
+                  L.zopt_moe_route, L.zopt_moe_plan, L.zopt_moe_route_backward, L.zopt_moe_forward,
+                  L.zopt_moe_backward):
+            f.restype = ctypes.c_int
         for f in (L.zopt_linear_xent, L.zopt_act8_pack, L.zopt_act8_unpack, L.zopt_act8_wgrad,
                   L.zopt_glu_forward, L.zopt_glu_backward):
             f.restype = ctypes.c_int
@@ -561,7 +585,9 @@ __all__ = ["adamw_shard_step", "adamw_shard_step_clipped", "grad_sq_norm", "grad
            "muon_output_view", "muon_step_groups", "muon_groups_workspace_bytes",
            "muon_groups_output_view", "MuonGraph", "set_ns_workgroup_limit", "set_ns_form",
            "linear_xent_loss", "linear_xent_grad", "glu_forward", "glu_backward", "act8_pack",
-           "act8_unpack", "act8_wgrad", "Act8", "ACTIVATIONS", "round_bf16", "shard_len", "lib",
+           "act8_unpack", "act8_wgrad", "Act8", "ACTIVATIONS", "rope_table", "qk_norm_rope",
+           "qk_norm_rope_backward", "ROPE_STYLES", "moe_route", "moe_route_backward", "moe_plan",
+           "moe_forward", "moe_backward", "Route", "SCORES", "round_bf16", "shard_len", "lib",
            "ZoptError", "LIB_PATH", "MAX_BATCH", "MAX_GROUPS"]
 
 
@@ -856,3 +882,404 @@ def glu_backward(dh, x, w_gate, w_up, act: str = "silu", checkpoint=None,
                                      _ptr(dw_up), lddw),
            "zopt_glu_backward", on, workspace)
     return dx, dw_gate, dw_up
+
+
+# ------------------------------------------- a decoder layer's other operators
+
+ROPE_STYLES = {"half": 0, "pairs": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+class Route(NamedTuple):
+    """Where tokens go (zopt_moe_route): experts int32 and weights fp32 [T,
+    top], an expert of -1 being none; offsets int32 [experts + 1], order int32
+    [T top] and place int32 [T, top], the slots sorted by expert."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    offsets: torch.Tensor
+    order: torch.Tensor
+    place: torch.Tensor
+
+
+def _one_of(value, table, name):
+    if value not in table:
+        raise ValueError(f"{name}: {value!r}, need one of {sorted(table)}")
+    return table[value]
+
+
+def _need_heads(t, shape, name, device=None):
+    """Checks that t is a bf16 GPU tensor [tokens, heads, width] (None: any
+    size there) whose heads are contiguous; returns its first two strides."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, need {torch.bfloat16}")
+    if t.dim() != 3 or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need "
+                         f"{tuple('any' if s is None else s for s in shape)}")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: must be a GPU tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: strides {tuple(t.stride())}, need contiguous heads")
+    return t.stride(0), t.stride(1)
+
+
+def _need_vector(t, dtype, n, name, device) -> None:
+    if t is None:
+        return
+    _need(t, dtype, n, name, device)
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need ({n},)")
+
+
+def _on_device(device):
+    """The device of a call's tensors made the current one, where it is not."""
+    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else _SAME
+
+
+class _Same:
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        return False
+
+
+_SAME = _Same()
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda",
+               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fp32 [positions, rot / 2, 2]: cosine and sine of p base^(-2 i / rot)
+    (zopt_rope_table)."""
+    dev = torch.device(device) if out is None else out.device
+    if dev.type != "cuda":
+        raise ValueError("rope_table: must be on a GPU")
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty((positions, rot // 2, 2), torch.float32)
+    _need(out, torch.float32, positions * (rot // 2) * 2, "out", dev)
+    if tuple(out.shape) != (positions, rot // 2, 2):
+        raise ValueError(f"out: shape {tuple(out.shape)}, need {(positions, rot // 2, 2)}")
+    with _on_device(dev):
+        _check(lib().zopt_rope_table(positions, rot, float(base), _ptr(out), on.handle),
+               "zopt_rope_table")
+    return out
+
+
+def _rope_args(q, k, table, position, w_q, w_k, eps, style):
+    """(sizes, what q and k are, the other arguments)"""
+    qs = _need_heads(q, (None, None, None), "q")
+    T, hq, width = q.shape
+    dev = q.device
+    hk, ks = 0, (0, 0)
+    if k is not None:
+        ks = _need_heads(k, (T, None, width), "k", dev)
+        hk = k.shape[1]
+        if hk == 0:
+            raise ValueError("k: no heads")
+    if hq == 0 or width == 0:
+        raise ValueError(f"q: shape {tuple(q.shape)} has no heads")
+    positions, rot = 0, 0
+    if table is not None:
+        if table.dim() != 3 or table.shape[2] != 2:
+            raise ValueError(f"table: shape {tuple(table.shape)}, need (positions, rot / 2, 2)")
+        positions, rot = table.shape[0], 2 * table.shape[1]
+        _need(table, torch.float32, positions * rot, "table", dev)
+    if rot > width:
+        raise ValueError(f"table: turns {rot} elements of heads of {width}")
+    _need_vector(position, torch.int64, T, "position", dev)
+    _need_vector(w_q, torch.bfloat16, width, "w_q", dev)
+    _need_vector(w_k, torch.bfloat16, width, "w_k", dev)
+    rest = (_ptr(table), positions, _ptr(position), _ptr(w_q), _ptr(w_k), float(eps),
+            _one_of(style, ROPE_STYLES, "style"))
+    return (T, hq, hk, width, rot), (_ptr(q), *qs, _ptr(k), *ks), rest
+
+
+def qk_norm_rope(q, k, table, position=None, w_q=None, w_k=None, eps: float = 1e-6,
+                 style: str = "half", out_q: Optional[torch.Tensor] = None,
+                 out_k: Optional[torch.Tensor] = None, stream=None):
+    """Every head of q and k divided by its root mean square, times w_q / w_k,
+    its first elements turned to the token's position (zopt_qk_norm_rope): q
+    and k bf16 [T, heads, width] with any strides of tokens and heads (k None:
+    queries alone), table fp32 [positions, rot / 2, 2] (None: no rotation),
+    position int64 [T] (None: 0, 1, ...; negative: the row is zero), w_q and
+    w_k bf16 [width] or None, style "half" or "pairs".  Returns (yq, yk), bf16;
+    out_q may be q, and out_k k."""
+    sizes, heads, rest = _rope_args(q, k, table, position, w_q, w_k, eps, style)
+    dev = q.device
+    on = _On(dev, stream)
+    if out_q is None:
+        out_q = on.empty(tuple(q.shape), torch.bfloat16)
+    outs = (out_q.data_ptr(), *_need_heads(out_q, q.shape, "out_q", dev))
+    if k is None:
+        out_k, outs = None, (*outs, None, 0, 0)
+    else:
+        if out_k is None:
+            out_k = on.empty(tuple(k.shape), torch.bfloat16)
+        outs = (*outs, out_k.data_ptr(), *_need_heads(out_k, k.shape, "out_k", dev))
+    with _on_device(dev):
+        _check(lib().zopt_qk_norm_rope(*sizes, *heads, *rest, *outs, on.handle), "zopt_qk_norm_rope")
+    return out_q, out_k
+
+
+def qk_norm_rope_backward(dyq, dyk, q, k, table, position=None, w_q=None, w_k=None,
+                          eps: float = 1e-6, style: str = "half",
+                          dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                          dw_q: Optional[torch.Tensor] = None, dw_k: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dq, dk, dw_q, dw_k) of qk_norm_rope from those of its outputs
+    and its arguments (zopt_qk_norm_rope_backward); dw_q and dw_k are None
+    where there is no weight.  dq may be dyq, and dk dyk."""
+    sizes, heads, rest = _rope_args(q, k, table, position, w_q, w_k, eps, style)
+    dev = q.device
+    on = _On(dev, stream)
+    width = sizes[3]
+    ins, outs, grads = (), (), []
+    for x, dy, dx, w, dw, name in ((q, dyq, dq, w_q, dw_q, "q"), (k, dyk, dk, w_k, dw_k, "k")):
+        if x is None:
+            ins, outs = (*ins, None, 0, 0), (*outs, None, 0, 0)
+            grads += [None, None]
+            continue
+        ins = (*ins, dy.data_ptr() if isinstance(dy, torch.Tensor) else None,
+               *_need_heads(dy, x.shape, f"dy{name}", dev))
+        if dx is None:
+            dx = on.empty(tuple(x.shape), torch.bfloat16)
+        outs = (*outs, dx.data_ptr(), *_need_heads(dx, x.shape, f"d{name}", dev))
+        if w is None:
+            dw = None
+        elif dw is None:
+            dw = on.empty((width,), torch.bfloat16)
+        _need_vector(dw, torch.bfloat16, width, f"dw_{name}", dev)
+        grads += [dx, dw]
+    with _on_device(dev):
+        _sized(lib().zopt_qk_norm_rope_backward,
+               (*sizes, *ins, *heads, *rest, *outs, _ptr(grads[1]), _ptr(grads[3])),
+               "zopt_qk_norm_rope_backward", on, workspace)
+    return grads[0], grads[2], grads[1], grads[3]
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _need_logits(t, name, rows=None, cols=None, device=None, dtype=None):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype not in _LOGITS or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name}: dtype {t.dtype}, need {dtype or 'float32 or bfloat16'}")
+    return _need_rows(t, t.dtype, rows, cols, name, device)
+
+
+def _need_route(r, T, name, device):
+    """Checks a Route; returns (experts of the layer, experts of a token)."""
+    if not isinstance(r, Route):
+        raise TypeError(f"{name}: expected a Route")
+    if r.experts.dim() != 2 or (T is not None and r.experts.shape[0] != T):
+        raise ValueError(f"{name}.experts: shape {tuple(r.experts.shape)}, need "
+                         f"({'any' if T is None else T}, 'any')")
+    rows, top = r.experts.shape
+    _need(r.experts, torch.int32, rows * top, f"{name}.experts", device)
+    for t, dtype, shape, what in ((r.weights, torch.float32, (rows, top), "weights"),
+                                  (r.order, torch.int32, (rows * top,), "order"),
+                                  (r.place, torch.int32, (rows, top), "place")):
+        _need(t, dtype, rows * top, f"{name}.{what}", device)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{name}.{what}: shape {tuple(t.shape)}, need {shape}")
+    E = r.offsets.numel() - 1
+    _need_vector(r.offsets, torch.int32, max(E + 1, 2), f"{name}.offsets", device)
+    return E, top
+
+
+def _route_empty(T, E, top, on, experts=None, weights=None) -> Route:
+    return Route(on.empty((T, top), torch.int32) if experts is None else experts,
+                 on.empty((T, top), torch.float32) if weights is None else weights,
+                 on.empty((E + 1,), torch.int32), on.empty((T * top,), torch.int32),
+                 on.empty((T, top), torch.int32))
+
+
+def moe_route(logits, top: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
+              groups: int = 1, top_groups: int = 1, renormalise: bool = True, scale: float = 1.0,
+              out: Optional[Route] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> Route:
+    """Each token's `top` experts and their weights from logits, fp32 or bf16
+    [T, experts], with the order in which the experts read the tokens
+    (zopt_moe_route): score "softmax" or "sigmoid"; bias fp32 [experts] has a
+    part in the choice alone; experts in `groups` equal ranges of which the best
+    `top_groups` are chosen from; weights are scale * score, over the sum of the
+    chosen ones with renormalise.  An expert with logit -inf is not chosen."""
+    ld = _need_logits(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    _need_vector(bias, torch.float32, E, "bias", dev)
+    on = _On(dev, stream)
+    if out is None:
+        out = _route_empty(T, E, top, on)
+    if _need_route(out, T, "out", dev) != (E, top):
+        raise ValueError(f"out: a Route of other experts than {E}, {top}")
+    with _on_device(dev):
+        _sized(lib().zopt_moe_route,
+               (T, E, top, _ptr(logits), ld, _LOGITS[logits.dtype], _one_of(score, SCORES, "score"),
+                _ptr(bias), groups, top_groups, int(renormalise), float(scale), *map(_ptr, out)),
+               "zopt_moe_route", on, workspace)
+    return out
+
+
+def moe_plan(experts, weights, num_experts: int, workspace: Optional[torch.Tensor] = None,
+             stream=None) -> Route:
+    """A Route of experts that the caller chose (zopt_moe_plan): experts int32
+    [T, top], numbers outside [0, num_experts) standing for none, and weights
+    fp32 [T, top], which it holds as they are."""
+    if not isinstance(experts, torch.Tensor):
+        raise TypeError("experts: expected a tensor")
+    if experts.dim() != 2:
+        raise ValueError(f"experts: shape {tuple(experts.shape)}, need [tokens, top]")
+    T, top = experts.shape
+    dev = experts.device
+    _need(experts, torch.int32, T * top, "experts", dev)
+    if num_experts < 1:
+        raise ValueError(f"num_experts: {num_experts}")
+    on = _On(dev, stream)
+    out = _route_empty(T, num_experts, top, on, experts, weights)
+    _need_route(out, T, "route", dev)
+    with _on_device(dev):
+        _sized(lib().zopt_moe_plan, (T, num_experts, top, _ptr(experts), *map(_ptr, out[2:])),
+               "zopt_moe_plan", on, workspace)
+    return out
+
+
+def moe_route_backward(dweights, logits, route: Route, score: str = "softmax",
+                       renormalise: bool = True, scale: float = 1.0,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient of moe_route's logits, in their type, from dweights fp32 [T,
+    top] (zopt_moe_route_backward)."""
+    ld = _need_logits(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if _need_route(route, T, "route", dev)[0] != E:
+        raise ValueError(f"route: not of {E} experts")
+    top = route.experts.shape[1]
+    _need(dweights, torch.float32, T * top, "dweights", dev)
+    if tuple(dweights.shape) != (T, top):
+        raise ValueError(f"dweights: shape {tuple(dweights.shape)}, need {(T, top)}")
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty((T, E), logits.dtype)
+    ldo = _need_logits(out, "out", T, E, dev, logits.dtype)
+    with _on_device(dev):
+        _check(lib().zopt_moe_route_backward(T, E, top, _ptr(dweights), _ptr(logits), ld,
+                                             _LOGITS[logits.dtype], _one_of(score, SCORES, "score"),
+                                             int(renormalise), float(scale), _ptr(route.experts),
+                                             _ptr(out), ldo, on.handle), "zopt_moe_route_backward")
+    return out
+
+
+def _need_experts(t, E, rows, cols, name, device):
+    """Checks that t is a bf16 GPU tensor [E, rows, cols] (None: any size) whose
+    matrices have contiguous rows and do not overlap; returns the strides of
+    rows and of experts."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, need {torch.bfloat16}")
+    want = (E, rows, cols)
+    if t.dim() != 3 or any(w is not None and s != w for s, w in zip(t.shape, want)) or 0 in t.shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need "
+                         f"{tuple('any' if w is None else w for w in want)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    e, r, c = t.shape
+    ld = t.stride(1) if r > 1 else c
+    group = t.stride(0) if e > 1 else r * ld
+    if c > 1 and t.stride(2) != 1 or ld < c or group < (r - 1) * ld + c:
+        raise ValueError(f"{name}: strides {tuple(t.stride())}, need contiguous rows of "
+                         "matrices that do not overlap")
+    return ld, group
+
+
+def _moe_args(x, w_gate, w_up, w_down, route, act):
+    ldx = _need_rows(x, torch.bfloat16, None, None, "x")
+    T, D = x.shape
+    dev = x.device
+    E, top = _need_route(route, T, "route", dev)
+    ldw = _need_experts(w_gate, E, None, D, "w_gate", dev)
+    F = w_gate.shape[1]
+    if _need_experts(w_up, E, F, D, "w_up", dev) != ldw:
+        raise ValueError("w_up: strides differ from w_gate's")
+    ldd = _need_experts(w_down, E, D, F, "w_down", dev)
+    return (T, D, F, E, top), (_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), *ldw, _ptr(w_down), *ldd,
+                               _act_id(act), _ptr(route.weights), _ptr(route.offsets),
+                               _ptr(route.order), _ptr(route.place))
+
+
+def moe_forward(x, w_gate, w_up, w_down, route: Route, act: str = "silu",
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """The experts' gated feed-forward (zopt_moe_forward): y bf16 [T, D], each
+    token's sum over its experts of weight * (act(x w_gate^T) * (x w_up^T))
+    w_down^T, of x bf16 [T, D], w_gate and w_up bf16 [experts, F, D] with the
+    same strides, w_down bf16 [experts, D, F], and a Route of moe_route or
+    moe_plan.  Tokens without an expert get zeros."""
+    sizes, args = _moe_args(x, w_gate, w_up, w_down, route, act)
+    dev = x.device
+    on = _On(dev, stream)
+    if out is None:
+        out = on.empty(tuple(x.shape), torch.bfloat16)
+    ldy = _need_rows(out, torch.bfloat16, *x.shape, "out", dev)
+    with _on_device(dev):
+        _sized(lib().zopt_moe_forward, (*sizes, *args, _ptr(out), ldy), "zopt_moe_forward", on, workspace)
+    return out
+
+
+def _experts_empty(E, rows, cols, strides, on):
+    ld, group = strides
+    if (ld, group) == (cols, rows * cols):
+        return on.empty((E, rows, cols), torch.bfloat16)
+    flat = on.empty(((E - 1) * group + (rows - 1) * ld + cols,), torch.bfloat16)
+    return flat.as_strided((E, rows, cols), (group, ld, 1))
+
+
+def moe_backward(dy, x, w_gate, w_up, w_down, route: Route, act: str = "silu",
+                 dx: Optional[torch.Tensor] = None, dw_gate: Optional[torch.Tensor] = None,
+                 dw_up: Optional[torch.Tensor] = None, dw_down: Optional[torch.Tensor] = None,
+                 dweights: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Gradients (dx, dw_gate, dw_up, dw_down, dweights) of moe_forward from dy
+    bf16 [T, D] and its arguments (zopt_moe_backward): bf16 but for dweights,
+    fp32 [T, top], which moe_route_backward takes.  The weights' gradients may be
+    views of a flat gradient vector."""
+    sizes, args = _moe_args(x, w_gate, w_up, w_down, route, act)
+    T, D, F, E, top = sizes
+    dev = x.device
+    lddy = _need_rows(dy, torch.bfloat16, T, D, "dy", dev)
+    on = _On(dev, stream)
+    if dx is None:
+        dx = on.empty((T, D), torch.bfloat16)
+    lddx = _need_rows(dx, torch.bfloat16, T, D, "dx", dev)
+    # (gate and up have one layout: one that is not given takes the other's)
+    ldw = (D, F * D)
+    for t, name in ((dw_up, "dw_up"), (dw_gate, "dw_gate")):
+        if t is not None:
+            ldw = _need_experts(t, E, F, D, name, dev)
+    if dw_gate is None:
+        dw_gate = _experts_empty(E, F, D, ldw, on)
+    if dw_up is None:
+        dw_up = _experts_empty(E, F, D, ldw, on)
+    if _need_experts(dw_up, E, F, D, "dw_up", dev) != _need_experts(dw_gate, E, F, D, "dw_gate", dev):
+        raise ValueError("dw_up: strides differ from dw_gate's")
+    if dw_down is None:
+        dw_down = on.empty((E, D, F), torch.bfloat16)
+    ldd = _need_experts(dw_down, E, D, F, "dw_down", dev)
+    if dweights is None:
+        dweights = on.empty((T, top), torch.float32)
+    _need(dweights, torch.float32, T * top, "dweights", dev)
+    if tuple(dweights.shape) != (T, top):
+        raise ValueError(f"dweights: shape {tuple(dweights.shape)}, need {(T, top)}")
+    with _on_device(dev):
+        _sized(lib().zopt_moe_backward,
+               (*sizes, _ptr(dy), lddy, *args, _ptr(dx), lddx, _ptr(dw_gate), _ptr(dw_up), *ldw,
+                _ptr(dw_down), *ldd, _ptr(dweights)), "zopt_moe_backward", on, workspace)
+    return dx, dw_gate, dw_up, dw_down, dweights

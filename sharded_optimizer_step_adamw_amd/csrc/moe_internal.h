@@ -1,0 +1,119 @@
+// moe_internal.h -- declarations shared by routing and the experts' gated
+// feed-forward (moe_route.hip, moe_rows.hip, moe_gemm.hip, moe_back_gemm.hip,
+// moe_api.hip).
+#pragma once
+
+#include "train_internal.h"
+
+namespace zopt {
+
+constexpr int kMaxExperts = 1024, kMaxTop = 32;
+
+// ---------------------------------------------------------------- routing
+
+struct RouteArgs {
+    int64_t tokens;
+    int32_t experts, top, bf16, sigmoid, groups, top_groups, renormalise;
+    float scale;
+    const void *logits;   // fp32 or bf16 [tokens, experts], row stride ld
+    int64_t ld;
+    const float *bias;    // [experts] or NULL
+    int32_t *chosen;      // [tokens, top]
+    float *weights;       // [tokens, top]
+    int32_t *counts;      // [blocks, experts]: how often each block of tokens chose each expert
+    int32_t block_tokens;
+};
+// Slots sorted by expert, stable: from the choice and the blocks' counts.
+struct PlanArgs {
+    int64_t tokens;
+    int32_t experts, top, block_tokens;
+    const int32_t *chosen;
+    int32_t *counts;
+    int32_t *offsets, *order, *place;
+};
+struct RouteBackArgs {
+    int64_t tokens;
+    int32_t experts, top, bf16, sigmoid, renormalise;
+    float scale;
+    const void *logits;
+    int64_t ld;
+    const int32_t *chosen;
+    const float *dweights;
+    void *dlogits;        // the logits' type, row stride lddl
+    int64_t lddl;
+};
+// Tokens of a block of the two passes, and how many blocks there are.
+int32_t route_block_tokens(int64_t tokens, int32_t top);
+hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+hipError_t launch_plan_count(const PlanArgs &a, hipStream_t stream);
+hipError_t launch_plan(const PlanArgs &a, hipStream_t stream);
+hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);
+
+// ---------------------------------------------------------------- experts
+
+// What precedes the products, all in one launch:
+//   kMoeTiles   the tile rows of height `height` (TgTileRow [1 + capacity]) from
+//               the offsets
+//   kMoeSizes   the experts, the one with the most rows first
+//   kMoeGather  dst [slots, round8(cols)] = the slots' rows of src, zero beyond
+//               cols; share (or NULL): the slots' weights
+//   kMoeCopy    dst [rows, round8(cols)] = src's rows, of which each
+//               `group_rows` lie `group_stride` apart
+enum MoePrepKind : int { kMoeTiles = 0, kMoeSizes = 1, kMoeGather = 2, kMoeCopy = 3 };
+struct MoePrep {
+    int32_t kind;
+    uint32_t blocks;              // set by the launch
+    int32_t height, capacity;
+    TgTileRow *tiles;
+    int32_t *sizes;
+    int64_t rows, cols;
+    const uint16_t *src;
+    int64_t ld, group_rows, group_stride;
+    uint16_t *dst;
+    const float *weights;
+    float *share;
+};
+constexpr int kMaxMoePreps = 10;
+struct MoePrepList {
+    MoePrep job[kMaxMoePreps];
+    int32_t n;
+    int32_t experts, top;
+    int64_t slots;                // tokens * top
+    const int32_t *offsets, *order;
+};
+hipError_t launch_moe_prep(MoePrepList &list, hipStream_t stream);
+
+// out [tokens, cols] = the sums over a token's slots of weights (NULL: 1) times
+// their rows [slots, cols] (row stride ld); and dweights [tokens, top] = the
+// sums of the slots' `parts` dots (NULL: not wanted).  A slot without a place
+// counts as zero.
+struct MoeCombine {
+    int64_t tokens, cols;
+    int32_t top;
+    int64_t slots;
+    const int32_t *place;
+    const float *weights;
+    const uint16_t *rows;
+    int64_t ld;
+    uint16_t *out;
+    int64_t ldo;
+    const float *dot;
+    int64_t lddot;
+    int32_t parts;
+    float *dweights;
+};
+hipError_t launch_moe_combine(const MoeCombine &c, hipStream_t stream);
+hipError_t launch_fill_zero_groups(uint16_t *dst, int64_t ld, int64_t group_stride, int64_t groups, int64_t rows,
+                                   int64_t cols, hipStream_t stream);
+
+// The products (train_internal.h's kinds, over groups).
+void plan_groups(TgEpilogue epi, TgGroups kind, TgLaunch &L);
+int tile_height(int tile);
+size_t group_part_bytes(TgGroups kind, const TgLaunch &L);
+hipError_t launch_rows_glu(TgLaunch &L, hipStream_t stream);                   // kTgGlu
+hipError_t launch_rows_store(bool b_km, TgLaunch &L, hipStream_t stream);      // kTgStore
+hipError_t launch_rows_float(TgLaunch &L, hipStream_t stream);                 // kTgFloat, B k-major
+hipError_t launch_rows_back(TgLaunch &L, hipStream_t stream);                  // kTgMoeBack
+hipError_t launch_depth(TgLaunch &L, hipStream_t stream);                      // kTgStore, both k-major
+
+}  // namespace zopt

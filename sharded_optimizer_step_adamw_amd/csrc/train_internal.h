@@ -33,7 +33,24 @@ struct TgSegment {
 //   kTgXent     exponentials and row statistics of a piece of logits
 //   kTgGlu      act(g) u from interleaved gate / up columns, with checkpoints
 //   kTgGluBack  dg, du (and h) from g, u and dh
-enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3, kTgSum = 4 };
+//   kTgFloat    sum -> fp32
+//   kTgMoeBack  kTgGluBack for rows with a weight each, from fp32 dh, with the
+//               weights' gradients
+enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3, kTgSum = 4, kTgFloat = 5, kTgMoeBack = 6 };
+
+// Products of several groups (experts) in one launch, whose sizes only the
+// device knows.  `first` [groups + 1]: the groups' rows lie at first[g] ..
+// first[g + 1] of the operands that the groups share.
+//   kGroupRows   those are rows of A and of the output; each group has a B
+//                (B's p, and groups' distance group_stride)
+//   kGroupDepth  those are the reduction of A and B; each group has an output
+//                (out, and group_out)
+enum TgGroups : int { kNoGroups = 0, kGroupRows = 1, kGroupDepth = 2 };
+// A tile row of kGroupRows: its group, its first row and the group's last.
+// The list's first entry holds the number of the others (in `group`).
+struct TgTileRow {
+    int32_t group, row, end, unused;
+};
 
 enum TgAct : int { kActSilu = 0, kActGelu = 1 };
 
@@ -91,6 +108,18 @@ struct TgLaunch {
     int64_t lddh;
     uint16_t *dg, *du;        // row stride lddg, columns [N, round up to 8) written as zero
     int64_t lddg;
+    // kTgMoeBack: h is share * act(g) u, dg and du are of share * dh (their strides
+    // lddg, as h's); dot [M, lddot]: the sums of dh act(g) u over 32 columns
+    const float *dhf;         // fp32, row stride lddh, columns [N, round up to 4) readable
+    const float *share;       // [M]
+    float *dot;
+    int64_t lddot;
+    // groups (tiles_m, whole, tiles, total and padded of kGroupRows: the kernel's own)
+    const int32_t *first;
+    const int32_t *by_size;   // kGroupDepth: the groups, the largest first
+    const TgTileRow *tile_row;
+    int32_t groups, slots;    // (no row of a group is past slots)
+    int64_t group_stride, group_out;
 };
 
 constexpr int kXentGroup = 64;  // columns per statistics group
