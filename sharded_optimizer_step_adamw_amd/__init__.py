@@ -907,36 +907,56 @@ def _one_of(value, table, name):
     return table[value]
 
 
-def _need_heads(t, shape, name, device=None):
-    """Checks that t is a bf16 GPU tensor [tokens, heads, width] (None: any
-    size there) whose heads are contiguous; returns its first two strides."""
+# (Most of a small call's time is the host's, so a check first asks in one
+# expression whether all is as it should be; only a call that will be refused
+# goes through the steps that say why.)
+
+def _need_heads(t, shape, name, index):
+    """Checks that t is a bf16 tensor [tokens, heads, width] (None: any size
+    there) on GPU `index` whose heads are contiguous; returns its strides."""
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == index >= 0:
+        have = t.shape
+        if len(have) == 3 and (have == shape or all(w is None or h == w for h, w in zip(have, shape))):
+            strides = t.stride()
+            if strides[2] == 1 or have[2] == 1:
+                return strides
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: dtype {t.dtype}, need {torch.bfloat16}")
-    if t.dim() != 3 or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+    if t.dim() != 3 or any(w is not None and h != w for h, w in zip(t.shape, shape)):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, need "
                          f"{tuple('any' if s is None else s for s in shape)}")
     if t.device.type != "cuda":
         raise ValueError(f"{name}: must be a GPU tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name}: strides {tuple(t.stride())}, need contiguous heads")
-    return t.stride(0), t.stride(1)
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    raise ValueError(f"{name}: strides {tuple(t.stride())}, need contiguous heads")
 
 
-def _need_vector(t, dtype, n, name, device) -> None:
+def _need_shape(t, dtype, shape, name, index):
+    """Checks that t is a contiguous tensor of dtype and shape on GPU `index`, or
+    None; returns its address."""
     if t is None:
-        return
-    _need(t, dtype, n, name, device)
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, need ({n},)")
+        return None
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == index >= 0 and t.is_contiguous()):
+        return t.data_ptr()
+    _need(t, dtype, 0, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, need {tuple(shape)}")
+    raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+
+
+def _new(on, like, shape, dtype=None):
+    """An output of the call's own stream."""
+    dtype = like.dtype if dtype is None else dtype
+    return on.empty(shape, dtype) if on.other else like.new_empty(shape, dtype=dtype)
 
 
 def _on_device(device):
     """The device of a call's tensors made the current one, where it is not."""
-    return torch.cuda.device(device) if torch.cuda.current_device() != device.index else _SAME
+    return torch.cuda.device(device) if torch._C._cuda_getDevice() != device.index else _SAME
 
 
 class _Same:
@@ -973,31 +993,49 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, device="cuda",
 
 def _rope_args(q, k, table, position, w_q, w_k, eps, style):
     """(sizes, what q and k are, the other arguments)"""
-    qs = _need_heads(q, (None, None, None), "q")
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q: expected a tensor")
+    index = q.get_device()
+    if index < 0:
+        index = -1
+    qs = _need_heads(q, (None, None, None), "q", index)
     T, hq, width = q.shape
-    dev = q.device
-    hk, ks = 0, (0, 0)
-    if k is not None:
-        ks = _need_heads(k, (T, None, width), "k", dev)
+    if k is None:
+        hk, ks, kp = 0, (0, 0, 0), None
+    else:
+        ks, kp = _need_heads(k, (T, None, width), "k", index), k.data_ptr()
         hk = k.shape[1]
         if hk == 0:
             raise ValueError("k: no heads")
     if hq == 0 or width == 0:
         raise ValueError(f"q: shape {tuple(q.shape)} has no heads")
-    positions, rot = 0, 0
+    positions, rot, tp = 0, 0, None
     if table is not None:
-        if table.dim() != 3 or table.shape[2] != 2:
-            raise ValueError(f"table: shape {tuple(table.shape)}, need (positions, rot / 2, 2)")
-        positions, rot = table.shape[0], 2 * table.shape[1]
-        _need(table, torch.float32, positions * rot, "table", dev)
-    if rot > width:
-        raise ValueError(f"table: turns {rot} elements of heads of {width}")
-    _need_vector(position, torch.int64, T, "position", dev)
-    _need_vector(w_q, torch.bfloat16, width, "w_q", dev)
-    _need_vector(w_k, torch.bfloat16, width, "w_k", dev)
-    rest = (_ptr(table), positions, _ptr(position), _ptr(w_q), _ptr(w_k), float(eps),
+        shape = table.shape if isinstance(table, torch.Tensor) else ()
+        if isinstance(table, torch.Tensor) and (len(shape) != 3 or shape[2] != 2):
+            raise ValueError(f"table: shape {tuple(shape)}, need (positions, rot / 2, 2)")
+        tp = _need_shape(table, torch.float32, shape, "table", index)
+        positions, rot = shape[0], 2 * shape[1]
+        if rot > width:
+            raise ValueError(f"table: turns {rot} elements of heads of {width}")
+    rest = (tp, positions, _need_shape(position, torch.int64, (T,), "position", index),
+            _need_shape(w_q, torch.bfloat16, (width,), "w_q", index),
+            _need_shape(w_k, torch.bfloat16, (width,), "w_k", index), eps,
             _one_of(style, ROPE_STYLES, "style"))
-    return (T, hq, hk, width, rot), (_ptr(q), *qs, _ptr(k), *ks), rest
+    return ((T, hq, hk, width, rot), (q.data_ptr(), qs[0], qs[1], kp, ks[0], ks[1]), rest)
+
+
+def _rope_out(t, like, name, on):
+    """An output that is given, or a new one, with its address and strides."""
+    shape = like.shape
+    if t is None:
+        t = _new(on, like, shape)
+        return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
+    s = _need_heads(t, shape, name, on.device.index)
+    return t, (t.data_ptr(), s[0], s[1])
+
+
+_NO_HEADS = (None, 0, 0)
 
 
 def qk_norm_rope(q, k, table, position=None, w_q=None, w_k=None, eps: float = 1e-6,
@@ -1011,19 +1049,11 @@ def qk_norm_rope(q, k, table, position=None, w_q=None, w_k=None, eps: float = 1e
     w_k bf16 [width] or None, style "half" or "pairs".  Returns (yq, yk), bf16;
     out_q may be q, and out_k k."""
     sizes, heads, rest = _rope_args(q, k, table, position, w_q, w_k, eps, style)
-    dev = q.device
-    on = _On(dev, stream)
-    if out_q is None:
-        out_q = on.empty(tuple(q.shape), torch.bfloat16)
-    outs = (out_q.data_ptr(), *_need_heads(out_q, q.shape, "out_q", dev))
-    if k is None:
-        out_k, outs = None, (*outs, None, 0, 0)
-    else:
-        if out_k is None:
-            out_k = on.empty(tuple(k.shape), torch.bfloat16)
-        outs = (*outs, out_k.data_ptr(), *_need_heads(out_k, k.shape, "out_k", dev))
-    with _on_device(dev):
-        _check(lib().zopt_qk_norm_rope(*sizes, *heads, *rest, *outs, on.handle), "zopt_qk_norm_rope")
+    on = _On(q.device, stream)
+    out_q, yq = _rope_out(out_q, q, "out_q", on)
+    out_k, yk = (None, _NO_HEADS) if k is None else _rope_out(out_k, k, "out_k", on)
+    with _on_device(on.device):
+        _check(lib().zopt_qk_norm_rope(*sizes, *heads, *rest, *yq, *yk, on.handle), "zopt_qk_norm_rope")
     return out_q, out_k
 
 
@@ -1036,31 +1066,27 @@ def qk_norm_rope_backward(dyq, dyk, q, k, table, position=None, w_q=None, w_k=No
     and its arguments (zopt_qk_norm_rope_backward); dw_q and dw_k are None
     where there is no weight.  dq may be dyq, and dk dyk."""
     sizes, heads, rest = _rope_args(q, k, table, position, w_q, w_k, eps, style)
-    dev = q.device
-    on = _On(dev, stream)
-    width = sizes[3]
+    on = _On(q.device, stream)
+    index = on.device.index
     ins, outs, grads = (), (), []
     for x, dy, dx, w, dw, name in ((q, dyq, dq, w_q, dw_q, "q"), (k, dyk, dk, w_k, dw_k, "k")):
         if x is None:
-            ins, outs = (*ins, None, 0, 0), (*outs, None, 0, 0)
-            grads += [None, None]
+            ins, outs = ins + _NO_HEADS, outs + _NO_HEADS
+            grads += [None, None, None]
             continue
-        ins = (*ins, dy.data_ptr() if isinstance(dy, torch.Tensor) else None,
-               *_need_heads(dy, x.shape, f"dy{name}", dev))
-        if dx is None:
-            dx = on.empty(tuple(x.shape), torch.bfloat16)
-        outs = (*outs, dx.data_ptr(), *_need_heads(dx, x.shape, f"d{name}", dev))
+        s = _need_heads(dy, x.shape, f"dy{name}", index)
+        dx, to = _rope_out(dx, x, f"d{name}", on)
+        ins, outs = ins + (dy.data_ptr(), s[0], s[1]), outs + to
         if w is None:
             dw = None
         elif dw is None:
-            dw = on.empty((width,), torch.bfloat16)
-        _need_vector(dw, torch.bfloat16, width, f"dw_{name}", dev)
-        grads += [dx, dw]
-    with _on_device(dev):
+            dw = _new(on, w, w.shape)
+        grads += [dx, dw, _need_shape(dw, torch.bfloat16, (sizes[3],), f"dw_{name}", index)]
+    with _on_device(on.device):
         _sized(lib().zopt_qk_norm_rope_backward,
-               (*sizes, *ins, *heads, *rest, *outs, _ptr(grads[1]), _ptr(grads[3])),
+               (*sizes, *ins, *heads, *rest, *outs, grads[2], grads[5]),
                "zopt_qk_norm_rope_backward", on, workspace)
-    return grads[0], grads[2], grads[1], grads[3]
+    return grads[0], grads[3], grads[1], grads[4]
 
 
 _LOGITS = {torch.float32: 0, torch.bfloat16: 1}
@@ -1074,31 +1100,32 @@ def _need_logits(t, name, rows=None, cols=None, device=None, dtype=None):
     return _need_rows(t, t.dtype, rows, cols, name, device)
 
 
-def _need_route(r, T, name, device):
-    """Checks a Route; returns (experts of the layer, experts of a token)."""
+def _need_route(r, T, name, index):
+    """Checks a Route; returns (experts of the layer, experts of a token) and
+    the addresses of its parts."""
     if not isinstance(r, Route):
         raise TypeError(f"{name}: expected a Route")
-    if r.experts.dim() != 2 or (T is not None and r.experts.shape[0] != T):
-        raise ValueError(f"{name}.experts: shape {tuple(r.experts.shape)}, need "
+    shape = r.experts.shape
+    if len(shape) != 2 or (T is not None and shape[0] != T):
+        raise ValueError(f"{name}.experts: shape {tuple(shape)}, need "
                          f"({'any' if T is None else T}, 'any')")
-    rows, top = r.experts.shape
-    _need(r.experts, torch.int32, rows * top, f"{name}.experts", device)
-    for t, dtype, shape, what in ((r.weights, torch.float32, (rows, top), "weights"),
-                                  (r.order, torch.int32, (rows * top,), "order"),
-                                  (r.place, torch.int32, (rows, top), "place")):
-        _need(t, dtype, rows * top, f"{name}.{what}", device)
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name}.{what}: shape {tuple(t.shape)}, need {shape}")
     E = r.offsets.numel() - 1
-    _need_vector(r.offsets, torch.int32, max(E + 1, 2), f"{name}.offsets", device)
-    return E, top
+    need = _need_shape
+    return E, shape[1], (need(r.experts, torch.int32, shape, f"{name}.experts", index),
+                         need(r.weights, torch.float32, shape, f"{name}.weights", index),
+                         need(r.offsets, torch.int32, (max(E, 1) + 1,), f"{name}.offsets", index),
+                         need(r.order, torch.int32, (shape[0] * shape[1],), f"{name}.order", index),
+                         need(r.place, torch.int32, shape, f"{name}.place", index))
 
 
-def _route_empty(T, E, top, on, experts=None, weights=None) -> Route:
-    return Route(on.empty((T, top), torch.int32) if experts is None else experts,
-                 on.empty((T, top), torch.float32) if weights is None else weights,
-                 on.empty((E + 1,), torch.int32), on.empty((T * top,), torch.int32),
-                 on.empty((T, top), torch.int32))
+def _route_parts(like, T, E, top, on, parts):
+    """offsets, order and place, and `parts` more [T, top]: int32 pieces of one
+    allocation."""
+    n = T * top
+    flat = _new(on, like, (E + 1 + (2 + parts) * n,), torch.int32)
+    matrix = lambda at: flat.as_strided((T, top), (top, 1), at)  # noqa: E731
+    return (flat.as_strided((E + 1,), (1,), 2 * n), flat.as_strided((n,), (1,), 0), matrix(n),
+            *(matrix(E + 1 + (2 + i) * n) for i in range(parts)))
 
 
 def moe_route(logits, top: int, score: str = "softmax", bias: Optional[torch.Tensor] = None,
@@ -1113,17 +1140,23 @@ def moe_route(logits, top: int, score: str = "softmax", bias: Optional[torch.Ten
     chosen ones with renormalise.  An expert with logit -inf is not chosen."""
     ld = _need_logits(logits, "logits")
     T, E = logits.shape
-    dev = logits.device
-    _need_vector(bias, torch.float32, E, "bias", dev)
-    on = _On(dev, stream)
+    on = _On(logits.device, stream)
+    index = on.device.index
     if out is None:
-        out = _route_empty(T, E, top, on)
-    if _need_route(out, T, "out", dev) != (E, top):
-        raise ValueError(f"out: a Route of other experts than {E}, {top}")
-    with _on_device(dev):
+        if top < 1:
+            raise ValueError(f"top: {top}")
+        offsets, order, place, experts, weights = _route_parts(logits, T, E, top, on, 2)
+        out = Route(experts, weights.view(torch.float32), offsets, order, place)
+        ptrs = [p.data_ptr() for p in out]
+    else:
+        e, k, ptrs = _need_route(out, T, "out", index)
+        if (e, k) != (E, top):
+            raise ValueError(f"out: a Route of {e} experts, {k} a token, need {E} and {top}")
+    with _on_device(on.device):
         _sized(lib().zopt_moe_route,
-               (T, E, top, _ptr(logits), ld, _LOGITS[logits.dtype], _one_of(score, SCORES, "score"),
-                _ptr(bias), groups, top_groups, int(renormalise), float(scale), *map(_ptr, out)),
+               (T, E, top, logits.data_ptr(), ld, _LOGITS[logits.dtype],
+                _one_of(score, SCORES, "score"), _need_shape(bias, torch.float32, (E,), "bias", index),
+                groups, top_groups, int(renormalise), scale, *ptrs),
                "zopt_moe_route", on, workspace)
     return out
 
@@ -1135,20 +1168,23 @@ def moe_plan(experts, weights, num_experts: int, workspace: Optional[torch.Tenso
     fp32 [T, top], which it holds as they are."""
     if not isinstance(experts, torch.Tensor):
         raise TypeError("experts: expected a tensor")
-    if experts.dim() != 2:
-        raise ValueError(f"experts: shape {tuple(experts.shape)}, need [tokens, top]")
-    T, top = experts.shape
-    dev = experts.device
-    _need(experts, torch.int32, T * top, "experts", dev)
+    shape = experts.shape
+    if len(shape) != 2 or shape[1] < 1:
+        raise ValueError(f"experts: shape {tuple(shape)}, need [tokens, top]")
     if num_experts < 1:
         raise ValueError(f"num_experts: {num_experts}")
-    on = _On(dev, stream)
-    out = _route_empty(T, num_experts, top, on, experts, weights)
-    _need_route(out, T, "route", dev)
-    with _on_device(dev):
-        _sized(lib().zopt_moe_plan, (T, num_experts, top, _ptr(experts), *map(_ptr, out[2:])),
+    index = experts.get_device()
+    address = _need_shape(experts, torch.int32, shape, "experts", index)
+    if not isinstance(weights, torch.Tensor):
+        raise TypeError("weights: expected a tensor")
+    _need_shape(weights, torch.float32, shape, "weights", index)
+    on = _On(experts.device, stream)
+    parts = _route_parts(experts, shape[0], num_experts, shape[1], on, 0)
+    with _on_device(on.device):
+        _sized(lib().zopt_moe_plan,
+               (shape[0], num_experts, shape[1], address, *(p.data_ptr() for p in parts)),
                "zopt_moe_plan", on, workspace)
-    return out
+    return Route(experts, weights, *parts)
 
 
 def moe_route_backward(dweights, logits, route: Route, score: str = "softmax",
@@ -1158,22 +1194,23 @@ def moe_route_backward(dweights, logits, route: Route, score: str = "softmax",
     top] (zopt_moe_route_backward)."""
     ld = _need_logits(logits, "logits")
     T, E = logits.shape
-    dev = logits.device
-    if _need_route(route, T, "route", dev)[0] != E:
-        raise ValueError(f"route: not of {E} experts")
-    top = route.experts.shape[1]
-    _need(dweights, torch.float32, T * top, "dweights", dev)
-    if tuple(dweights.shape) != (T, top):
-        raise ValueError(f"dweights: shape {tuple(dweights.shape)}, need {(T, top)}")
-    on = _On(dev, stream)
+    on = _On(logits.device, stream)
+    index = on.device.index
+    e, top, ptrs = _need_route(route, T, "route", index)
+    if e != E:
+        raise ValueError(f"route: of {e} experts, need {E}")
+    if not isinstance(dweights, torch.Tensor):
+        raise TypeError("dweights: expected a tensor")
+    dw = _need_shape(dweights, torch.float32, (T, top), "dweights", index)
     if out is None:
-        out = on.empty((T, E), logits.dtype)
-    ldo = _need_logits(out, "out", T, E, dev, logits.dtype)
-    with _on_device(dev):
-        _check(lib().zopt_moe_route_backward(T, E, top, _ptr(dweights), _ptr(logits), ld,
+        out, ldo = _new(on, logits, (T, E)), E
+    else:
+        ldo = _need_logits(out, "out", T, E, on.device, logits.dtype)
+    with _on_device(on.device):
+        _check(lib().zopt_moe_route_backward(T, E, top, dw, logits.data_ptr(), ld,
                                              _LOGITS[logits.dtype], _one_of(score, SCORES, "score"),
-                                             int(renormalise), float(scale), _ptr(route.experts),
-                                             _ptr(out), ldo, on.handle), "zopt_moe_route_backward")
+                                             int(renormalise), scale, ptrs[0], out.data_ptr(), ldo,
+                                             on.handle), "zopt_moe_route_backward")
     return out
 
 
@@ -1181,6 +1218,11 @@ def _need_experts(t, E, rows, cols, name, device):
     """Checks that t is a bf16 GPU tensor [E, rows, cols] (None: any size) whose
     matrices have contiguous rows and do not overlap; returns the strides of
     rows and of experts."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == 3 and t.device == device
+            and t.is_contiguous()):
+        e, r, c = t.shape
+        if e == E and (rows is None or r == rows) and (cols is None or c == cols) and e * r * c > 0:
+            return c, r * c
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     if t.dtype != torch.bfloat16:
@@ -1204,15 +1246,14 @@ def _moe_args(x, w_gate, w_up, w_down, route, act):
     ldx = _need_rows(x, torch.bfloat16, None, None, "x")
     T, D = x.shape
     dev = x.device
-    E, top = _need_route(route, T, "route", dev)
+    E, top, ptrs = _need_route(route, T, "route", dev.index)
     ldw = _need_experts(w_gate, E, None, D, "w_gate", dev)
     F = w_gate.shape[1]
     if _need_experts(w_up, E, F, D, "w_up", dev) != ldw:
         raise ValueError("w_up: strides differ from w_gate's")
     ldd = _need_experts(w_down, E, D, F, "w_down", dev)
-    return (T, D, F, E, top), (_ptr(x), ldx, _ptr(w_gate), _ptr(w_up), *ldw, _ptr(w_down), *ldd,
-                               _act_id(act), _ptr(route.weights), _ptr(route.offsets),
-                               _ptr(route.order), _ptr(route.place))
+    return (T, D, F, E, top), (x.data_ptr(), ldx, w_gate.data_ptr(), w_up.data_ptr(), *ldw,
+                               w_down.data_ptr(), *ldd, _act_id(act), *ptrs[1:])
 
 
 def moe_forward(x, w_gate, w_up, w_down, route: Route, act: str = "silu",
@@ -1227,10 +1268,12 @@ def moe_forward(x, w_gate, w_up, w_down, route: Route, act: str = "silu",
     dev = x.device
     on = _On(dev, stream)
     if out is None:
-        out = on.empty(tuple(x.shape), torch.bfloat16)
-    ldy = _need_rows(out, torch.bfloat16, *x.shape, "out", dev)
+        out, ldy = _new(on, x, x.shape), sizes[1]
+    else:
+        ldy = _need_rows(out, torch.bfloat16, *x.shape, "out", dev)
     with _on_device(dev):
-        _sized(lib().zopt_moe_forward, (*sizes, *args, _ptr(out), ldy), "zopt_moe_forward", on, workspace)
+        _sized(lib().zopt_moe_forward, (*sizes, *args, out.data_ptr(), ldy), "zopt_moe_forward", on,
+               workspace)
     return out
 
 
@@ -1257,8 +1300,9 @@ def moe_backward(dy, x, w_gate, w_up, w_down, route: Route, act: str = "silu",
     lddy = _need_rows(dy, torch.bfloat16, T, D, "dy", dev)
     on = _On(dev, stream)
     if dx is None:
-        dx = on.empty((T, D), torch.bfloat16)
-    lddx = _need_rows(dx, torch.bfloat16, T, D, "dx", dev)
+        dx, lddx = _new(on, x, (T, D)), D
+    else:
+        lddx = _need_rows(dx, torch.bfloat16, T, D, "dx", dev)
     # (gate and up have one layout: one that is not given takes the other's)
     ldw = (D, F * D)
     for t, name in ((dw_up, "dw_up"), (dw_gate, "dw_gate")):
@@ -1274,12 +1318,10 @@ def moe_backward(dy, x, w_gate, w_up, w_down, route: Route, act: str = "silu",
         dw_down = on.empty((E, D, F), torch.bfloat16)
     ldd = _need_experts(dw_down, E, D, F, "dw_down", dev)
     if dweights is None:
-        dweights = on.empty((T, top), torch.float32)
-    _need(dweights, torch.float32, T * top, "dweights", dev)
-    if tuple(dweights.shape) != (T, top):
-        raise ValueError(f"dweights: shape {tuple(dweights.shape)}, need {(T, top)}")
+        dweights = _new(on, x, (T, top), torch.float32)
+    dw = _need_shape(dweights, torch.float32, (T, top), "dweights", dev.index)
     with _on_device(dev):
         _sized(lib().zopt_moe_backward,
-               (*sizes, _ptr(dy), lddy, *args, _ptr(dx), lddx, _ptr(dw_gate), _ptr(dw_up), *ldw,
-                _ptr(dw_down), *ldd, _ptr(dweights)), "zopt_moe_backward", on, workspace)
+               (*sizes, dy.data_ptr(), lddy, *args, dx.data_ptr(), lddx, dw_gate.data_ptr(),
+                dw_up.data_ptr(), *ldw, dw_down.data_ptr(), *ldd, dw), "zopt_moe_backward", on, workspace)
     return dx, dw_gate, dw_up, dw_down, dweights

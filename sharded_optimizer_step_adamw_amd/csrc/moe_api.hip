@@ -16,11 +16,17 @@ zopt_status check_route(int64_t T, int32_t E, int32_t k) {
         return ZOPT_ERR_SIZE;
     return T * k <= kMaxSlots ? ZOPT_OK : ZOPT_ERR_SIZE;
 }
-int64_t plan_blocks(int64_t T, int32_t k) {
-    const int64_t each = route_block_tokens(T, k);
-    return (T + each - 1) / each;
+// The sort's workspace for blocks of `each` tokens: their counts and the
+// experts' totals.
+size_t plan_bytes(int64_t T, int32_t E, int32_t each) {
+    const int64_t blocks = (T + each - 1) / each;
+    return blocks > 1 ? (size_t)up((blocks + 1) * E * 4, 256) : 0;
 }
-size_t plan_bytes(int64_t T, int32_t E, int32_t k) { return (size_t)up(plan_blocks(T, k) * E * 4, 256); }
+PlanArgs plan_args(int64_t T, int32_t E, int32_t k, int32_t each, const int32_t *chosen, void *workspace,
+                   int32_t *offsets, int32_t *order, int32_t *place) {
+    int32_t *counts = static_cast<int32_t *>(workspace);
+    return PlanArgs{T, E, k, each, chosen, counts, counts + (T + each - 1) / each * E, offsets, order, place};
+}
 
 // A weight [experts, rows, cols] as the products read it, in place or a padded
 // copy.
@@ -211,7 +217,8 @@ ZOPT_EXPORT zopt_status zopt_moe_route(int64_t T, int32_t experts, int32_t top, 
     if (!stride_ok(ld, experts) || !range(groups, 1, kMaxRanges < experts ? kMaxRanges : experts) || experts % groups ||
         !range(top_groups, 1, groups) || top > experts / groups * top_groups)
         return ZOPT_ERR_SIZE;
-    const size_t need = plan_bytes(T, experts, top);
+    const int32_t each = route_block_tokens(T, experts, groups, top);
+    const size_t need = plan_bytes(T, experts, each);
     if (workspace == nullptr) {
         *workspace_bytes = need;
         return ZOPT_OK;
@@ -225,14 +232,11 @@ ZOPT_EXPORT zopt_status zopt_moe_route(int64_t T, int32_t experts, int32_t top, 
     const zopt_status ws = workspace_check(need, workspace, *workspace_bytes);
     if (ws != ZOPT_OK) return ws;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    int32_t *counts = static_cast<int32_t *>(workspace);
-    PlanArgs p{T, experts, top, route_block_tokens(T, top), chosen, counts, offsets, order, place};
-    if (T > 0) {
-        RouteArgs a{T, experts, top, bf16, score == ZOPT_SCORE_SIGMOID, groups, top_groups, renormalise, scale, logits, ld,
-                    bias, chosen, weights, counts, p.block_tokens};
-        ZOPT_TRY(launch_route(a, s));
-    }
-    return device(launch_plan(p, s));
+    const PlanArgs p = plan_args(T, experts, top, each, chosen, workspace, offsets, order, place);
+    if (T == 0) return device(launch_plan(p, s));
+    const RouteArgs a{T, experts, top, bf16, score == ZOPT_SCORE_SIGMOID, groups, top_groups, renormalise, scale, logits,
+                      ld, bias, chosen, weights, p.block_tokens};
+    return device(launch_route(a, p, s));
 }
 
 ZOPT_EXPORT zopt_status zopt_moe_plan(int64_t T, int32_t experts, int32_t top, const int32_t *chosen, int32_t *offsets,
@@ -242,7 +246,8 @@ ZOPT_EXPORT zopt_status zopt_moe_plan(int64_t T, int32_t experts, int32_t top, c
     // (any number of experts a token, the same one more than once too)
     if (!range(T, 0, kMaxRows) || !range(experts, 1, kMaxExperts) || !range(top, 1, kMaxTop) || T * top > kMaxSlots)
         return ZOPT_ERR_SIZE;
-    const size_t need = plan_bytes(T, experts, top);
+    const int32_t each = route_block_tokens(T, 0, 1, top);
+    const size_t need = plan_bytes(T, experts, each);
     if (workspace == nullptr) {
         *workspace_bytes = need;
         return ZOPT_OK;
@@ -252,7 +257,7 @@ ZOPT_EXPORT zopt_status zopt_moe_plan(int64_t T, int32_t experts, int32_t top, c
     const zopt_status ws = workspace_check(need, workspace, *workspace_bytes);
     if (ws != ZOPT_OK) return ws;
     hipStream_t s = static_cast<hipStream_t>(stream);
-    PlanArgs p{T, experts, top, route_block_tokens(T, top), chosen, static_cast<int32_t *>(workspace), offsets, order, place};
+    const PlanArgs p = plan_args(T, experts, top, each, chosen, workspace, offsets, order, place);
     if (T > 0) ZOPT_TRY(launch_plan_count(p, s));
     return device(launch_plan(p, s));
 }

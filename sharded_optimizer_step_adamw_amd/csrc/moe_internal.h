@@ -20,7 +20,6 @@ struct RouteArgs {
     const float *bias;    // [experts] or NULL
     int32_t *chosen;      // [tokens, top]
     float *weights;       // [tokens, top]
-    int32_t *counts;      // [blocks, experts]: how often each block of tokens chose each expert
     int32_t block_tokens;
 };
 // Slots sorted by expert, stable: from the choice and the blocks' counts.
@@ -28,7 +27,7 @@ struct PlanArgs {
     int64_t tokens;
     int32_t experts, top, block_tokens;
     const int32_t *chosen;
-    int32_t *counts;
+    int32_t *counts, *total;  // [blocks, experts] and [experts] (blocks > 1)
     int32_t *offsets, *order, *place;
 };
 struct RouteBackArgs {
@@ -42,9 +41,9 @@ struct RouteBackArgs {
     void *dlogits;        // the logits' type, row stride lddl
     int64_t lddl;
 };
-// Tokens of a block of the two passes, and how many blocks there are.
-int32_t route_block_tokens(int64_t tokens, int32_t top);
-hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
+// Tokens of a block (experts 0: that only sorts).
+int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top);
+hipError_t launch_route(const RouteArgs &a, const PlanArgs &plan, hipStream_t stream);
 hipError_t launch_plan_count(const PlanArgs &a, hipStream_t stream);
 hipError_t launch_plan(const PlanArgs &a, hipStream_t stream);
 hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);

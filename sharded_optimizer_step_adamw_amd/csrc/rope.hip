@@ -2,6 +2,7 @@
 // their positions, and their gradients.
 #include <cmath>
 
+#include "lanes.h"
 #include "rope_internal.h"
 
 namespace zopt {
@@ -9,35 +10,41 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 2 V 16-bit values: V at p, V at p2 (contiguous: p2 = p + V)
+// V 16-bit values as they lie in memory
 template <int V>
-__device__ __forceinline__ void load_part(const uint16_t *p, float *v) {
+struct Raw {
+    uint32_t v[V > 1 ? V / 2 : 1];
+};
+template <int V, bool PAST>
+__device__ __forceinline__ Raw<V> load_raw(const uint16_t *p) {
+    Raw<V> r;
     if constexpr (V == 8) {
-        const tg_u32x4 r = tg_load<tg_u32x4>(p);
+        const tg_u32x4 x = tg_load<tg_u32x4, PAST>(p);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            v[2 * k] = __uint_as_float(r[k] << 16);
-            v[2 * k + 1] = __uint_as_float(r[k] & 0xFFFF0000u);
-        }
+        for (int k = 0; k < 4; ++k) r.v[k] = x[k];
     } else if constexpr (V == 4) {
-        const tg_u32x2 r = tg_load<tg_u32x2>(p);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            v[2 * k] = __uint_as_float(r[k] << 16);
-            v[2 * k + 1] = __uint_as_float(r[k] & 0xFFFF0000u);
-        }
+        const tg_u32x2 x = tg_load<tg_u32x2, PAST>(p);
+        r.v[0] = x.x;
+        r.v[1] = x.y;
+    } else if constexpr (V == 2) {
+        r.v[0] = tg_load<uint32_t>(p);
     } else {
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] = __uint_as_float((uint32_t)p[k] << 16);
+        r.v[0] = p[0];
     }
+    return r;
 }
 template <int V>
+__device__ __forceinline__ void widen(const Raw<V> &r, float *v) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[k] = __uint_as_float(k & 1 ? r.v[k / 2] & 0xFFFF0000u : r.v[k / 2] << 16);
+}
+template <int V, bool PAST>
 __device__ __forceinline__ void store_part(uint16_t *p, const float *v) {
     if constexpr (V == 8) {
-        tg_store(p, tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
+        tg_store<PAST>(p, tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
                              tg_pack_bf16(v[6], v[7])});
     } else if constexpr (V == 4) {
-        tg_store(p, tg_u32x2{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3])});
+        tg_store<PAST>(p, tg_u32x2{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3])});
     } else {
 #pragma unroll
         for (int k = 0; k < V; ++k) p[k] = (uint16_t)tg_pack_bf16(v[k], 0.0f);
@@ -65,9 +72,15 @@ __device__ __forceinline__ void turn(float (&v)[2 * V], const float2 (&cs)[V], i
 // A row (one head of one token) is held by `group` lanes: a lane has NP pieces
 // of 2 V elements, V of them where the first of each turned pair lies, V where
 // the second does (style pairs, and elements that do not turn: 2 V neighbours),
-// so that a rotation needs no other lane.
-template <int V, int NP, bool BACK>
-__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
+// so that a rotation needs no other lane, and a row's two sums (of squares, and
+// back of g n w) are joined in registers.  A block walks rows of one side, the
+// next row's elements on their way while it works on one.
+// Bound by HBM: 65536 tokens of 32 + 8 heads of 128 take 242 us forward (1.34 GB,
+// 5.55 TB/s; a 2 GiB copy reaches 4.97) and 358 back (2.01 GB, 5.6), 13% and 23%
+// less than without the row read ahead and with accesses through the caches.
+// 8-byte pieces on twice the lanes took 279 and 442.
+template <int V, int NP, bool BACK, bool PAST>
+__global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
     const bool second = (int)blockIdx.x >= a.first_blocks;
     const RopeSide &S = a.side[second ? 1 : 0];
     const int block = second ? blockIdx.x - a.first_blocks : blockIdx.x;
@@ -91,8 +104,8 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
             dw[j][k] = 0.0f;
         }
         if (S.w != nullptr) {
-            if (have[j]) load_part<V>(S.w + at[j], &w[j][0]);
-            if (have2[j]) load_part<V>(S.w + at2[j], &w[j][V]);
+            if (have[j]) widen<V>(load_raw<V, false>(S.w + at[j]), &w[j][0]);
+            if (have2[j]) widen<V>(load_raw<V, false>(S.w + at2[j]), &w[j][V]);
         }
     }
     const float inv_width = 1.0f / (float)a.width;
@@ -102,39 +115,75 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     int head = (int)(row - t * S.heads);
     const int64_t step_t = step / S.heads;
     const int step_h = (int)(step - step_t * S.heads);
+    // A row's position and elements, read a row ahead of their use
+    struct Row {
+        int64_t pos;
+        Raw<V> x[NP], x2[NP], d[NP], d2[NP];
+    };
+    auto fetch = [&](Row &R) __attribute__((always_inline)) {
+        R.pos = -1;
+        if (row < rows) R.pos = a.position != nullptr ? a.position[t] : t;
+        if (row >= rows) return;
+        const uint16_t *p = S.x + t * S.xt + head * S.xh, *q = S.dy + t * S.dt + head * S.dh;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            if (have[j]) R.x[j] = load_raw<V, PAST>(p + at[j]);
+            if (have2[j]) R.x2[j] = load_raw<V, PAST>(p + at2[j]);
+            if constexpr (BACK) {
+                if (have[j]) R.d[j] = load_raw<V, PAST>(q + at[j]);
+                if (have2[j]) R.d2[j] = load_raw<V, PAST>(q + at2[j]);
+            }
+        }
+    };
+    auto advance = [&]() __attribute__((always_inline)) {
+        row += step;
+        t += step_t;
+        head += step_h;
+        if (head >= S.heads) {
+            head -= S.heads;
+            ++t;
+        }
+    };
+    Row cur, next;
+    fetch(cur);
     // (all lanes of a wave stay in the loop: the sums below are over lanes)
     for (int64_t base = row - threadIdx.x / G; base < rows; base += step) {
         const bool live = row < rows;
-        int64_t pos = -1;
-        if (live) pos = a.position != nullptr ? a.position[t] : t;
+        uint16_t *const out = S.out + t * S.ot + head * S.oh;
+        const int64_t pos = cur.pos;
         const bool none = pos < 0, known = !none && pos < a.positions;
         // (a row without a position is zeros, one whose position the table lacks is NaN)
         const float fill = none || known ? 0.0f : NAN;
         float x[NP][2 * V], d[NP][2 * V];
         float2 cs[NP][V];
-        float ss = 0.0f;
 #pragma unroll
         for (int j = 0; j < NP; ++j) {
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) x[j][k] = d[j][k] = fill;
-#pragma unroll
             for (int k = 0; k < V; ++k) cs[j][k] = make_float2(1.0f, 0.0f);
-            if (known) {
-                const uint16_t *p = S.x + t * S.xt + head * S.xh;
-                if (have[j]) load_part<V>(p + at[j], &x[j][0]);
-                if (have2[j]) load_part<V>(p + at2[j], &x[j][V]);
-                if constexpr (BACK) {
-                    const uint16_t *q = S.dy + t * S.dt + head * S.dh;
-                    if (have[j]) load_part<V>(q + at[j], &d[j][0]);
-                    if (have2[j]) load_part<V>(q + at2[j], &d[j][V]);
-                }
-                if (turns[j]) __builtin_memcpy(cs[j], a.table + pos * half + V * (gl + j * G), sizeof(float2) * V);
+            if (known && turns[j]) __builtin_memcpy(cs[j], a.table + pos * half + V * (gl + j * G), sizeof(float2) * V);
+        }
+        advance();
+        fetch(next);
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            widen<V>(cur.x[j], &x[j][0]);
+            widen<V>(cur.x2[j], &x[j][V]);
+            if constexpr (BACK) {
+                widen<V>(cur.d[j], &d[j][0]);
+                widen<V>(cur.d2[j], &d[j][V]);
             }
             // (places past the row's end, in a wrong row too, add nothing)
 #pragma unroll
-            for (int k = 0; k < 2 * V; ++k) ss += (k < V ? have[j] : have2[j]) ? x[j][k] * x[j][k] : 0.0f;
+            for (int k = 0; k < 2 * V; ++k) {
+                const bool in = k < V ? have[j] : have2[j];
+                x[j][k] = !in ? 0.0f : known ? x[j][k] : fill;
+                if constexpr (BACK) d[j][k] = !in ? 0.0f : known ? d[j][k] : fill;
+                ss += x[j][k] * x[j][k];
+            }
         }
-        for (int o = 1; o < G; o <<= 1) ss += __shfl_xor(ss, o);
+        cur = next;
+        ss = group_sum(ss, G);
         const float r = none ? 0.0f : 1.0f / sqrtf(ss * inv_width + a.eps);
         if constexpr (!BACK) {
 #pragma unroll
@@ -153,30 +202,21 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
                     x[j][k] *= r;
                     dw[j][k] += d[j][k] * x[j][k];
                     d[j][k] *= w[j][k];
-                    m += (k < V ? have[j] : have2[j]) ? d[j][k] * x[j][k] : 0.0f;
+                    m += d[j][k] * x[j][k];
                 }
             }
-            for (int o = 1; o < G; o <<= 1) m += __shfl_xor(m, o);
-            m *= inv_width;
+            m = group_sum(m, G) * inv_width;
 #pragma unroll
             for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int k = 0; k < 2 * V; ++k) x[j][k] = r * (d[j][k] - x[j][k] * m);
         }
         if (live) {
-            uint16_t *o = S.out + t * S.ot + head * S.oh;
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
-                if (have[j]) store_part<V>(o + at[j], &x[j][0]);
-                if (have2[j]) store_part<V>(o + at2[j], &x[j][V]);
+                if (have[j]) store_part<V, PAST>(out + at[j], &x[j][0]);
+                if (have2[j]) store_part<V, PAST>(out + at2[j], &x[j][V]);
             }
-        }
-        row += step;
-        t += step_t;
-        head += step_h;
-        if (head >= S.heads) {
-            head -= S.heads;
-            ++t;
         }
     }
     if constexpr (BACK) {
@@ -204,21 +244,25 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs a) {
     }
 }
 
-// dw from the blocks' sums: a block 16 columns of one side, 16 threads each,
-// which add every 16th block's, then those in order.
-__global__ __launch_bounds__(kThreads) void rope_dw_kernel(RopeArgs a) {
-    __shared__ float sums[16][17];
-    const int each = (a.width + 15) / 16, side = blockIdx.x / each, e = (blockIdx.x % each) * 16 + (threadIdx.x & 15);
+// dw from the blocks' sums: a block 16 columns of one side, 64 threads each,
+// which add every 64th block's, then those in order.
+__global__ __launch_bounds__(1024) void rope_dw_kernel(RopeArgs a) {
+    __shared__ float sums[64][17];
+    const int each = (a.width + 15) / 16, side = blockIdx.x / each, c = threadIdx.x & 15, r = threadIdx.x >> 4;
+    const int e = (blockIdx.x - side * each) * 16 + c;
     const RopeSide &S = a.side[side];
     const int b0 = side == 0 ? 0 : a.first_blocks, b1 = side == 0 ? a.first_blocks : a.blocks;
     float v = 0.0f;
-    if (e < a.width)
-        for (int b = b0 + (threadIdx.x >> 4); b < b1; b += 16) v += a.part[(int64_t)b * a.width + e];
-    sums[threadIdx.x >> 4][threadIdx.x & 15] = v;
+    if (e < a.width) {
+#pragma unroll 8
+        for (int b = b0 + r; b < b1; b += 64) v += a.part[(int64_t)b * a.width + e];
+    }
+    sums[r][c] = v;
     __syncthreads();
-    if (threadIdx.x < 16 && e < a.width && S.dw != nullptr) {
+    if (r == 0 && e < a.width && S.dw != nullptr) {
         v = 0.0f;
-        for (int k = 0; k < 16; ++k) v += sums[k][threadIdx.x];
+#pragma unroll 8
+        for (int k = 0; k < 64; ++k) v += sums[k][c];
         S.dw[e] = (uint16_t)tg_pack_bf16(v, 0.0f);
     }
 }
@@ -243,27 +287,37 @@ int piece(const RopeArgs &a) {
         if (a.width % (2 * v) == 0 && a.rot % (2 * v) == 0) return v;
     return 1;
 }
-template <bool BACK>
+template <bool BACK, bool PAST>
 hipError_t run(const RopeArgs &a, hipStream_t stream) {
     const size_t lds = BACK ? (size_t)(kThreads / 64) * a.width * 4 : 0;
     const dim3 grid((uint32_t)a.blocks), block(kThreads);
     switch (piece(a)) {
-        case 8: hipLaunchKernelGGL((rope_kernel<8, 1, BACK>), grid, block, lds, stream, a); break;
-        case 4: hipLaunchKernelGGL((rope_kernel<4, 1, BACK>), grid, block, lds, stream, a); break;
-        case 2: hipLaunchKernelGGL((rope_kernel<2, 2, BACK>), grid, block, lds, stream, a); break;
-        default: hipLaunchKernelGGL((rope_kernel<1, 4, BACK>), grid, block, lds, stream, a); break;
+        case 8: hipLaunchKernelGGL((rope_kernel<8, 1, BACK, PAST>), grid, block, lds, stream, a); break;
+        case 4: hipLaunchKernelGGL((rope_kernel<4, 1, BACK, PAST>), grid, block, lds, stream, a); break;
+        case 2: hipLaunchKernelGGL((rope_kernel<2, 2, BACK, PAST>), grid, block, lds, stream, a); break;
+        default: hipLaunchKernelGGL((rope_kernel<1, 4, BACK, PAST>), grid, block, lds, stream, a); break;
     }
     return hipGetLastError();
+}
+template <bool BACK>
+hipError_t run(const RopeArgs &a, hipStream_t stream) {
+    // Rows that do not fit the memory-side cache go past it: 65536 tokens of 40
+    // heads of 128 take 251 us forward and 358 back so, 273 and 404 otherwise; 8192
+    // (84 MB in) the same either way.
+    const int64_t bytes = a.tokens * (a.side[0].heads + a.side[1].heads) * a.width * 2 * (BACK ? 3 : 2);
+    return bytes > 2 * kCacheBytes ? run<BACK, true>(a, stream) : run<BACK, false>(a, stream);
 }
 
 }  // namespace
 
-void plan_rope(RopeArgs &a, bool back) {
+void plan_rope(RopeArgs &a) {
     const int v = piece(a), pieces = (a.width + 2 * v - 1) / (2 * v);
     int g = 1;
     while (g < pieces && g < 64) g <<= 1;
     a.group = g;
-    const int64_t per = kThreads / g, most = back ? 1024 : 4096;
+    // (as many blocks as the GPU's 256 CUs hold: forward 242 us with 1024, 251 with
+    // 4096; backward, whose blocks' sums are added up, 358, 364 with 2048)
+    const int64_t per = kThreads / g, most = 1024;
     const int64_t q = (a.tokens * a.side[0].heads + per - 1) / per, k = (a.tokens * a.side[1].heads + per - 1) / per;
     int64_t bq = q, bk = k;
     if (q + k > most) {
@@ -281,7 +335,7 @@ hipError_t launch_rope(const RopeArgs &a, hipStream_t stream) { return run<false
 hipError_t launch_rope_back(const RopeArgs &a, hipStream_t stream) {
     hipError_t e = a.blocks > 0 ? run<true>(a, stream) : hipSuccess;
     if (e == hipSuccess && (a.side[0].dw != nullptr || a.side[1].dw != nullptr)) {
-        hipLaunchKernelGGL(rope_dw_kernel, dim3((uint32_t)((a.width + 15) / 16 * 2)), dim3(kThreads), 0, stream, a);
+        hipLaunchKernelGGL(rope_dw_kernel, dim3((uint32_t)((a.width + 15) / 16 * 2)), dim3(1024), 0, stream, a);
         e = hipGetLastError();
     }
     return e;

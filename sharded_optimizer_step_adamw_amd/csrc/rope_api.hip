@@ -78,7 +78,7 @@ ZOPT_EXPORT zopt_status zopt_qk_norm_rope(int64_t T, int32_t heads_q, int32_t he
     RopeArgs a = common(T, heads_q, heads_k, width, rot, table, positions, position, eps, style);
     a.side[0] = RopeSide{q, nullptr, yq, q_token, q_head, 0, 0, yq_token, yq_head, w_q, nullptr, heads_q};
     a.side[1] = RopeSide{k, nullptr, yk, k_token, k_head, 0, 0, yk_token, yk_head, w_k, nullptr, heads_k};
-    plan_rope(a, false);
+    plan_rope(a);
     return device(launch_rope(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -98,7 +98,7 @@ ZOPT_EXPORT zopt_status zopt_qk_norm_rope_backward(
                         !writes_ok(T, heads_k, width, dk_token, dk_head)))
         return ZOPT_ERR_SIZE;
     RopeArgs a = common(T, heads_q, heads_k, width, rot, table, positions, position, eps, style);
-    plan_rope(a, true);
+    plan_rope(a);
     const bool sums = dw_q != nullptr || dw_k != nullptr;
     const size_t need = sums ? (size_t)up((int64_t)a.blocks * width * 4, 256) : 0;
     if (workspace == nullptr) {

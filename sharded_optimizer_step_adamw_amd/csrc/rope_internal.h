@@ -28,7 +28,7 @@ struct RopeArgs {
     int32_t blocks;
 };
 // Sets group and the blocks.
-void plan_rope(RopeArgs &a, bool back);
+void plan_rope(RopeArgs &a);
 hipError_t launch_rope(const RopeArgs &a, hipStream_t stream);
 hipError_t launch_rope_back(const RopeArgs &a, hipStream_t stream);
 hipError_t launch_rope_table(int64_t positions, int32_t rot, double base, float2 *table, hipStream_t stream);
