@@ -51,6 +51,25 @@ bool weight_needs_copy(const uint16_t *p, int64_t ld, int64_t group, int64_t col
     return !aligned16(p) || (ld & 7) || (group & 7) || (cols & 7) || ld > kMaxStride;
 }
 
+// A matrix [tokens, cols] whose rows the products take by expert: gathered as it
+// lies, or from a copy in the slots' order (row stride up(cols, 8)): where it
+// is not aligned, where it spans more than the products' 32-bit offsets reach,
+// and for the weight gradients.
+struct Rows {
+    const uint16_t *p, *slots;
+    int64_t ld;
+    bool gathered, copy;
+    size_t at;
+};
+Rows token_rows(const uint16_t *p, int64_t ld, int64_t tokens, int64_t top, int64_t cols, bool copy, Carve &c) {
+    Rows r{p, nullptr, ld, false, copy, 0};
+    r.gathered = aligned16(p) && !(ld & 7) && !(cols & 7) && ld <= kMaxStride &&
+                 ((tokens - 1) * ld + cols) * 2 <= kGatherBytes;
+    r.copy = copy || !r.gathered;
+    if (r.copy) r.at = c.take(tokens * top * up(cols, 8) * 2);
+    return r;
+}
+
 // What a call does, from its sizes alone: both the size query and the call make
 // it.
 struct MoePlan {
@@ -58,7 +77,8 @@ struct MoePlan {
     int32_t E, k;
     bool back;
     Weight wg, wu, wd;
-    size_t x, dy, share, h, dh, dg, du, rows, dot, sizes, part, total;
+    Rows x, dy;
+    size_t token, share, h, dh, dg, du, rows, dot, sizes, part, total;
     int64_t parts;  // dots of a slot
     size_t tiles[3];
     TgLaunch glu, down, dhf, dx, dwgu, dwd;
@@ -71,6 +91,7 @@ struct MoePlan {
         L.N = (int32_t)N;
         L.groups = E;
         L.slots = (int32_t)S;
+        L.tokens = (int32_t)T;
         return L;
     }
     static TgSegment segment(TgOperand a, TgOperand b) {
@@ -80,6 +101,9 @@ struct MoePlan {
     // operands: the slots' rows along the reduction and across it, a weight's
     TgOperand slots_along(const void *p, int64_t ld, int64_t cols) const {
         return TgOperand{static_cast<const uint16_t *>(p), ld, (int32_t)S, (int32_t)up(cols, 8)};
+    }
+    TgOperand rows_along(const Rows &r, int64_t cols) const {
+        return r.gathered ? slots_along(r.p, r.ld, cols) : slots_along(r.slots, up(cols, 8), cols);
     }
     TgOperand slots_across(const void *p, int64_t ld, int64_t cols) const {
         return TgOperand{static_cast<const uint16_t *>(p), ld, (int32_t)up(cols, 8), (int32_t)S};
@@ -96,7 +120,8 @@ struct MoePlan {
     int32_t average() const { return (int32_t)((S / E + 63) / 64 * 2); }
 };
 
-MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const uint16_t *wg, const uint16_t *wu,
+MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const uint16_t *x, int64_t ldx,
+                 const uint16_t *dy, int64_t lddy, const uint16_t *wg, const uint16_t *wu,
                  int64_t ldw, int64_t groupw, const uint16_t *wd, int64_t ldd, int64_t groupd, bool back) {
     MoePlan p{};
     Carve c;
@@ -119,18 +144,19 @@ MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const ui
         p.total = c.total();
         return p;
     }
-    p.x = c.take(S * p.Dp * 2);
+    p.x = token_rows(x, ldx, T, k, D, back, c);
+    p.token = c.take(S * 4);
     p.h = c.take(S * p.Fp * 2);
     p.rows = c.take(S * p.Dp * 2);
     p.glu = p.launch(S, F);
     p.glu.prob[0].seg[0].stages = (int32_t)((p.Dp + 63) / 64 * 2);
-    plan_groups(back ? kTgMoeBack : kTgGlu, kGroupRows, p.glu);
+    plan_groups(back ? kTgMoeBack : kTgGlu, kGroupRows, false, p.glu);
     if (!back) {
         p.down = p.launch(S, D);
         p.down.prob[0].seg[0].stages = (int32_t)((p.Fp + 63) / 64 * 2);
-        plan_groups(kTgStore, kGroupRows, p.down);
+        plan_groups(kTgStore, kGroupRows, false, p.down);
     } else {
-        p.dy = c.take(S * p.Dp * 2);
+        p.dy = token_rows(dy, lddy, T, k, D, true, c);
         p.share = c.take(S * 4);
         p.dh = c.take(S * p.Fp * 4);
         p.dg = c.take(S * p.Fp * 2);
@@ -140,18 +166,18 @@ MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const ui
         p.sizes = c.take(E * 4);
         p.dhf = p.launch(S, F);
         p.dhf.prob[0].seg[0].stages = (int32_t)((p.Dp + 63) / 64 * 2);
-        plan_groups(kTgFloat, kGroupRows, p.dhf);
+        plan_groups(kTgFloat, kGroupRows, true, p.dhf);
         p.dx = p.launch(S, D);
         p.dx.prob[0].nseg = 2;
         p.dx.prob[0].seg[0].stages = p.dx.prob[0].seg[1].stages = (int32_t)((p.Fp + 63) / 64 * 2);
-        plan_groups(kTgStore, kGroupRows, p.dx);
+        plan_groups(kTgStore, kGroupRows, true, p.dx);
         p.dwgu = p.launch(F, D);
         p.dwgu.nprob = 2;
         p.dwgu.prob[0].seg[0].stages = p.average();
-        plan_groups(kTgStore, kGroupDepth, p.dwgu);
+        plan_groups(kTgStore, kGroupDepth, true, p.dwgu);
         p.dwd = p.launch(D, F);
         p.dwd.prob[0].seg[0].stages = p.average();
-        plan_groups(kTgStore, kGroupDepth, p.dwd);
+        plan_groups(kTgStore, kGroupDepth, true, p.dwd);
         p.part = c.take(larger(group_part_bytes(kGroupDepth, p.dwgu), group_part_bytes(kGroupDepth, p.dwd)));
     }
     const TgLaunch *rows[3] = {&p.glu, back ? &p.dhf : &p.down, back ? &p.dx : nullptr};
@@ -187,13 +213,13 @@ struct Preps {
         j.tiles = reinterpret_cast<TgTileRow *>(ws + at);
         L.tile_row = j.tiles;
     }
-    MoePrep &gather(const uint16_t *src, int64_t ld, int64_t cols, void *dst) {
+    void place(Rows &r, int64_t cols, char *ws) {
+        if (!r.copy) return;
         MoePrep &j = add(kMoeGather);
-        j.src = src;
-        j.ld = ld;
+        j.src = r.p;
+        j.ld = r.ld;
         j.cols = cols;
-        j.dst = static_cast<uint16_t *>(dst);
-        return j;
+        r.slots = j.dst = reinterpret_cast<uint16_t *>(ws + r.at);
     }
 };
 
@@ -235,7 +261,7 @@ ZOPT_EXPORT zopt_status zopt_moe_route(int64_t T, int32_t experts, int32_t top, 
     const PlanArgs p = plan_args(T, experts, top, each, chosen, workspace, offsets, order, place);
     if (T == 0) return device(launch_plan(p, s));
     const RouteArgs a{T, experts, top, bf16, score == ZOPT_SCORE_SIGMOID, groups, top_groups, renormalise, scale, logits,
-                      ld, bias, chosen, weights, p.block_tokens};
+                      ld, bias, chosen, weights, p.block_tokens, 0};
     return device(launch_route(a, p, s));
 }
 
@@ -302,7 +328,8 @@ ZOPT_EXPORT zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_
     const zopt_status st = check_moe(T, D, F, experts, top, ldx, ldw, w_expert, ldd, wd_expert);
     if (st != ZOPT_OK) return st;
     if (!stride_ok(ldy, D)) return ZOPT_ERR_SIZE;
-    MoePlan p = moe_plan(T, D, F, experts, top, w_gate, w_up, ldw, w_expert, w_down, ldd, wd_expert, false);
+    MoePlan p = moe_plan(T, D, F, experts, top, x, ldx, nullptr, 0, w_gate, w_up, ldw, w_expert, w_down, ldd, wd_expert,
+                         false);
     if (workspace == nullptr) {
         *workspace_bytes = p.total;
         return ZOPT_OK;
@@ -327,9 +354,10 @@ ZOPT_EXPORT zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_
     preps.place(p.wg, ldw, w_expert, experts, F, D, ws);
     preps.place(p.wu, ldw, w_expert, experts, F, D, ws);
     preps.place(p.wd, ldd, wd_expert, experts, D, F, ws);
-    preps.gather(x, ldx, D, ws + p.x);
+    preps.place(p.x, D, ws);
+    p.glu.token = preps.add(kMoeTokens).token = reinterpret_cast<int32_t *>(ws + p.token);
     ZOPT_TRY(launch_moe_prep(preps.list, s));
-    const TgOperand xs = p.slots_along(ws + p.x, p.Dp, D);
+    const TgOperand xs = p.rows_along(p.x, D);
     p.glu.prob[0].nseg = 2;
     p.glu.prob[0].seg[0] = MoePlan::segment(xs, MoePlan::along(p.wg, F, D));
     p.glu.prob[0].seg[1] = MoePlan::segment(xs, MoePlan::along(p.wu, F, D));
@@ -337,7 +365,7 @@ ZOPT_EXPORT zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_
     p.glu.act = act;
     p.glu.h = reinterpret_cast<uint16_t *>(ws + p.h);
     p.glu.ldc = p.Fp;
-    ZOPT_TRY(launch_rows_glu(p.glu, s));
+    ZOPT_TRY(launch_rows_glu(p.x.gathered, p.glu, s));
     p.down.prob[0].seg[0] = MoePlan::segment(p.slots_along(ws + p.h, p.Fp, F), MoePlan::along(p.wd, D, F));
     p.down.prob[0].out = reinterpret_cast<uint16_t *>(ws + p.rows);
     p.down.ldc = p.Dp;
@@ -371,7 +399,8 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     if (st != ZOPT_OK) return st;
     if (!stride_ok(lddy, D) || !stride_ok(lddx, D) || !stride_ok(lddw, D) || !stride_ok(lddd, F)) return ZOPT_ERR_SIZE;
     if (!group_ok(dw_expert, lddw, F, D) || !group_ok(dwd_expert, lddd, D, F)) return ZOPT_ERR_SIZE;
-    MoePlan p = moe_plan(T, D, F, experts, top, w_gate, w_up, ldw, w_expert, w_down, ldd, wd_expert, true);
+    MoePlan p = moe_plan(T, D, F, experts, top, x, ldx, dy, lddy, w_gate, w_up, ldw, w_expert, w_down, ldd, wd_expert,
+                         true);
     if (workspace == nullptr) {
         *workspace_bytes = p.total;
         return ZOPT_OK;
@@ -405,19 +434,22 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     preps.place(p.wg, ldw, w_expert, experts, F, D, ws);
     preps.place(p.wu, ldw, w_expert, experts, F, D, ws);
     preps.place(p.wd, ldd, wd_expert, experts, D, F, ws);
-    preps.gather(x, ldx, D, ws + p.x);
-    MoePrep &j = preps.gather(dy, lddy, D, ws + p.dy);
+    preps.place(p.x, D, ws);
+    preps.place(p.dy, D, ws);
+    MoePrep &j = preps.add(kMoeTokens);
+    j.token = reinterpret_cast<int32_t *>(ws + p.token);
     j.weights = weights;
     j.share = reinterpret_cast<float *>(ws + p.share);
+    for (TgLaunch *L : {&p.dhf, &p.glu}) L->token = j.token;
     ZOPT_TRY(launch_moe_prep(preps.list, s));
     // dh = dy w_down, before the slots' weights
-    p.dhf.prob[0].seg[0] = MoePlan::segment(p.slots_along(ws + p.dy, p.Dp, D), MoePlan::across(p.wd, D, F));
+    p.dhf.prob[0].seg[0] = MoePlan::segment(p.rows_along(p.dy, D), MoePlan::across(p.wd, D, F));
     p.dhf.prob[0].sum = reinterpret_cast<float *>(ws + p.dh);
     p.dhf.ldsum = p.Fp;
     p.dhf.group_stride = p.wd.group;
-    ZOPT_TRY(launch_rows_float(p.dhf, s));
+    ZOPT_TRY(launch_rows_float(p.dy.gathered, p.dhf, s));
     // g and u again; dg, du, share h and the dots
-    const TgOperand xs = p.slots_along(ws + p.x, p.Dp, D);
+    const TgOperand xs = p.rows_along(p.x, D);
     p.glu.prob[0].nseg = 2;
     p.glu.prob[0].seg[0] = MoePlan::segment(xs, MoePlan::along(p.wg, F, D));
     p.glu.prob[0].seg[1] = MoePlan::segment(xs, MoePlan::along(p.wu, F, D));
@@ -433,7 +465,7 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     p.glu.share = reinterpret_cast<const float *>(ws + p.share);
     p.glu.dot = reinterpret_cast<float *>(ws + p.dot);
     p.glu.lddot = p.parts;
-    ZOPT_TRY(launch_rows_back(p.glu, s));
+    ZOPT_TRY(launch_rows_back(p.x.gathered, p.glu, s));
     // dx = dg w_gate + du w_up, a row a slot, then summed over each token's
     p.dx.prob[0].seg[0] = MoePlan::segment(p.slots_along(ws + p.dg, p.Fp, F), MoePlan::across(p.wg, F, D));
     p.dx.prob[0].seg[1] = MoePlan::segment(p.slots_along(ws + p.du, p.Fp, F), MoePlan::across(p.wu, F, D));
@@ -463,7 +495,7 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
         L->by_size = sizes;
         L->part = reinterpret_cast<float *>(ws + p.part);
     }
-    const TgOperand xa = p.slots_across(ws + p.x, p.Dp, D);
+    const TgOperand xa = p.slots_across(p.x.slots, p.Dp, D);
     p.dwgu.prob[0].seg[0].a = p.slots_across(ws + p.dg, p.Fp, F);
     p.dwgu.prob[0].seg[0].b = xa;
     p.dwgu.prob[1].nseg = 1;
@@ -474,7 +506,7 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     p.dwgu.ldc = lddw;
     p.dwgu.group_out = dw_expert;
     ZOPT_TRY(launch_depth(p.dwgu, s));
-    p.dwd.prob[0].seg[0].a = p.slots_across(ws + p.dy, p.Dp, D);
+    p.dwd.prob[0].seg[0].a = p.slots_across(p.dy.slots, p.Dp, D);
     p.dwd.prob[0].seg[0].b = p.slots_across(ws + p.h, p.Fp, F);
     p.dwd.prob[0].out = dw_down;
     p.dwd.ldc = lddd;

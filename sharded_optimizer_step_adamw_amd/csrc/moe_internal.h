@@ -21,6 +21,7 @@ struct RouteArgs {
     int32_t *chosen;      // [tokens, top]
     float *weights;       // [tokens, top]
     int32_t block_tokens;
+    int32_t sort_here;    // (set by the launch) the one block, of all its threads, also sorts
 };
 // Slots sorted by expert, stable: from the choice and the blocks' counts.
 struct PlanArgs {
@@ -43,7 +44,7 @@ struct RouteBackArgs {
 };
 // Tokens of a block (experts 0: that only sorts).
 int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top);
-hipError_t launch_route(const RouteArgs &a, const PlanArgs &plan, hipStream_t stream);
+hipError_t launch_route(RouteArgs a, const PlanArgs &plan, hipStream_t stream);
 hipError_t launch_plan_count(const PlanArgs &a, hipStream_t stream);
 hipError_t launch_plan(const PlanArgs &a, hipStream_t stream);
 hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);
@@ -54,17 +55,18 @@ hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);
 //   kMoeTiles   the tile rows of height `height` (TgTileRow [1 + capacity]) from
 //               the offsets
 //   kMoeSizes   the experts, the one with the most rows first
-//   kMoeGather  dst [slots, round8(cols)] = the slots' rows of src, zero beyond
-//               cols; share (or NULL): the slots' weights
+//   kMoeTokens  token [slots]: the slots' tokens (-1: none); share (or
+//               NULL): their weights
+//   kMoeGather  dst [slots, round8(cols)] = the slots' rows of src, zero beyond cols
 //   kMoeCopy    dst [rows, round8(cols)] = src's rows, of which each
 //               `group_rows` lie `group_stride` apart
-enum MoePrepKind : int { kMoeTiles = 0, kMoeSizes = 1, kMoeGather = 2, kMoeCopy = 3 };
+enum MoePrepKind : int { kMoeTiles = 0, kMoeSizes = 1, kMoeGather = 2, kMoeCopy = 3, kMoeTokens = 4 };
 struct MoePrep {
     int32_t kind;
     uint32_t blocks;              // set by the launch
     int32_t height, capacity;
     TgTileRow *tiles;
-    int32_t *sizes;
+    int32_t *sizes, *token;
     int64_t rows, cols;
     const uint16_t *src;
     int64_t ld, group_rows, group_stride;
@@ -72,7 +74,7 @@ struct MoePrep {
     const float *weights;
     float *share;
 };
-constexpr int kMaxMoePreps = 10;
+constexpr int kMaxMoePreps = 11;
 struct MoePrepList {
     MoePrep job[kMaxMoePreps];
     int32_t n;
@@ -106,13 +108,13 @@ hipError_t launch_fill_zero_groups(uint16_t *dst, int64_t ld, int64_t group_stri
                                    int64_t cols, hipStream_t stream);
 
 // The products (train_internal.h's kinds, over groups).
-void plan_groups(TgEpilogue epi, TgGroups kind, TgLaunch &L);
+void plan_groups(TgEpilogue epi, TgGroups kind, bool b_km, TgLaunch &L);
 int tile_height(int tile);
 size_t group_part_bytes(TgGroups kind, const TgLaunch &L);
-hipError_t launch_rows_glu(TgLaunch &L, hipStream_t stream);                   // kTgGlu
+hipError_t launch_rows_glu(bool gather, TgLaunch &L, hipStream_t stream);      // kTgGlu
 hipError_t launch_rows_store(bool b_km, TgLaunch &L, hipStream_t stream);      // kTgStore
-hipError_t launch_rows_float(TgLaunch &L, hipStream_t stream);                 // kTgFloat, B k-major
-hipError_t launch_rows_back(TgLaunch &L, hipStream_t stream);                  // kTgMoeBack
+hipError_t launch_rows_float(bool gather, TgLaunch &L, hipStream_t stream);    // kTgFloat, B k-major
+hipError_t launch_rows_back(bool gather, TgLaunch &L, hipStream_t stream);     // kTgMoeBack
 hipError_t launch_depth(TgLaunch &L, hipStream_t stream);                      // kTgStore, both k-major
 
 }  // namespace zopt

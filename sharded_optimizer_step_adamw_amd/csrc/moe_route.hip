@@ -218,6 +218,7 @@ __device__ __forceinline__ Pick choose(const RouteLane &l, K (&rank)[NV], const 
 // all of them (NULL: this one's own).  Each wave walks a part of the slots in
 // order; lanes with one expert find each other by the bits of its number.
 // next: LDS, [waves + 1][experts].
+// (THREADS: the block's)
 template <int THREADS>
 __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blocks, const int32_t *base,
                                            const int32_t *total, int *next) {
@@ -412,12 +413,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, PlanA
         }
     }
     __syncthreads();
-    if (gridDim.x == 1) {
+    if (a.sort_here) {
         __threadfence_block();
         __syncthreads();
         sort_block<kRouteThreads>(plan, 0, 1, nullptr, nullptr, hist);
         return;
     }
+    // (one block's slots are counted where they are sorted)
+    if (gridDim.x == 1) return;
     for (int e = threadIdx.x; e < E; e += blockDim.x) plan.counts[(int64_t)blockIdx.x * E + e] = hist[e];
 }
 
@@ -590,12 +593,13 @@ int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int3
     return (int32_t)(each < least ? least : each);
 }
 
-hipError_t launch_route(const RouteArgs &a, const PlanArgs &plan, hipStream_t stream) {
+hipError_t launch_route(RouteArgs a, const PlanArgs &plan, hipStream_t stream) {
     const Lanes l = lanes_of(a.experts, a.top);
     const uint32_t blocks = (uint32_t)blocks_of(a.tokens, a.block_tokens);
     const int threads = route_lds(a.experts, a.groups, a.top, kRouteThreads) <= kRouteLds ? kRouteThreads : 256;
     const size_t choice = route_lds(a.experts, a.groups, a.top, threads);
-    const size_t sort = blocks == 1 ? (size_t)(kRouteThreads / 64 + 1) * a.experts * 4 : 0;
+    a.sort_here = blocks == 1 && threads == kRouteThreads;
+    const size_t sort = a.sort_here ? (size_t)(kRouteThreads / 64 + 1) * a.experts * 4 : 0;
     const size_t bytes = choice > sort ? choice : sort;
     const dim3 grid(blocks), block(threads);
     if (l.nv == 1) hipLaunchKernelGGL(route_kernel<1>, grid, block, bytes, stream, a, plan, l.G);
@@ -604,7 +608,7 @@ hipError_t launch_route(const RouteArgs &a, const PlanArgs &plan, hipStream_t st
     else if (l.nv == 8) hipLaunchKernelGGL(route_kernel<8>, grid, block, bytes, stream, a, plan, l.G);
     else hipLaunchKernelGGL(route_kernel<16>, grid, block, bytes, stream, a, plan, l.G);
     hipError_t e = hipGetLastError();
-    return e == hipSuccess && blocks > 1 ? launch_plan(plan, stream) : e;
+    return e == hipSuccess && !a.sort_here ? launch_plan(plan, stream) : e;
 }
 
 hipError_t launch_plan_count(const PlanArgs &a, hipStream_t stream) {

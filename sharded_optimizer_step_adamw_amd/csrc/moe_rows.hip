@@ -37,7 +37,7 @@ __device__ __forceinline__ void bounds(const MoePrepList &l, int e, int &lo, int
 }
 
 __device__ __forceinline__ void prep_tiles(const MoePrepList &l, const MoePrep &j) {
-    __shared__ int at[kMaxExperts + 1];
+    __shared__ int at[kMaxExperts];
     __shared__ int part[kThreads];
     constexpr int kEach = kMaxExperts / kThreads;
     int lo, n, sum = 0;
@@ -93,16 +93,40 @@ __device__ __forceinline__ void prep_sizes(const MoePrepList &l, const MoePrep &
     }
 }
 
+// A wave four times 1 KiB of a row, so that what leads to a row is read once for
+// them: 16 bytes a thread took half as long again.
+constexpr int kGatherPieces = 4 * 64;
 __device__ __forceinline__ void prep_gather(const MoePrepList &l, const MoePrep &j, int64_t block) {
-    const int64_t per = (j.cols + 7) / 8, total = (int64_t)within(l.offsets[l.experts], l.slots) * per;
-    for (int64_t id = block * kThreads + threadIdx.x; id < total; id += (int64_t)j.blocks * kThreads) {
-        const int64_t s = id / per, c = (id - s * per) * 8, left = j.cols - c;
+    const int64_t per = (j.cols + 7) / 8, chunks = (per + kGatherPieces - 1) / kGatherPieces;
+    const int64_t total = within(l.offsets[l.experts], l.slots) * chunks;
+    const int lane = threadIdx.x & 63;
+    for (int64_t id = (block * kThreads + threadIdx.x) >> 6; id < total; id += (int64_t)j.blocks * (kThreads / 64)) {
+        const int64_t s = id / chunks, c0 = (id - s * chunks) * kGatherPieces + lane;
         const int slot = l.order[s];
         const bool some = slot >= 0 && slot < l.slots;
-        tg_u32x4 v{0, 0, 0, 0};
-        if (some) v = tg_load8h(j.src + (int64_t)(slot / l.top) * j.ld + c, left > 8 ? 8 : (int)left);
-        *reinterpret_cast<tg_u32x4 *>(j.dst + id * 8) = v;
-        if (j.share != nullptr && c == 0) j.share[s] = some ? j.weights[slot] : 0.0f;
+        const uint16_t *from = j.src + (int64_t)(some ? slot / l.top : 0) * j.ld;
+        uint16_t *to = j.dst + s * per * 8;
+        tg_u32x4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t c = c0 + i * 64;
+            v[i] = tg_u32x4{0, 0, 0, 0};
+            if (some && c < per) v[i] = tg_load8h(from + c * 8, j.cols - c * 8 > 8 ? 8 : (int)(j.cols - c * 8));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t c = c0 + i * 64;
+            if (c < per) *reinterpret_cast<tg_u32x4 *>(to + c * 8) = v[i];
+        }
+    }
+}
+
+__device__ __forceinline__ void prep_tokens(const MoePrepList &l, const MoePrep &j, int64_t block) {
+    for (int64_t s = block * kThreads + threadIdx.x; s < l.slots; s += (int64_t)j.blocks * kThreads) {
+        const int slot = l.order[s];
+        const bool some = slot >= 0 && slot < l.slots;
+        j.token[s] = some ? slot / l.top : -1;
+        if (j.share != nullptr) j.share[s] = some ? j.weights[slot] : 0.0f;
     }
 }
 
@@ -126,6 +150,8 @@ __global__ __launch_bounds__(kThreads) void moe_prep_kernel(MoePrepList list) {
         prep_sizes(list, j);
     else if (j.kind == kMoeGather)
         prep_gather(list, j, block);
+    else if (j.kind == kMoeTokens)
+        prep_tokens(list, j, block);
     else
         prep_copy(j, block);
 }
@@ -179,8 +205,11 @@ hipError_t launch_moe_prep(MoePrepList &list, hipStream_t stream) {
     uint32_t total = 0;
     for (int k = 0; k < list.n; ++k) {
         MoePrep &j = list.job[k];
-        const int64_t rows = j.kind == kMoeGather ? list.slots : j.rows;
-        j.blocks = j.kind == kMoeTiles || j.kind == kMoeSizes ? 1 : blocks_for(rows * ((j.cols + 7) / 8));
+        const int64_t per = (j.cols + 7) / 8;
+        j.blocks = j.kind == kMoeTiles || j.kind == kMoeSizes ? 1
+                   : j.kind == kMoeTokens                     ? blocks_for(list.slots)
+                   : j.kind == kMoeGather ? blocks_for(list.slots * ((per + kGatherPieces - 1) / kGatherPieces) * 64)
+                                          : blocks_for(j.rows * per);
         total += j.blocks;
     }
     if (total == 0) return hipSuccess;

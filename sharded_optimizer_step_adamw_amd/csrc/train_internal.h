@@ -46,6 +46,8 @@ enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3, k
 //   kGroupDepth  those are the reduction of A and B; each group has an output
 //                (out, and group_out)
 enum TgGroups : int { kNoGroups = 0, kGroupRows = 1, kGroupDepth = 2 };
+// What a gathered operand spans at most (its offsets are 32 bits wide).
+constexpr int64_t kGatherBytes = 0xFFFF0000ll;
 // A tile row of kGroupRows: its group, its first row and the group's last.
 // The list's first entry holds the number of the others (in `group`).
 struct TgTileRow {
@@ -119,6 +121,10 @@ struct TgLaunch {
     const int32_t *by_size;   // kGroupDepth: the groups, the largest first
     const TgTileRow *tile_row;
     int32_t groups, slots;    // (no row of a group is past slots)
+    // gathered A (kGroupRows): row r is row token[r] of the operand, which has `tokens`
+    // (negative: a row of zeros)
+    const int32_t *token;
+    int32_t tokens;
     int64_t group_stride, group_out;
 };
 

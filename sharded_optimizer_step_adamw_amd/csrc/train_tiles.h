@@ -537,7 +537,15 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, i
 // kGroupDepth: every group has all tiles, the largest group's first, so that the
 // tiles of a round take about the same time; a group without rows has tiles of
 // zeros.
-template <int TILE, int EPI, bool AKM, bool BKM, int GRP = kNoGroups>
+// (A wave whose rows lie behind the tile's end multiplies zeros.  Leaving its
+// products out changed nothing, a stage of one wave a SIMD being bound by its
+// synchronisation, nor did taking such tiles last.)
+// A gathered A: a lane's rows have offsets of their own, read from the list of
+// rows a tile ahead.  On [32768, 4096] gathered from 8192 tokens the gate's
+// products take 877 us so, 899 and 77 for a copy in order otherwise.  (Gathering
+// the k-major operands of the weight gradients by scalar loads a stage ahead was
+// 30% slower than from such a copy, and the copies cost 12%.)
+template <int TILE, int EPI, bool AKM, bool BKM, int GRP = kNoGroups, bool LIST = false>
 __global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64)
 __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) {
     using C = Cfg<TILE>;
@@ -554,6 +562,8 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     static_assert(!GLU || NW % 4 == 0, "a wave loads rows of the gate or of the up projection");
     constexpr int BO = GLU ? BN / 2 : BN;  // output columns of a tile
     constexpr int kOut = 0x7FFFFFF0;       // a byte offset past every descriptor
+    constexpr int kFar = (int)kGatherBytes;  // ... and past a gathered operand's
+    static_assert(!LIST || (GRP == kGroupRows && !AKM), "gathered rows are A's, row-major");
     // exponentials: the targets of a tile's rows, of this tile and the next
     constexpr bool XENT = EPI == kTgXent;
     constexpr int TGB = XENT ? (BM * 8 < 1024 ? 1024 : BM * 8) : 0;
@@ -628,7 +638,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         T.stage0 = T.split < 0 ? 0 : T.split * part;
         T.live = all - T.stage0;
         if (T.split >= 0 && T.live > part) T.live = part;
-        if (GRP == kGroupDepth && T.live < 0) T.live = 0;
+        if (GRP == kGroupDepth && T.live <= 0) T.live = T.stage0 = 0;  // (a part past the group's end: zeros)
         T.stages = T.live < 4 ? 4 : T.live;  // (the switch to the next tile is kStages before)
         return true;
     };
@@ -646,7 +656,9 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     const uint16_t *pa = nullptr, *pb = nullptr;
     int ka = 0, kb = 0, lda = 0, ldb = 0, ea = 0, eb = 0, seg_left = 0, total_left = 0;
     int sprob = 0, sm0 = 0, sn0 = 0, sgroup = 0, sfirst = 0, send = 0;
-    int va[PAIRS ? 1 : LA], vb[PAIRS ? 1 : LB];
+    int va[PAIRS && !LIST ? 1 : LA], vb[PAIRS ? 1 : LB];
+    // LIST: the operand's rows of the next tile
+    int ahead[LIST ? LA : 1];
     // row-major: the lane's row of a kilobyte's and its k offset
     const int krow = PAIRS ? lane >> 3 : lane >> 2;
     const int chunk8 = (PAIRS ? (lane & 7) ^ (lane >> 3) : (lane & 3) ^ ((lane >> 3) & 3)) << 3;
@@ -684,6 +696,15 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
             e = ((left < extent ? left : extent) - 1) * ld * 2;
         }
     };
+    auto fetch_list = [&](const Tile &T) __attribute__((always_inline)) {
+        if constexpr (LIST) {
+#pragma unroll
+            for (int x = 0; x < LA; ++x) {
+                const int row = T.m0 + first_a * (16 / SPL) + krow + rows_a(x);
+                ahead[x] = row < T.end ? L.token[row] : -1;
+            }
+        }
+    };
     auto open_segment = [&](int s, int k0) __attribute__((always_inline)) {
         const TgProblem &P = L.prob[sprob];
         const TgSegment &S = P.seg[s];
@@ -698,7 +719,14 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         seg_left = S.stages - k0 / kBK;
         if constexpr (GRP == kGroupRows) {
             const TgOperand &B = GLU && (wave & 2) ? P.seg[1].b : S.b;
-            corner(TgOperand{S.a.p, S.a.ld, send, S.a.k}, AKM, sm0, BM, k0, pa, ka, lda, ea);
+            if constexpr (LIST) {
+                pa = S.a.p + k0;
+                ka = S.a.k - k0;
+                lda = (int)S.a.ld;
+                ea = (int)((uint32_t)(L.tokens - 1) * (uint32_t)lda * 2u);
+            } else {
+                corner(TgOperand{S.a.p, S.a.ld, send, S.a.k}, AKM, sm0, BM, k0, pa, ka, lda, ea);
+            }
             corner(TgOperand{B.p + sgroup * L.group_stride, B.ld, B.outer, B.k}, BKM, sn0, BO, k0, pb, kb, ldb, eb);
             return;
         }
@@ -735,15 +763,21 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         const int blk = first_b / SPL, n = (first_b & (SPL - 1)) * 8 + krow;
         const int row = (GLU ? blk >> 2 : blk >> 1) * 32 + 8 * (n >> 2) + 4 * (blk & 1) + (n & 3);
         const int base_b = BKM ? across(first_b, BN, ldb, eb) : (row * ldb + chunk8) * 2;
+        if constexpr (LIST) {
 #pragma unroll
-        for (int x = 0; x < (PAIRS ? 1 : LA); ++x) va[x] = plus(base_a, rows_a(x) * lda);
+            for (int x = 0; x < LA; ++x)
+                va[x] = ahead[x] < 0 ? kFar : (int)(((uint32_t)ahead[x] * (uint32_t)lda + (uint32_t)chunk8) * 2u);
+        } else {
+#pragma unroll
+            for (int x = 0; x < (PAIRS ? 1 : LA); ++x) va[x] = plus(base_a, rows_a(x) * lda);
+        }
 #pragma unroll
         for (int x = 0; x < (PAIRS ? 1 : LB); ++x) vb[x] = plus(base_b, rows_b(x) * ldb);
     };
     auto extent = [&](bool km, int k, int ld, int e) __attribute__((always_inline)) -> int {
         if (total_left <= 0 || k <= 0) return 0;
         if (km) return ((k < kBK * SPL ? k : kBK * SPL) - 1) * ld * 2 + e;
-        return e + k * 2;
+        return (int)((uint32_t)e + (uint32_t)k * 2u);
     };
     // load y: A's kilobytes, then B's
     __amdgpu_buffer_rsrc_t ra, rb;
@@ -755,8 +789,13 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         // (a chunk past the row's end would be the next row's)
         if (y < LA) {
             const int kilo = first_a + kx(spread_a, y);
-            const int first = AKM || chunk8 < ka ? va[PAIRS ? 0 : y] : kOut;
-            const int o = PAIRS ? plus(first, rows_a(y) * lda) : first;
+            int o;
+            if constexpr (LIST) {
+                o = chunk8 < ka ? va[y] : kFar;
+            } else {
+                const int first = AKM || chunk8 < ka ? va[PAIRS ? 0 : y] : kOut;
+                o = PAIRS ? plus(first, rows_a(y) * lda) : first;
+            }
             __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, LDS_ADDR(&lds[sbase + kilo * 1024]), 16, o, 0, 0, 0);
         } else {
             const int x = y - LA, kilo = first_b + kx(spread_b, x);
@@ -911,6 +950,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     int slot = seek(blockIdx.x, cu);
     if (slot < 0) return;
     load_targets(cu, 0);
+    fetch_list(cu);
     stream(cu, true);
 #pragma unroll
     for (int s = 0; s < kStages; s += SPL) {
@@ -934,6 +974,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = tg_f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (more) fetch_list(nx);
         // (from stage kStages before the end on, the loads are the next tile's
         // first ones, or zeros)
 #pragma clang loop unroll(disable)
@@ -1018,7 +1059,7 @@ int compute_units() {
     return cus;
 }
 
-template <int TILE, int EPI, bool AKM, bool BKM, int GRP = kNoGroups>
+template <int TILE, int EPI, bool AKM, bool BKM, int GRP = kNoGroups, bool LIST = false>
 hipError_t run(TgLaunch &L, hipStream_t stream) {
     using C = Cfg<TILE>;
     constexpr bool GLU = EPI == kTgGlu || EPI == kTgGluBack || EPI == kTgMoeBack;
@@ -1035,7 +1076,7 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
     L.padded = (L.total + 7) / 8 * 8;
     const int64_t round = (int64_t)compute_units() * (C::WPE * 4 / (threads / 64));
     const uint32_t grid = (uint32_t)(L.padded < round ? L.padded : round);
-    hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM, GRP>), dim3(grid + ((EPI == kTgStore || EPI == kTgSum) && L.sum_up.loss != nullptr ? 1 : 0)),
+    hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM, GRP, LIST>), dim3(grid + ((EPI == kTgStore || EPI == kTgSum) && L.sum_up.loss != nullptr ? 1 : 0)),
                        dim3(threads), 0, stream, L);
     hipError_t e = hipGetLastError();
     if (GRP != kGroupRows && e == hipSuccess && L.splits > 1) {
