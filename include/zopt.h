@@ -912,8 +912,9 @@ zopt_status zopt_moe_route_backward(int64_t T, int32_t experts, int32_t top,
  *                 (Others give wrong sums, but no access outside the buffers.)
  *   y             bf16 [T, D], row stride ldy, written.
  * The sizes of the experts' shares stay on the device: nothing waits for them.
- * h and a slot's row of y are rounded to bf16 (8 bits: as a dense layer's h and
- * output are), sums are fp32.
+ * Sums are fp32; h is rounded to bf16 between the products, as a dense layer's is,
+ * and a slot's row of y, before the sum over the token's slots, to 11 bits (fp16
+ * with a power of two for 64 neighbours), as y to bf16 in the end.
  * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE; ZOPT_ERR_HYPER (act);
  * ZOPT_ERR_WORKSPACE; ZOPT_ERR_DEVICE.
  */
@@ -934,8 +935,9 @@ zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_t experts, i
  *                 dwd_expert; zero for experts without a token.
  *   dweights      float [T, top], 0 for slots without an expert.
  * All are written.  A row of x and of dy whose token has no expert reaches
- * none of them.  dg, du, weight h and a slot's row of dx are rounded to bf16
- * between the products; dy w_down, and with it dweights, is kept in fp32.
+ * none of them.  dg, du and weight h are rounded to bf16 between the products, a
+ * slot's row of dx to 11 bits as one of y; dy w_down, and with it dweights, is kept
+ * in fp32.
  * Other arguments and errors as zopt_moe_forward.
  */
 zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32_t experts, int32_t top,

@@ -78,9 +78,10 @@ struct MoePlan {
     bool back;
     Weight wg, wu, wd;
     Rows x, dy;
-    size_t token, share, h, dh, dg, du, rows, dot, sizes, part, total;
+    size_t token, share, h, dh, dg, du, rows, scale, dot, total;
+    int64_t scales;  // exponents of a slot's row
     int64_t parts;  // dots of a slot
-    size_t tiles[3];
+    size_t tiles[3], items[2], joins[2], part[2];
     TgLaunch glu, down, dhf, dx, dwgu, dwd;
 
     TgLaunch launch(int64_t M, int64_t N) const {
@@ -148,13 +149,15 @@ MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const ui
     p.token = c.take(S * 4);
     p.h = c.take(S * p.Fp * 2);
     p.rows = c.take(S * p.Dp * 2);
+    p.scales = (D + kRowsGroup - 1) / kRowsGroup;
+    p.scale = c.take(S * p.scales);
     p.glu = p.launch(S, F);
     p.glu.prob[0].seg[0].stages = (int32_t)((p.Dp + 63) / 64 * 2);
     plan_groups(back ? kTgMoeBack : kTgGlu, kGroupRows, false, p.glu);
     if (!back) {
         p.down = p.launch(S, D);
         p.down.prob[0].seg[0].stages = (int32_t)((p.Fp + 63) / 64 * 2);
-        plan_groups(kTgStore, kGroupRows, false, p.down);
+        plan_groups(kTgRows, kGroupRows, false, p.down);
     } else {
         p.dy = token_rows(dy, lddy, T, k, D, true, c);
         p.share = c.take(S * 4);
@@ -163,14 +166,13 @@ MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const ui
         p.du = c.take(S * p.Fp * 2);
         p.parts = (F + 31) / 32;
         p.dot = c.take(S * p.parts * 4);
-        p.sizes = c.take(E * 4);
         p.dhf = p.launch(S, F);
         p.dhf.prob[0].seg[0].stages = (int32_t)((p.Dp + 63) / 64 * 2);
         plan_groups(kTgFloat, kGroupRows, true, p.dhf);
         p.dx = p.launch(S, D);
         p.dx.prob[0].nseg = 2;
         p.dx.prob[0].seg[0].stages = p.dx.prob[0].seg[1].stages = (int32_t)((p.Fp + 63) / 64 * 2);
-        plan_groups(kTgStore, kGroupRows, true, p.dx);
+        plan_groups(kTgRows, kGroupRows, true, p.dx);
         p.dwgu = p.launch(F, D);
         p.dwgu.nprob = 2;
         p.dwgu.prob[0].seg[0].stages = p.average();
@@ -178,7 +180,16 @@ MoePlan moe_plan(int64_t T, int64_t D, int64_t F, int32_t E, int32_t k, const ui
         p.dwd = p.launch(D, F);
         p.dwd.prob[0].seg[0].stages = p.average();
         plan_groups(kTgStore, kGroupDepth, true, p.dwd);
-        p.part = c.take(larger(group_part_bytes(kGroupDepth, p.dwgu), group_part_bytes(kGroupDepth, p.dwd)));
+        int i = 0;
+        for (TgLaunch *L : {&p.dwgu, &p.dwd}) {
+            // (groups of more than part_rows rows, and the parts of all of them)
+            const int64_t splits = S / L->part_rows;
+            L->join_limit = (int32_t)(splits < E ? splits : E);
+            L->item_limit = (int32_t)(E + 2 * splits);
+            p.part[i] = c.take(group_part_bytes(*L));
+            p.items[i] = c.take((1 + L->item_limit) * (int64_t)sizeof(TgItem));
+            p.joins[i++] = c.take((L->join_limit + 1) * (int64_t)sizeof(TgItem));
+        }
     }
     const TgLaunch *rows[3] = {&p.glu, back ? &p.dhf : &p.down, back ? &p.dx : nullptr};
     for (int i = 0; i < 3; ++i)
@@ -213,6 +224,14 @@ struct Preps {
         j.tiles = reinterpret_cast<TgTileRow *>(ws + at);
         L.tile_row = j.tiles;
     }
+    void items(TgLaunch &L, size_t at, size_t joins, char *ws) {
+        MoePrep &j = add(kMoeItems);
+        j.height = L.part_rows;
+        j.tiles = reinterpret_cast<TgItem *>(ws + at);
+        j.joins = reinterpret_cast<TgItem *>(ws + joins);
+        L.items = j.tiles;
+        L.joins = j.joins;
+    }
     void place(Rows &r, int64_t cols, char *ws) {
         if (!r.copy) return;
         MoePrep &j = add(kMoeGather);
@@ -243,7 +262,8 @@ ZOPT_EXPORT zopt_status zopt_moe_route(int64_t T, int32_t experts, int32_t top, 
     if (!stride_ok(ld, experts) || !range(groups, 1, kMaxRanges < experts ? kMaxRanges : experts) || experts % groups ||
         !range(top_groups, 1, groups) || top > experts / groups * top_groups)
         return ZOPT_ERR_SIZE;
-    const int32_t each = route_block_tokens(T, experts, groups, top);
+    const bool scored = bias != nullptr || groups > 1;
+    const int32_t each = route_block_tokens(T, experts, groups, top, scored);
     const size_t need = plan_bytes(T, experts, each);
     if (workspace == nullptr) {
         *workspace_bytes = need;
@@ -261,7 +281,7 @@ ZOPT_EXPORT zopt_status zopt_moe_route(int64_t T, int32_t experts, int32_t top, 
     const PlanArgs p = plan_args(T, experts, top, each, chosen, workspace, offsets, order, place);
     if (T == 0) return device(launch_plan(p, s));
     const RouteArgs a{T, experts, top, bf16, score == ZOPT_SCORE_SIGMOID, groups, top_groups, renormalise, scale, logits,
-                      ld, bias, chosen, weights, p.block_tokens, 0};
+                      ld, bias, chosen, weights, p.block_tokens, 0, 0, scored};
     return device(launch_route(a, p, s));
 }
 
@@ -272,7 +292,7 @@ ZOPT_EXPORT zopt_status zopt_moe_plan(int64_t T, int32_t experts, int32_t top, c
     // (any number of experts a token, the same one more than once too)
     if (!range(T, 0, kMaxRows) || !range(experts, 1, kMaxExperts) || !range(top, 1, kMaxTop) || T * top > kMaxSlots)
         return ZOPT_ERR_SIZE;
-    const int32_t each = route_block_tokens(T, 0, 1, top);
+    const int32_t each = route_block_tokens(T, -experts, 1, top, false);
     const size_t need = plan_bytes(T, experts, each);
     if (workspace == nullptr) {
         *workspace_bytes = need;
@@ -368,9 +388,11 @@ ZOPT_EXPORT zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_
     ZOPT_TRY(launch_rows_glu(p.x.gathered, p.glu, s));
     p.down.prob[0].seg[0] = MoePlan::segment(p.slots_along(ws + p.h, p.Fp, F), MoePlan::along(p.wd, D, F));
     p.down.prob[0].out = reinterpret_cast<uint16_t *>(ws + p.rows);
+    p.down.row_scale = reinterpret_cast<uint8_t *>(ws + p.scale);
+    p.down.ldscale = p.scales;
     p.down.ldc = p.Dp;
     p.down.group_stride = p.wd.group;
-    ZOPT_TRY(launch_rows_store(false, p.down, s));
+    ZOPT_TRY(launch_rows(false, p.down, s));
     MoeCombine c{};
     c.tokens = T;
     c.cols = D;
@@ -379,6 +401,8 @@ ZOPT_EXPORT zopt_status zopt_moe_forward(int64_t T, int64_t D, int64_t F, int32_
     c.place = place;
     c.weights = weights;
     c.rows = reinterpret_cast<const uint16_t *>(ws + p.rows);
+    c.scale = reinterpret_cast<const uint8_t *>(ws + p.scale);
+    c.ldscale = p.scales;
     c.ld = p.Dp;
     c.out = y;
     c.ldo = ldy;
@@ -430,7 +454,8 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     preps.tiles(p.glu, p.tiles[0], p.capacity(p.glu), ws);
     preps.tiles(p.dhf, p.tiles[1], p.capacity(p.dhf), ws);
     preps.tiles(p.dx, p.tiles[2], p.capacity(p.dx), ws);
-    preps.add(kMoeSizes).sizes = reinterpret_cast<int32_t *>(ws + p.sizes);
+    preps.items(p.dwgu, p.items[0], p.joins[0], ws);
+    preps.items(p.dwd, p.items[1], p.joins[1], ws);
     preps.place(p.wg, ldw, w_expert, experts, F, D, ws);
     preps.place(p.wu, ldw, w_expert, experts, F, D, ws);
     preps.place(p.wd, ldd, wd_expert, experts, D, F, ws);
@@ -470,9 +495,11 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     p.dx.prob[0].seg[0] = MoePlan::segment(p.slots_along(ws + p.dg, p.Fp, F), MoePlan::across(p.wg, F, D));
     p.dx.prob[0].seg[1] = MoePlan::segment(p.slots_along(ws + p.du, p.Fp, F), MoePlan::across(p.wu, F, D));
     p.dx.prob[0].out = reinterpret_cast<uint16_t *>(ws + p.rows);
+    p.dx.row_scale = reinterpret_cast<uint8_t *>(ws + p.scale);
+    p.dx.ldscale = p.scales;
     p.dx.ldc = p.Dp;
     p.dx.group_stride = p.wg.group;
-    ZOPT_TRY(launch_rows_store(true, p.dx, s));
+    ZOPT_TRY(launch_rows(true, p.dx, s));
     MoeCombine c{};
     c.tokens = T;
     c.cols = D;
@@ -480,6 +507,8 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     c.slots = p.S;
     c.place = place;
     c.rows = reinterpret_cast<const uint16_t *>(ws + p.rows);
+    c.scale = reinterpret_cast<const uint8_t *>(ws + p.scale);
+    c.ldscale = p.scales;
     c.ld = p.Dp;
     c.out = dx;
     c.ldo = lddx;
@@ -487,14 +516,9 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     c.lddot = p.parts;
     c.parts = (int32_t)p.parts;
     c.dweights = dweights;
-    ZOPT_TRY(launch_moe_combine(c, s));
     // the weights' gradients
-    const int32_t *sizes = reinterpret_cast<const int32_t *>(ws + p.sizes);
-    for (TgLaunch *L : {&p.dwgu, &p.dwd}) {
-        L->first = offsets;
-        L->by_size = sizes;
-        L->part = reinterpret_cast<float *>(ws + p.part);
-    }
+    p.dwgu.part = reinterpret_cast<float *>(ws + p.part[0]);
+    p.dwd.part = reinterpret_cast<float *>(ws + p.part[1]);
     const TgOperand xa = p.slots_across(p.x.slots, p.Dp, D);
     p.dwgu.prob[0].seg[0].a = p.slots_across(ws + p.dg, p.Fp, F);
     p.dwgu.prob[0].seg[0].b = xa;
@@ -511,5 +535,12 @@ ZOPT_EXPORT zopt_status zopt_moe_backward(int64_t T, int64_t D, int64_t F, int32
     p.dwd.prob[0].out = dw_down;
     p.dwd.ldc = lddd;
     p.dwd.group_out = dwd_expert;
-    return device(launch_depth(p.dwd, s));
+    ZOPT_TRY(launch_depth(p.dwd, s));
+    int i = 0;
+    for (const TgLaunch *L : {&p.dwgu, &p.dwd}) {
+        MoeJoin &j = c.join[i++];
+        j.L = *L;
+        tile_shape(L->tile, j.height, j.width, j.rows, j.cols);
+    }
+    return device(launch_moe_combine(c, s));
 }

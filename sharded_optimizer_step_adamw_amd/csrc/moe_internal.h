@@ -22,6 +22,8 @@ struct RouteArgs {
     float *weights;       // [tokens, top]
     int32_t block_tokens;
     int32_t sort_here;    // (set by the launch) the one block, of all its threads, also sorts
+    int32_t row_floats;   // (set by the launch) LDS of a token's ranges
+    int32_t scored;       // ranks are scores and biases, not the logits
 };
 // Slots sorted by expert, stable: from the choice and the blocks' counts.
 struct PlanArgs {
@@ -42,8 +44,8 @@ struct RouteBackArgs {
     void *dlogits;        // the logits' type, row stride lddl
     int64_t lddl;
 };
-// Tokens of a block (experts 0: that only sorts).
-int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top);
+// Tokens of a block (experts negative: that only sorts).
+int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top, bool scored);
 hipError_t launch_route(RouteArgs a, const PlanArgs &plan, hipStream_t stream);
 hipError_t launch_plan_count(const PlanArgs &a, hipStream_t stream);
 hipError_t launch_plan(const PlanArgs &a, hipStream_t stream);
@@ -54,19 +56,21 @@ hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);
 // What precedes the products, all in one launch:
 //   kMoeTiles   the tile rows of height `height` (TgTileRow [1 + capacity]) from
 //               the offsets
-//   kMoeSizes   the experts, the one with the most rows first
+//   kMoeItems   the items of a sum over the experts' rows (TgItem [1 + capacity])
+//               and the joins of their parts, of `height` rows at most: the parts,
+//               and behind them the experts of one part, the largest first
 //   kMoeTokens  token [slots]: the slots' tokens (-1: none); share (or
 //               NULL): their weights
 //   kMoeGather  dst [slots, round8(cols)] = the slots' rows of src, zero beyond cols
 //   kMoeCopy    dst [rows, round8(cols)] = src's rows, of which each
 //               `group_rows` lie `group_stride` apart
-enum MoePrepKind : int { kMoeTiles = 0, kMoeSizes = 1, kMoeGather = 2, kMoeCopy = 3, kMoeTokens = 4 };
+enum MoePrepKind : int { kMoeTiles = 0, kMoeItems = 1, kMoeGather = 2, kMoeCopy = 3, kMoeTokens = 4 };
 struct MoePrep {
     int32_t kind;
     uint32_t blocks;              // set by the launch
     int32_t height, capacity;
-    TgTileRow *tiles;
-    int32_t *sizes, *token;
+    TgTileRow *tiles, *joins;
+    int32_t *token;
     int64_t rows, cols;
     const uint16_t *src;
     int64_t ld, group_rows, group_stride;
@@ -74,7 +78,7 @@ struct MoePrep {
     const float *weights;
     float *share;
 };
-constexpr int kMaxMoePreps = 11;
+constexpr int kMaxMoePreps = 12;
 struct MoePrepList {
     MoePrep job[kMaxMoePreps];
     int32_t n;
@@ -85,9 +89,16 @@ struct MoePrepList {
 hipError_t launch_moe_prep(MoePrepList &list, hipStream_t stream);
 
 // out [tokens, cols] = the sums over a token's slots of weights (NULL: 1) times
-// their rows [slots, cols] (row stride ld); and dweights [tokens, top] = the
-// sums of the slots' `parts` dots (NULL: not wanted).  A slot without a place
-// counts as zero.
+// their rows [slots, cols] (of kTgRows: row stride ld, exponents' ldscale).  A slot without a place counts as zero.
+// With dweights also what else ends a backward pass, in the same launch:
+// dweights [tokens, top] = the sums of the slots' `parts` dots, and the joins of
+// the weight gradients that were summed in parts.
+struct MoeJoin {
+    TgLaunch L;          // of which the part, items, joins, out, ldc, group_out, sizes
+    int32_t rows, cols;  // waves of a tile across its rows and columns
+    int32_t height, width;
+    uint32_t blocks;     // (set by the launch)
+};
 struct MoeCombine {
     int64_t tokens, cols;
     int32_t top;
@@ -95,24 +106,29 @@ struct MoeCombine {
     const int32_t *place;
     const float *weights;
     const uint16_t *rows;
-    int64_t ld;
+    const uint8_t *scale;
+    int64_t ld, ldscale;
     uint16_t *out;
     int64_t ldo;
     const float *dot;
     int64_t lddot;
     int32_t parts;
     float *dweights;
+    MoeJoin join[2];
+    uint32_t sum_blocks, dot_blocks;  // (set by the launch)
 };
-hipError_t launch_moe_combine(const MoeCombine &c, hipStream_t stream);
+hipError_t launch_moe_combine(MoeCombine &c, hipStream_t stream);
 hipError_t launch_fill_zero_groups(uint16_t *dst, int64_t ld, int64_t group_stride, int64_t groups, int64_t rows,
                                    int64_t cols, hipStream_t stream);
 
 // The products (train_internal.h's kinds, over groups).
 void plan_groups(TgEpilogue epi, TgGroups kind, bool b_km, TgLaunch &L);
 int tile_height(int tile);
-size_t group_part_bytes(TgGroups kind, const TgLaunch &L);
+// rows and columns of a tile and its waves across them
+void tile_shape(int tile, int32_t &height, int32_t &width, int32_t &rows, int32_t &cols);
+size_t group_part_bytes(const TgLaunch &L);  // kGroupDepth
 hipError_t launch_rows_glu(bool gather, TgLaunch &L, hipStream_t stream);      // kTgGlu
-hipError_t launch_rows_store(bool b_km, TgLaunch &L, hipStream_t stream);      // kTgStore
+hipError_t launch_rows(bool b_km, TgLaunch &L, hipStream_t stream);            // kTgRows
 hipError_t launch_rows_float(bool gather, TgLaunch &L, hipStream_t stream);    // kTgFloat, B k-major
 hipError_t launch_rows_back(bool gather, TgLaunch &L, hipStream_t stream);     // kTgMoeBack
 hipError_t launch_depth(TgLaunch &L, hipStream_t stream);                      // kTgStore, both k-major

@@ -1,6 +1,7 @@
 // moe_route.hip -- routing of tokens to experts: scores, choice, weights, the
 // slots' order by expert, and the logits' gradient.
 #include <cmath>
+#include <type_traits>
 
 #include "lanes.h"
 #include "moe_internal.h"
@@ -8,9 +9,12 @@
 namespace zopt {
 namespace {
 
-constexpr int kRouteThreads = 512, kPlanThreads = 256;
-// A grid of one block chooses and sorts in one launch.
-constexpr int64_t kOneBlockSlots = 2048;
+constexpr int kRouteThreads = 512, kPlanThreads = 256, kAloneThreads = 1024;
+// A grid of one block chooses and sorts in one launch; experts already chosen are
+// sorted by one block of 1024 threads up to so many slots (5331 of 13 experts: 11
+// us, in three launches of more blocks 14).
+constexpr int64_t kOneBlockSlots = 2048, kAloneSlots = 8192;
+constexpr int kAloneExperts = 512;
 
 // ------------------------------------------------------------------ scores
 
@@ -45,11 +49,16 @@ __device__ __forceinline__ void read_logits(const void *p, int64_t i, int left, 
     for (int k = 0; k < NV; ++k) z[k] = k < left ? read_logit(p, i + k, bf16) : -INFINITY;
 }
 
-// log of the logistic function, and the function
-__device__ __forceinline__ float log_logistic(float z) { return fminf(z, 0.0f) - log1pf(expf(-fabsf(z))); }
 __device__ __forceinline__ float logistic(float z) {
     const float e = expf(-fabsf(z));
     return (z >= 0.0f ? 1.0f : e) / (1.0f + e);
+}
+// What weights are in proportion to, of a logit z among the chosen ones, whose
+// largest is m: its exponential or logistic, both times a power of e that keeps the
+// largest near 1 however small they are (0 beside a NaN, whose own is one).
+__device__ __forceinline__ float proportion(float z, float m, bool sigmoid) {
+    if (!sigmoid) return expf(z - m);
+    return (z >= 0.0f ? 1.0f : expf(z - fminf(m, 0.0f))) / (1.0f + expf(-fabsf(z)));
 }
 
 // Ranks as whole numbers in the same order: 0 for -inf (an expert that is not
@@ -66,151 +75,198 @@ __device__ __forceinline__ uint64_t rank_of(double v) {
 }
 
 struct RouteLane {
-    int G, gl, first, row;  // lanes of a token, the lane's number there, its first lane, the token's number in the block
+    int gl, first, row;  // the lane's number of its token's G, the first of them, the token's number in the block
 };
 
-// Two-best sums of the ranges of experts, and -inf to the experts of all but
-// the best top_groups.  Returns how near the choice of ranges was: the sum of
-// the last one chosen less that of the first one left (inf: no choice).
-template <int NV, class R>
-__device__ __forceinline__ R choose_ranges(const RouteArgs &a, const RouteLane &l, R (&key)[NV], double *lds) {
-    const int size = a.experts / a.groups, lanes = size / NV;
-    const R kNone = -(R)INFINITY;
-    auto order = [](R v) __attribute__((always_inline)) { return v != v ? (R)-3.0e38f : v; };
-    R own = kNone;
-    int g = 0, groups = a.groups;
-    // (the token's own LDS in both types: its neighbours' may be in use in the other one)
-    R *sums = reinterpret_cast<R *>(lds + (int64_t)l.row * (a.experts + a.groups)) + a.experts;
-    if (lanes * NV == size && (lanes & (lanes - 1)) == 0 && a.experts == l.G * NV) {
-        // a range is a power of two of lanes
-        struct Two {
-            R b1, b2;
-        } two{kNone, kNone};
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const R k = order(key[i]);
-            two.b2 = k > two.b1 ? two.b1 : k > two.b2 ? k : two.b2;
-            two.b1 = k > two.b1 ? k : two.b1;
-        }
-        two = join(two, lanes, [](Two x, Two y) {
-            const R lo = x.b1 < y.b1 ? x.b1 : y.b1, hi = x.b2 > y.b2 ? x.b2 : y.b2;
-            return Two{x.b1 > y.b1 ? x.b1 : y.b1, lo > hi ? lo : hi};
-        });
-        own = two.b2 == kNone ? two.b1 : two.b1 + two.b2;
-        g = l.gl / lanes;
-        if (l.gl % lanes == 0) sums[g] = own;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    } else {
-        R *keys = sums - a.experts;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (l.gl * NV + i < a.experts) keys[l.gl * NV + i] = order(key[i]);
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        for (int x = l.gl; x < groups; x += l.G) {
-            R b1 = kNone, b2 = kNone;
-            for (int i = 0; i < size; ++i) {
-                const R k = keys[x * size + i];
-                b2 = k > b1 ? b1 : k > b2 ? k : b2;
-                b1 = k > b1 ? k : b1;
-            }
-            sums[x] = b2 == kNone ? b1 : b1 + b2;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        g = -1;
+// (what lanes of one wave have written to LDS, read by others of it)
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// Whether a range of experts is a power of two of whole lanes.
+__host__ __device__ __forceinline__ bool even_ranges(int experts, int groups, int G, int nv) {
+    const int size = experts / groups, lanes = size / nv;
+    return lanes * nv == size && (lanes & (lanes - 1)) == 0 && experts == G * nv;
+}
+
+struct BestTwo {
+    float b1, b2;
+    __device__ __forceinline__ void add(float k) {
+        b2 = k > b1 ? b1 : k > b2 ? k : b2;
+        b1 = k > b1 ? k : b1;
     }
-    R last = (R)INFINITY, left = kNone;
-    auto before = [&](R v, int x) __attribute__((always_inline)) {
+    __device__ __forceinline__ float sum() const { return b2 == -INFINITY ? b1 : b1 + b2; }
+};
+
+// The ranges' sums of their two best; -inf to the experts of all but the best
+// top_groups.  Returns how near that choice was: the last sum chosen less the
+// first one left (inf: none was left).  lds: of the token, its ranges' sums and,
+// where ranges are not even, the experts' keys.
+template <int NV, int G>
+__device__ __forceinline__ float choose_ranges(const RouteArgs &a, const RouteLane &l, float (&key)[NV], float *sums) {
+    const int size = a.experts / a.groups, lanes = size / NV, e0 = l.gl * NV;
+    auto order = [](float v) __attribute__((always_inline)) { return v != v ? -3.0e38f : v; };
+    float last = INFINITY, left = -INFINITY;
+    // whether range x, of sum v, stays
+    auto stays = [&](float v, int x) __attribute__((always_inline)) {
         int n = 0;
-        for (int h = 0; h < groups; ++h) {
-            const R s = sums[h];
+        for (int h = 0; h < a.groups; ++h) {
+            const float s = sums[h];
             n += s > v || (s == v && h < x) ? 1 : 0;
         }
-        return n;
-    };
-    auto stays = [&](R v, int x) __attribute__((always_inline)) {
-        const bool in = before(v, x) < a.top_groups;
-        if (in) last = v < last ? v : last;
-        else left = v > left ? v : left;
+        const bool in = n < a.top_groups;
+        last = in && v < last ? v : last;
+        left = !in && v > left ? v : left;
         return in;
     };
-    if (g >= 0) {
-        const bool in = stays(own, g);
+    if (even_ranges(a.experts, a.groups, G, NV)) {
+        BestTwo two{-INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < NV; ++i) key[i] = in ? key[i] : kNone;
+        for (int i = 0; i < NV; ++i) two.add(order(key[i]));
+        two = join(two, lanes, [](BestTwo x, BestTwo y) {
+            return BestTwo{fmaxf(x.b1, y.b1), fmaxf(fminf(x.b1, y.b1), fmaxf(x.b2, y.b2))};
+        });
+        const int g = l.gl / lanes;
+        if (l.gl % lanes == 0) sums[g] = two.sum();
+        wave_sync();
+        const bool in = stays(two.sum(), g);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) key[i] = in ? key[i] : -INFINITY;
     } else {
+        float *keys = sums + a.groups;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (e0 + i < a.experts) keys[e0 + i] = order(key[i]);
+        wave_sync();
+        for (int x = l.gl; x < a.groups; x += G) {
+            BestTwo two{-INFINITY, -INFINITY};
+            for (int i = 0; i < size; ++i) two.add(keys[x * size + i]);
+            sums[x] = two.sum();
+        }
+        wave_sync();
         int at = -1;
         bool in = false;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int e = l.gl * NV + i;
-            if (e >= a.experts) continue;
-            if (e / size != at) {
-                at = e / size;
+            if (e0 + i >= a.experts) continue;
+            if ((e0 + i) / size != at) {
+                at = (e0 + i) / size;
                 in = stays(sums[at], at);
             }
-            key[i] = in ? key[i] : kNone;
+            key[i] = in ? key[i] : -INFINITY;
         }
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    last = join(last, l.G, [](R x, R y) { return x < y ? x : y; });
-    left = group_max(left, l.G);
-    return left == kNone ? (R)INFINITY : last - left;
+    wave_sync();
+    last = join(last, G, [](float x, float y) { return fminf(x, y); });
+    left = group_fmax(left, G);
+    return left == -INFINITY ? INFINITY : last - left;
 }
 
-// What lane j of a token knows of its j-th best expert.
-struct Pick {
-    int expert;       // -1: none
-    float z, bias, key;
-};
-
-// The best `count` experts, one after the other: the best rank of all lanes,
-// the lowest lane that has it, its lowest expert of that rank.
-template <int NV, class K>
-__device__ __forceinline__ Pick choose(const RouteLane &l, K (&rank)[NV], const float (&z)[NV], const float (&bias)[NV],
-                                       const float (&key)[NV], int count) {
-    Pick p{-1, 0.0f, 0.0f, 0.0f};
-    const uint64_t lanes = l.G == 64 ? ~0ull : (1ull << l.G) - 1;
+// The best `count` experts, one after the other, the j-th returned in lane j (-1:
+// none is left): the best rank of all lanes, the lowest lane that has it, its
+// lowest expert of that rank.
+template <int NV, int G>
+__device__ __forceinline__ int choose(const RouteLane &l, uint32_t (&rank)[NV], int count) {
+    int chosen = -1;
+    constexpr uint64_t lanes = G == 64 ? ~0ull : (1ull << (G & 63)) - 1;
     for (int j = 0; j < count; ++j) {
-        K best = rank[0];
+        uint32_t best = rank[0];
         int at = 0;
 #pragma unroll
         for (int i = 1; i < NV; ++i) {
             at = rank[i] > best ? i : at;
             best = rank[i] > best ? rank[i] : best;
         }
-        const K top = group_max(best, l.G);
+        const uint32_t top = group_max(best, G);
         const uint64_t have = (__ballot(best == top) >> l.first) & lanes;
         const int lead = __builtin_ctzll(have);
-        float zi = z[0], bi = bias[0], ki = key[0];
+        const int e = __shfl(l.gl * NV + at, l.first + lead);
+        if (l.gl == j) chosen = top != 0 ? e : -1;
+        const int gone = l.gl == lead ? at : -1;
 #pragma unroll
-        for (int i = 1; i < NV; ++i) {
-            zi = at == i ? z[i] : zi;
-            bi = at == i ? bias[i] : bi;
-            ki = at == i ? key[i] : ki;
-        }
-        const int from = l.first + lead;
-        const int e = __shfl(l.gl * NV + at, from);
-        zi = __shfl(zi, from);
-        if (l.gl == j) {
-            p.expert = top != 0 ? e : -1;
-            p.z = zi;
-        }
-        if (sizeof(K) == 4) {
-            bi = __shfl(bi, from);
-            ki = __shfl(ki, from);
-            if (l.gl == j) {
-                p.bias = bi;
-                p.key = ki;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) rank[i] = l.gl == lead && at == i ? 0 : rank[i];
+        for (int i = 0; i < NV; ++i) rank[i] = gone == i ? 0 : rank[i];
     }
-    return p;
+    return chosen;
+}
+
+// The choice of one token in 64 bits, by a whole wave: the j-th best expert
+// returned in lane j.  lds: [experts + groups], the wave's.  It runs for few
+// tokens, mostly not yet in the instruction cache: loops are short.
+__device__ __forceinline__ int choose_exactly(const RouteArgs &a, int64_t t, double *lds) {
+    const int lane = threadIdx.x & 63, E = a.experts;
+    constexpr double kNone = -INFINITY;
+    uint64_t *keys = reinterpret_cast<uint64_t *>(lds);
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int e = lane; e < E; e += 64) {
+        const float z = read_logit(a.logits, t * a.ld + e, a.bf16);
+        lds[e] = (double)z;
+        top = fmaxf(top, z);
+    }
+    double total = 1.0, ref = 0.0;
+    if (!a.sigmoid) {
+        top = group_fmax(top, 64);
+        ref = top == -INFINITY ? 0.0 : (double)top;
+        total = 0.0;
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64) total += exp(lds[e] - ref);
+        total = group_sum(total, 64);
+    }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) {
+        const double z = lds[e], x = exp(a.sigmoid ? -z : z - ref);
+        double k = (a.sigmoid ? 1.0 : x) / (a.sigmoid ? 1.0 + x : total);
+        if (a.bias != nullptr) k += (double)a.bias[e];
+        lds[e] = z == kNone ? kNone : k != k ? -1.7e308 : k;
+    }
+    wave_sync();
+    if (a.groups > 1) {
+        const int size = E / a.groups;
+        double b1 = kNone, b2 = kNone;
+        if (lane < a.groups) {
+#pragma unroll 4
+            for (int i = 0; i < size; ++i) {
+                const double k = lds[lane * size + i];
+                b2 = k > b1 ? b1 : k > b2 ? k : b2;
+                b1 = k > b1 ? k : b1;
+            }
+            b1 = b2 == kNone ? b1 : b1 + b2;
+            lds[E + lane] = b1;
+        }
+        wave_sync();
+        int before = 0;
+#pragma unroll 4
+        for (int h = 0; h < a.groups; ++h) {
+            const double s = lds[E + h];
+            before += s > b1 || (s == b1 && h < lane) ? 1 : 0;
+        }
+        const uint64_t in = __ballot(lane < a.groups && before < a.top_groups);
+#pragma unroll 1
+        for (int e = lane; e < E; e += 64)
+            if (!((in >> (e / size)) & 1)) lds[e] = kNone;
+        wave_sync();
+    }
+#pragma unroll 1
+    for (int e = lane; e < E; e += 64) keys[e] = rank_of(lds[e]);
+    int chosen = -1;
+#pragma unroll 1
+    for (int j = 0; j < a.top; ++j) {
+        uint64_t best = 0;
+        int at = 0x7FFFFFFF;
+#pragma unroll 4
+        for (int e = lane; e < E; e += 64) {
+            const uint64_t k = keys[e];
+            at = k > best ? e : at;
+            best = k > best ? k : best;
+        }
+        const uint64_t most = group_max(best, 64);
+        at = join(best == most ? at : 0x7FFFFFFF, 64, [](int x, int y) { return x < y ? x : y; });
+        if (lane == j) chosen = most != 0 ? at : -1;
+        if (most != 0 && (at & 63) == lane) keys[at] = 0;
+    }
+    wave_sync();
+    return chosen;
 }
 
 // Sorts the slots of block `block` of `blocks`: base [experts], how many slots
@@ -297,126 +353,133 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 }
 
 // G lanes a token, NV neighbouring experts a lane.  Ranks by score and bias are
-// formed in fp32 first, off by less than 2^-19 (1 + |rank|): the sum of at most
-// 16 6-fold joined exponentials by 22 2^-24 of itself, each exponential,
-// quotient and the bias's addition by some 2^-24 more.  Where two of the best
-// lie closer than that could hide, and are not of the same logit and bias, the
-// wave's tokens are ranked again in 64 bits.
-template <int NV>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a, PlanArgs plan, int G) {
+// formed in fp32 first, off by less than 2^-22 (p + |rank|), p the score: an
+// exponential by a step or two of its own size, 1 + it and the quotient by half
+// a step each (the softmax's sum is kept in 64 bits), the bias's addition by half a
+// step of the rank.  Then the best and two more are looked at again, the logistic's
+// scores in 64 bits: each has to lie before the next, by more than both may be off
+// if they are not of the same logit and bias, and the last before whatever was left.
+// A token where that does not hold is ranked again in 64 bits throughout; with
+// the next one's 32-bit rank for all of them instead, sixteen times as many were.
+// Bound by instruction issue and latency (16384 tokens over 256 experts in 8
+// groups, 16.8 MB: 35 us; 45 with 4 experts a lane, and 54 held to 80 registers for
+// more waves).
+template <int NV, int G>
+__global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, PlanArgs plan) {
     extern __shared__ double lds[];
-    const int E = a.experts;
-    int *hist = reinterpret_cast<int *>(lds);
-    double *keys = lds + (E + 1) / 2;
+    const int E = a.experts, waves = blockDim.x / 64;
+    double *exact = lds + (threadIdx.x >> 6) * (E + a.groups);
+    float *rows = reinterpret_cast<float *>(lds + (a.scored ? waves * (E + a.groups) : 0));
+    int *hist = reinterpret_cast<int *>(rows + blockDim.x / G * a.row_floats);
     const int lane = threadIdx.x & 63, per = blockDim.x / G;
-    const RouteLane l{G, lane & (G - 1), lane & ~(G - 1), (int)threadIdx.x / G};
-    const bool scored = a.bias != nullptr || a.groups > 1;
+    const RouteLane l{lane & (G - 1), lane & ~(G - 1), (int)threadIdx.x / G};
     for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * a.block_tokens;
     const int64_t t1 = t0 + a.block_tokens < a.tokens ? t0 + a.block_tokens : a.tokens;
-    float bias[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int e = l.gl * NV + i;
-        bias[i] = a.bias != nullptr && e < E ? a.bias[e] : 0.0f;
-    }
     for (int64_t base = t0; base < t1; base += per) {
         const int64_t t = base + l.row;
         const bool live = t < t1;
-        float z[NV], key[NV];
+        float z[NV];
         read_logits<NV>(a.logits, t * a.ld + l.gl * NV, live ? E - l.gl * NV : 0, a.bf16, z);
-        float top = -INFINITY, sum = 0.0f;
-        if (!a.sigmoid && (scored || !a.renormalise)) {
+        uint32_t rank[NV];
+        float top = -INFINITY, ref = 0.0f, sum = 1.0f;
+        float key[NV];
+        if (!a.sigmoid && (a.scored || !a.renormalise)) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) top = fmaxf(top, z[i]);
             top = group_fmax(top, G);
-            const float ref = top == -INFINITY ? 0.0f : top;
+            ref = top == -INFINITY ? 0.0f : top;
+            double total = 0.0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                key[i] = __expf(z[i] - ref);
-                sum += key[i];
+                key[i] = expf(z[i] - ref);
+                total += (double)key[i];
             }
-            sum = group_sum(sum, G);
+            sum = (float)group_sum(total, G);
         }
-        uint32_t rank[NV];
         bool near = false;
-        Pick p;
-        if (scored) {
-            const float inv = 1.0f / sum;
+        int expert;
+        float zc = -INFINITY;  // the lane's expert's logit
+        if (a.scored) {
+            auto score = [&](float z, float e) __attribute__((always_inline)) {
+                return a.sigmoid ? 1.0f / (1.0f + expf(-z)) : e / sum;
+            };
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const float s = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-z[i])) : key[i] * inv;
-                key[i] = z[i] == -INFINITY ? -INFINITY : s + bias[i];
+                const int e = l.gl * NV + i;
+                key[i] = score(z[i], key[i]) + (a.bias != nullptr && e < E ? a.bias[e] : 0.0f);
+                key[i] = z[i] == -INFINITY ? -INFINITY : key[i];
             }
             if (a.groups > 1) {
-                const float gap = choose_ranges<NV, float>(a, l, key, keys);
-                near = !(gap > 0x1p-15f);  // (of sums of two, each rank below 2 in size)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) near |= fabsf(key[i]) > 2.0f && key[i] != -INFINITY;
+                const float gap = choose_ranges<NV, G>(a, l, key, rows + l.row * a.row_floats);
+                near |= !(gap > 0x1p-18f);  // (of sums of two, each p + |rank| at most 3)
             }
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                rank[i] = rank_of(key[i]);
-                near |= fabsf(key[i]) > 2.0f && key[i] != -INFINITY && a.groups > 1;
+            for (int i = 0; i < NV; ++i) rank[i] = rank_of(key[i]);
+            expert = choose<NV, G>(l, rank, a.top + 2);
+            float bc = 0.0f;
+            double exactly = -INFINITY, off = 0.0;  // the rank again, and how far it may be off
+            float about = -INFINITY, about_off = 0.0f;
+            if (expert >= 0) {
+                zc = read_logit(a.logits, t * a.ld + expert, a.bf16);
+                bc = a.bias != nullptr ? a.bias[expert] : 0.0f;
+                const float p = score(zc, a.sigmoid ? 0.0f : expf(zc - ref));
+                about = p + bc;
+                about_off = 0x1p-22f * (p + fabsf(about));
+                exactly = a.sigmoid ? 1.0 / (1.0 + exp(-(double)zc)) + (double)bc : (double)about;
+                off = a.sigmoid ? 0.0 : (double)about_off;
+                near |= about != about;
             }
-            p = choose<NV>(l, rank, z, bias, key, a.top + 1);
-            // against the one before
-            const float before = __shfl_up(p.key, 1), zb = __shfl_up(p.z, 1), bb = __shfl_up(p.bias, 1);
-            const int eb = __shfl_up(p.expert, 1);
-            if (l.gl > 0 && l.gl <= a.top && p.expert >= 0 && eb >= 0) {
-                const bool apart = before - p.key > 0x1p-18f * (1.0f + fmaxf(fabsf(before), fabsf(p.key)));
-                near |= !apart && !(zb == p.z && bb == p.bias);
+            const double before = __shfl_up(exactly, 1), before_off = __shfl_up(off, 1);
+            const bool same = __shfl_up(zc, 1) == zc && __shfl_up(bc, 1) == bc && __shfl_up(expert, 1) >= 0 && expert >= 0;
+            // before this one; before this one and all that were left
+            const bool first = expert < 0 || before - exactly > before_off + off || same;
+            const bool clear = expert < 0 || before - (double)about > before_off + (double)about_off;
+            // (lane top: the first one left; if it is the last one's equal, the next)
+            const uint64_t clears = __ballot(clear) >> l.first, sames = __ballot(same) >> l.first;
+            near |= l.gl > 0 && l.gl < a.top && !first;
+            near |= !((clears >> a.top & 1) || ((sames >> a.top & 1) && (clears >> (a.top + 1) & 1)));
+            uint64_t again = __ballot(near && live);
+            while (again != 0) {
+                // the lowest token of those, by all lanes
+                const int first = __builtin_ctzll(again) & ~(G - 1);
+                const int exactly = choose_exactly(a, base + (threadIdx.x - lane + first) / G, exact);
+                const int mine = __shfl(exactly, l.gl);
+                if (l.first == first) {
+                    expert = mine;
+                    zc = expert >= 0 ? read_logit(a.logits, t * a.ld + expert, a.bf16) : -INFINITY;
+                }
+                again &= ~((G == 64 ? ~0ull : (1ull << (G & 63)) - 1) << first);
             }
-            near |= p.key != p.key;
         } else {
 #pragma unroll
             for (int i = 0; i < NV; ++i) rank[i] = rank_of(z[i]);
-            p = choose<NV>(l, rank, z, bias, z, a.top);
+            expert = choose<NV, G>(l, rank, a.top);
+            if (expert >= 0) zc = read_logit(a.logits, t * a.ld + expert, a.bf16);
         }
-        if (__any(near)) {
-            const bool again = group_max(near ? 1 : 0, G) != 0;
-            double wide[NV], total = 0.0;
-            if (!a.sigmoid) {
-                const double ref = top == -INFINITY ? 0.0 : (double)top;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    wide[i] = z[i] == -INFINITY ? 0.0 : exp((double)z[i] - ref);
-                    total += wide[i];
-                }
-                total = group_sum(total, G);
-            }
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)z[i])) : wide[i] / total;
-                wide[i] = z[i] == -INFINITY ? -(double)INFINITY : s + (double)bias[i];
-            }
-            if (a.groups > 1) choose_ranges<NV, double>(a, l, wide, keys);
-            uint64_t wide_rank[NV];
-#pragma unroll
-            for (int i = 0; i < NV; ++i) wide_rank[i] = rank_of(wide[i]);
-            const Pick q = choose<NV>(l, wide_rank, z, bias, z, a.top);
-            if (again) p = q;
-        }
-        const bool picked = p.expert >= 0 && l.gl < a.top;
+        const bool picked = expert >= 0 && l.gl < a.top;
         float w = 0.0f;
         if (a.renormalise) {
-            const float x = !picked ? -INFINITY : a.sigmoid ? log_logistic(p.z) : p.z;
-            const float m = group_fmax(x, G), e = picked ? expf(x - m) : 0.0f;
+            const float m = group_fmax(picked ? zc : -INFINITY, G), e = picked ? proportion(zc, m, a.sigmoid) : 0.0f;
             const float s = group_sum(e, G);
             w = picked ? a.scale * (e / s) : 0.0f;
         } else if (picked) {
-            w = a.scale * (a.sigmoid ? logistic(p.z) : expf(p.z - top) / sum);
+            w = a.scale * (a.sigmoid ? logistic(zc) : expf(zc - top) / sum);
         }
         if (live && l.gl < a.top) {
-            a.chosen[t * a.top + l.gl] = p.expert;
+            a.chosen[t * a.top + l.gl] = picked ? expert : -1;
             a.weights[t * a.top + l.gl] = w;
-            if (picked && gridDim.x > 1) atomicAdd(&hist[p.expert], 1);
+            if (picked && gridDim.x > 1) atomicAdd(&hist[expert], 1);
         }
     }
     __syncthreads();
     if (a.sort_here) {
         __threadfence_block();
         __syncthreads();
-        sort_block<kRouteThreads>(plan, 0, 1, nullptr, nullptr, hist);
+        sort_block<kRouteThreads>(plan, 0, 1, nullptr, nullptr, reinterpret_cast<int *>(lds));
         return;
     }
     // (one block's slots are counted where they are sorted)
@@ -473,15 +536,16 @@ __global__ __launch_bounds__(1024) void plan_scan_kernel(PlanArgs a, int blocks)
     }
 }
 
-__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void plan_kernel(PlanArgs a) {
     extern __shared__ int next[];
     const bool alone = gridDim.x == 1;
-    sort_block<kPlanThreads>(a, blockIdx.x, gridDim.x, alone ? nullptr : a.counts + (int64_t)blockIdx.x * a.experts,
+    sort_block<THREADS>(a, blockIdx.x, gridDim.x, alone ? nullptr : a.counts + (int64_t)blockIdx.x * a.experts,
                              alone ? nullptr : a.total, next);
 }
 
-template <int NV>
-__global__ __launch_bounds__(256) void route_back_kernel(RouteBackArgs a, int G) {
+template <int NV, int G>
+__global__ __launch_bounds__(256) void route_back_kernel(RouteBackArgs a) {
     const int E = a.experts, lane = threadIdx.x & 63, gl = lane & (G - 1), first_lane = lane - gl, e0 = gl * NV;
     const int per = 256 / G, own = threadIdx.x / G;
     for (int64_t base = (int64_t)blockIdx.x * per; base < a.tokens; base += (int64_t)gridDim.x * per) {
@@ -502,8 +566,7 @@ __global__ __launch_bounds__(256) void route_back_kernel(RouteBackArgs a, int G)
         for (int i = 0; i < NV; ++i) v[i] = 0.0f;
         float d = 0.0f;
         if (a.renormalise) {
-            const float l = e < 0 ? -INFINITY : a.sigmoid ? log_logistic(z) : z;
-            const float m = group_fmax(l, G), x = e < 0 ? 0.0f : expf(l - m);
+            const float m = group_fmax(z, G), x = e < 0 ? 0.0f : proportion(z, m, a.sigmoid);
             const float s = group_sum(x, G), w = e < 0 ? 0.0f : x / s;
             const float dot = group_sum(w * g, G);
             d = w * (g - dot);
@@ -560,33 +623,55 @@ __global__ __launch_bounds__(256) void route_back_kernel(RouteBackArgs a, int G)
     }
 }
 
-// Lanes of a token: one for four experts, more than the experts chosen, at
-// most a wave; and experts of a lane.
+// Lanes of a token, two more than the experts chosen at least, and experts of a
+// lane: 8 from 128 experts on, else 4 (and 16 where a wave's lanes do not do).
+// Choosing 8 of 128 for 16384 tokens takes 10.4 us with 8, 14.3 with 4; 6 of 60 for
+// 4099 7.4 with 4.
 struct Lanes {
     int G, nv;
 };
 Lanes lanes_of(int experts, int top) {
-    int g = 1;
-    while (g < 64 && (g * 4 < experts || g <= top)) g <<= 1;
-    int nv = 1;
-    while (nv * g < experts) nv <<= 1;
-    return {g, nv};
+    const int each = experts < 128 ? 4 : 8;
+    int g = 2;
+    while (g < 64 && (g * each < experts || g <= top + 1)) g <<= 1;
+    return {g, experts <= 4 * g ? 4 : experts <= 8 * g ? 8 : 16};
+}
+// f<NV, G>()
+template <class F>
+void with_lanes(Lanes l, F f) {
+    using std::integral_constant;
+    if (l.nv == 16) f(integral_constant<int, 16>{}, integral_constant<int, 64>{});
+    else if (l.nv == 8 && l.G == 64) f(integral_constant<int, 8>{}, integral_constant<int, 64>{});
+    else if (l.nv == 8 && l.G == 32) f(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+    else if (l.nv == 8) f(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+    else if (l.G == 64) f(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else if (l.G == 32) f(integral_constant<int, 4>{}, integral_constant<int, 32>{});
+    else if (l.G == 16) f(integral_constant<int, 4>{}, integral_constant<int, 16>{});
+    else if (l.G == 8) f(integral_constant<int, 4>{}, integral_constant<int, 8>{});
+    else if (l.G == 4) f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+    else f(integral_constant<int, 4>{}, integral_constant<int, 2>{});
 }
 int64_t blocks_of(int64_t tokens, int32_t each) { return (tokens + each - 1) / each; }
 
-// LDS of the choice with `threads` a block
-size_t route_lds(int32_t experts, int32_t groups, int32_t top, int threads) {
-    const int64_t rows = groups > 1 ? threads / lanes_of(experts, top).G : 0;
-    return (size_t)((experts + 1) / 2 + rows * (experts + groups)) * 8;
+// LDS of the choice with `threads` a block: the waves' for the choice in 64 bits,
+// the tokens' for their ranges, the experts' counts
+int32_t route_row(int32_t experts, int32_t groups, int32_t top) {
+    const Lanes l = lanes_of(experts, top);
+    return groups == 1 ? 0 : even_ranges(experts, groups, l.G, l.nv) ? groups : groups + experts;
+}
+size_t route_lds(int32_t experts, int32_t groups, int32_t top, bool scored, int threads) {
+    return (size_t)(scored ? threads / 64 * (experts + groups) * 8 : 0) +
+           (size_t)(threads / lanes_of(experts, top).G * route_row(experts, groups, top) + experts) * 4;
 }
 constexpr size_t kRouteLds = 48 << 10;
 
 }  // namespace
 
-int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top) {
+int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top, bool scored) {
     const int64_t at_once = experts > 0 ? kRouteThreads / lanes_of(experts, top).G : 0;
+    if (experts < 0 && tokens * top <= kAloneSlots && -experts <= kAloneExperts) return (int32_t)(tokens > 0 ? tokens : 1);
     if (tokens * top <= kOneBlockSlots &&
-        (experts == 0 || (tokens <= 4 * at_once && route_lds(experts, groups, top, kRouteThreads) <= kRouteLds)))
+        (experts < 0 || (tokens <= 4 * at_once && route_lds(experts, groups, top, scored, kRouteThreads) <= kRouteLds)))
         return (int32_t)(tokens > 0 ? tokens : 1);
     // at most 1024 blocks, of 256 slots or of what a block chooses at once or more
     const int64_t each = (tokens + 1023) / 1024, least = experts > 0 ? at_once : (256 + top - 1) / top;
@@ -596,17 +681,17 @@ int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int3
 hipError_t launch_route(RouteArgs a, const PlanArgs &plan, hipStream_t stream) {
     const Lanes l = lanes_of(a.experts, a.top);
     const uint32_t blocks = (uint32_t)blocks_of(a.tokens, a.block_tokens);
-    const int threads = route_lds(a.experts, a.groups, a.top, kRouteThreads) <= kRouteLds ? kRouteThreads : 256;
-    const size_t choice = route_lds(a.experts, a.groups, a.top, threads);
+    const int threads =
+        route_lds(a.experts, a.groups, a.top, a.scored, kRouteThreads) <= kRouteLds ? kRouteThreads : 256;
+    const size_t choice = route_lds(a.experts, a.groups, a.top, a.scored, threads);
     a.sort_here = blocks == 1 && threads == kRouteThreads;
+    a.row_floats = route_row(a.experts, a.groups, a.top);
     const size_t sort = a.sort_here ? (size_t)(kRouteThreads / 64 + 1) * a.experts * 4 : 0;
     const size_t bytes = choice > sort ? choice : sort;
-    const dim3 grid(blocks), block(threads);
-    if (l.nv == 1) hipLaunchKernelGGL(route_kernel<1>, grid, block, bytes, stream, a, plan, l.G);
-    else if (l.nv == 2) hipLaunchKernelGGL(route_kernel<2>, grid, block, bytes, stream, a, plan, l.G);
-    else if (l.nv == 4) hipLaunchKernelGGL(route_kernel<4>, grid, block, bytes, stream, a, plan, l.G);
-    else if (l.nv == 8) hipLaunchKernelGGL(route_kernel<8>, grid, block, bytes, stream, a, plan, l.G);
-    else hipLaunchKernelGGL(route_kernel<16>, grid, block, bytes, stream, a, plan, l.G);
+    with_lanes(l, [&](auto NV, auto G) {
+        hipLaunchKernelGGL((route_kernel<decltype(NV)::value, decltype(G)::value>), dim3(blocks), dim3(threads), bytes,
+                           stream, a, plan);
+    });
     hipError_t e = hipGetLastError();
     return e == hipSuccess && !a.sort_here ? launch_plan(plan, stream) : e;
 }
@@ -626,8 +711,12 @@ hipError_t launch_plan(const PlanArgs &a, hipStream_t stream) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(plan_kernel, dim3((uint32_t)(blocks > 0 ? blocks : 1)), dim3(kPlanThreads),
-                       (kPlanThreads / 64 + 1) * a.experts * 4, stream, a);
+    if (blocks == 1 && a.tokens * a.top > kPlanThreads && a.experts <= kAloneExperts)
+        hipLaunchKernelGGL(plan_kernel<kAloneThreads>, dim3(1), dim3(kAloneThreads), (kAloneThreads / 64 + 1) * a.experts * 4,
+                           stream, a);
+    else
+        hipLaunchKernelGGL(plan_kernel<kPlanThreads>, dim3((uint32_t)(blocks > 0 ? blocks : 1)), dim3(kPlanThreads),
+                           (kPlanThreads / 64 + 1) * a.experts * 4, stream, a);
     return hipGetLastError();
 }
 
@@ -635,12 +724,10 @@ hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream) {
     const Lanes l = lanes_of(a.experts, a.top);
     const int per = 256 / l.G;
     const int64_t blocks = (a.tokens + per - 1) / per;
-    const dim3 grid((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)), block(256);
-    if (l.nv == 1) hipLaunchKernelGGL(route_back_kernel<1>, grid, block, 0, stream, a, l.G);
-    else if (l.nv == 2) hipLaunchKernelGGL(route_back_kernel<2>, grid, block, 0, stream, a, l.G);
-    else if (l.nv == 4) hipLaunchKernelGGL(route_back_kernel<4>, grid, block, 0, stream, a, l.G);
-    else if (l.nv == 8) hipLaunchKernelGGL(route_back_kernel<8>, grid, block, 0, stream, a, l.G);
-    else hipLaunchKernelGGL(route_back_kernel<16>, grid, block, 0, stream, a, l.G);
+    with_lanes(l, [&](auto NV, auto G) {
+        hipLaunchKernelGGL((route_back_kernel<decltype(NV)::value, decltype(G)::value>),
+                           dim3((uint32_t)(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, stream, a);
+    });
     return hipGetLastError();
 }
 

@@ -1,7 +1,9 @@
 // moe_rows.hip -- the passes over rows around the experts' products: tokens
 // gathered by expert, the tile rows of experts whose sizes only the device
 // knows, and the sums over a token's experts.  All are bound by HBM.
+#include "lanes.h"
 #include "moe_internal.h"
+#include "tile_walk.h"
 
 namespace zopt {
 namespace {
@@ -13,13 +15,6 @@ uint32_t blocks_for(int64_t n) {
     return (uint32_t)(b < 1 ? 1 : b > (1 << 20) ? (1 << 20) : b);
 }
 
-__device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(p[k] << 16);
-        v[2 * k + 1] = __uint_as_float(p[k] & 0xFFFF0000u);
-    }
-}
 __device__ __forceinline__ tg_u32x4 pack8(const float (&v)[8]) {
     return tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
                     tg_pack_bf16(v[6], v[7])};
@@ -77,19 +72,62 @@ __device__ __forceinline__ void prep_tiles(const MoePrepList &l, const MoePrep &
     }
 }
 
-__device__ __forceinline__ void prep_sizes(const MoePrepList &l, const MoePrep &j) {
+// How many parts expert e has (1: it is whole), and how many rows each
+__device__ __forceinline__ int parts_of(int n, int most, int &rows) {
+    const int parts = n <= most ? 1 : (n + most - 1) / most;
+    rows = parts == 1 ? n : ((n + parts - 1) / parts + 63) / 64 * 64;
+    return parts == 1 ? 1 : (n + rows - 1) / rows;
+}
+__device__ __forceinline__ void prep_items(const MoePrepList &l, const MoePrep &j) {
     __shared__ int size[kMaxExperts];
-    int lo, n;
-    for (int e = threadIdx.x; e < l.experts; e += kThreads) {
+    __shared__ int part[2][kThreads];
+    constexpr int kEach = kMaxExperts / kThreads;
+    int lo, n, rows, sum = 0, split = 0;
+    for (int i = 0; i < kEach; ++i) {
+        const int e = threadIdx.x * kEach + i;
+        if (e >= l.experts) break;
         bounds(l, e, lo, n);
-        size[e] = n;
+        const int parts = parts_of(n, j.height, rows);
+        size[e] = parts > 1 ? -1 : n;
+        sum += parts > 1 ? parts : 0;
+        split += parts > 1 ? 1 : 0;
     }
+    part[0][threadIdx.x] = sum;
+    part[1][threadIdx.x] = split;
     __syncthreads();
+    for (int o = 1; o < kThreads; o <<= 1) {
+        const int v = (int)threadIdx.x >= o ? part[0][threadIdx.x - o] : 0;
+        const int w = (int)threadIdx.x >= o ? part[1][threadIdx.x - o] : 0;
+        __syncthreads();
+        part[0][threadIdx.x] += v;
+        part[1][threadIdx.x] += w;
+        __syncthreads();
+    }
+    const int parts = part[0][kThreads - 1], joins = part[1][kThreads - 1];
+    // (more than a routing's offsets give: offsets that are none, and no items)
+    const bool wrong = parts > 2 * (l.slots / j.height) || joins > l.slots / j.height;
+    if (threadIdx.x == 0) j.tiles[0] = wrong ? TgItem{0, 0, 0, 0} : TgItem{parts + l.experts - joins, parts, joins, 0};
+    if (wrong) return;
+    int at = part[0][threadIdx.x] - sum, join = part[1][threadIdx.x] - split;
+    for (int i = 0; i < kEach; ++i) {
+        const int e = threadIdx.x * kEach + i;
+        if (e >= l.experts) break;
+        bounds(l, e, lo, n);
+        const int own = parts_of(n, j.height, rows);
+        if (own == 1) continue;
+        j.joins[join++] = TgItem{e, at, at + own, 0};
+        for (int p = 0; p < own; ++p) {
+            const int end = (p + 1) * rows < n ? (p + 1) * rows : n;
+            j.tiles[1 + at++] = TgItem{e, lo + p * rows, lo + end, 0};
+        }
+    }
+    // the others by size: tiles that run together then take about the same time
     for (int e = threadIdx.x; e < l.experts; e += kThreads) {
-        const int own = size[e];
+        if (size[e] < 0) continue;
         int rank = 0;
-        for (int i = 0; i < l.experts; ++i) rank += size[i] > own || (size[i] == own && i < e) ? 1 : 0;
-        j.sizes[rank] = e;
+        for (int i = 0; i < l.experts; ++i) rank += size[i] > size[e] || (size[i] == size[e] && i < e) ? 1 : 0;
+        bounds(l, e, lo, n);
+        j.tiles[1 + parts + rank] = TgItem{e, lo, lo + n, 0};
     }
 }
 
@@ -146,8 +184,8 @@ __global__ __launch_bounds__(kThreads) void moe_prep_kernel(MoePrepList list) {
     const MoePrep &j = list.job[k];
     if (j.kind == kMoeTiles)
         prep_tiles(list, j);
-    else if (j.kind == kMoeSizes)
-        prep_sizes(list, j);
+    else if (j.kind == kMoeItems)
+        prep_items(list, j);
     else if (j.kind == kMoeGather)
         prep_gather(list, j, block);
     else if (j.kind == kMoeTokens)
@@ -157,37 +195,95 @@ __global__ __launch_bounds__(kThreads) void moe_prep_kernel(MoePrepList list) {
 }
 
 // Eight columns a thread; the sum over a token's slots in fp32, in their order.
-__global__ __launch_bounds__(kThreads) void moe_combine_kernel(MoeCombine c) {
+__device__ __forceinline__ void combine_rows(const MoeCombine &c, int64_t block) {
     const int64_t per = (c.cols + 7) / 8, total = c.tokens * per;
-    for (int64_t id = blockIdx.x * (int64_t)kThreads + threadIdx.x; id < total; id += (int64_t)gridDim.x * kThreads) {
+    for (int64_t id = block * kThreads + threadIdx.x; id < total; id += (int64_t)c.sum_blocks * kThreads) {
         const int64_t t = id / per, col = (id - t * per) * 8, left = c.cols - col;
         float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
         for (int k = 0; k < c.top; ++k) {
             const int s = c.place[t * c.top + k];
             if (s < 0 || s >= c.slots) continue;
             const float w = c.weights != nullptr ? c.weights[t * c.top + k] : 1.0f;
-            float v[8];
-            unpack8(*reinterpret_cast<const tg_u32x4 *>(c.rows + s * c.ld + col), v);
+            const tg_u32x4 r = *reinterpret_cast<const tg_u32x4 *>(c.rows + s * c.ld + col);
+            const uint32_t e = c.scale[s * c.ldscale + col / kRowsGroup];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum[i] += w * v[i];
+            for (int i = 0; i < 4; ++i) {
+                const tg_f16x2 h = __builtin_bit_cast(tg_f16x2, (uint32_t)r[i]);
+                sum[2 * i] += w * tg_rows_out((float)h.x, e);
+                sum[2 * i + 1] += w * tg_rows_out((float)h.y, e);
+            }
         }
         tg_store8h(c.out + t * c.ldo + col, pack8(sum), left > 8 ? 8 : (int)left);
     }
 }
 
 // The gradients of the tokens' weights: one wave a slot.
-__global__ __launch_bounds__(kThreads) void moe_dweights_kernel(MoeCombine c) {
+__device__ __forceinline__ void combine_dots(const MoeCombine &c, int64_t block) {
     const int lane = threadIdx.x & 63;
-    for (int64_t i = (blockIdx.x * (int64_t)kThreads + threadIdx.x) >> 6; i < c.tokens * c.top;
-         i += (int64_t)gridDim.x * (kThreads / 64)) {
+    for (int64_t i = (block * kThreads + threadIdx.x) >> 6; i < c.tokens * c.top;
+         i += (int64_t)c.dot_blocks * (kThreads / 64)) {
         const int s = c.place[i];
         float sum = 0.0f;
         if (s >= 0 && s < c.slots)
             for (int p = lane; p < c.parts; p += 64) sum += c.dot[s * c.lddot + p];
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+        sum = group_sum(sum, 64);
         if (lane == 0) c.dweights[i] = sum;
     }
+}
+
+// A weight gradient's tiles that were summed in parts: a wave 16 rows of what one
+// wave of the tile held, the parts added in order.
+__device__ __forceinline__ void join_parts(const MoeJoin &j, int64_t block) {
+    const TgLaunch &L = j.L;
+    const int lane = threadIdx.x & 63, c = lane & 15, q = lane >> 4, waves = j.rows * j.cols;
+    const int blocks16 = j.height / j.rows / 16, per = L.tiles_m * L.tiles_n * L.nprob;
+    const int64_t total = (int64_t)L.items[0].end * per * waves * blocks16;
+    for (int64_t id = (block * kThreads + threadIdx.x) >> 6; id < total; id += (int64_t)j.blocks * (kThreads / 64)) {
+        const int64_t tile = id / (waves * blocks16);
+        const int wave = (int)(id / blocks16 % waves), i = (int)(id % blocks16), rest = (int)(tile % per);
+        const TgItem join = L.joins[tile / per];
+        const tg_f32x4 *p = reinterpret_cast<const tg_f32x4 *>(L.part) +
+                            ((((int64_t)join.row * per + rest) * waves + wave) * blocks16 + i) * (4 * 64) + lane;
+        tg_f32x4 acc[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[k] = p[k * 64];
+#pragma unroll 2
+        for (int s = join.row + 1; s < join.end; ++s) {
+            p += (int64_t)per * waves * blocks16 * (4 * 64);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) acc[k] += p[k * 64];
+        }
+        int prob, ti, tj;
+        item_tile(L, rest, prob, ti, tj);
+        const int row = ti * j.height + (wave / j.cols) * (blocks16 * 16) + i * 16 + c;
+        const int col = tj * j.width + (wave % j.cols) * 64 + q * 4;
+        if (row >= L.M) continue;
+        uint16_t *o = L.prob[prob].out + join.group * L.group_out + row * L.ldc + col;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int left = L.N - col - k * 16;
+            const tg_u32x2 v{tg_pack_bf16(acc[k][0], acc[k][1]), tg_pack_bf16(acc[k][2], acc[k][3])};
+            if (left >= 4) {
+                tg_store(o + k * 16, v);
+            } else {
+                if (left > 0) o[k * 16] = (uint16_t)v.x;
+                if (left > 1) o[k * 16 + 1] = (uint16_t)(v.x >> 16);
+                if (left > 2) o[k * 16 + 2] = (uint16_t)v.y;
+            }
+        }
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void moe_combine_kernel(MoeCombine c) {
+    // (what has long chains of loads first)
+    uint32_t block = blockIdx.x;
+    if (block < c.join[0].blocks) return join_parts(c.join[0], block);
+    block -= c.join[0].blocks;
+    if (block < c.join[1].blocks) return join_parts(c.join[1], block);
+    block -= c.join[1].blocks;
+    if (block < c.dot_blocks) return combine_dots(c, block);
+    combine_rows(c, block - c.dot_blocks);
 }
 
 __global__ __launch_bounds__(kThreads) void fill_zero_groups_kernel(uint16_t *dst, int64_t ld, int64_t group_stride,
@@ -206,7 +302,7 @@ hipError_t launch_moe_prep(MoePrepList &list, hipStream_t stream) {
     for (int k = 0; k < list.n; ++k) {
         MoePrep &j = list.job[k];
         const int64_t per = (j.cols + 7) / 8;
-        j.blocks = j.kind == kMoeTiles || j.kind == kMoeSizes ? 1
+        j.blocks = j.kind == kMoeTiles || j.kind == kMoeItems ? 1
                    : j.kind == kMoeTokens                     ? blocks_for(list.slots)
                    : j.kind == kMoeGather ? blocks_for(list.slots * ((per + kGatherPieces - 1) / kGatherPieces) * 64)
                                           : blocks_for(j.rows * per);
@@ -217,14 +313,21 @@ hipError_t launch_moe_prep(MoePrepList &list, hipStream_t stream) {
     return hipGetLastError();
 }
 
-hipError_t launch_moe_combine(const MoeCombine &c, hipStream_t stream) {
-    hipLaunchKernelGGL(moe_combine_kernel, dim3(blocks_for(c.tokens * ((c.cols + 7) / 8))), dim3(kThreads), 0, stream, c);
-    hipError_t e = hipGetLastError();
-    if (e == hipSuccess && c.dweights != nullptr) {
-        hipLaunchKernelGGL(moe_dweights_kernel, dim3(blocks_for(c.tokens * c.top * 64)), dim3(kThreads), 0, stream, c);
-        e = hipGetLastError();
+hipError_t launch_moe_combine(MoeCombine &c, hipStream_t stream) {
+    c.sum_blocks = blocks_for(c.tokens * ((c.cols + 7) / 8));
+    c.dot_blocks = c.dweights != nullptr ? blocks_for(c.tokens * c.top * 64) : 0;
+    for (MoeJoin &j : c.join) {
+        // (how many groups have parts only the device knows: few blocks, which mostly
+        // end at once)
+        const int64_t waves = c.dweights != nullptr ? (int64_t)j.L.join_limit * j.L.tiles_m * j.L.tiles_n * j.L.nprob *
+                                                          j.cols * (j.height / 16)
+                                                    : 0;
+        const int64_t blocks = (waves + 3) / 4;
+        j.blocks = (uint32_t)(blocks < 1024 ? blocks : 1024);
     }
-    return e;
+    hipLaunchKernelGGL(moe_combine_kernel, dim3(c.sum_blocks + c.dot_blocks + c.join[0].blocks + c.join[1].blocks),
+                       dim3(kThreads), 0, stream, c);
+    return hipGetLastError();
 }
 
 hipError_t launch_fill_zero_groups(uint16_t *dst, int64_t ld, int64_t group_stride, int64_t groups, int64_t rows,

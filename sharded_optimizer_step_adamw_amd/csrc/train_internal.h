@@ -36,11 +36,14 @@ struct TgSegment {
 //   kTgFloat    sum -> fp32
 //   kTgMoeBack  kTgGluBack for rows with a weight each, from fp32 dh, with the
 //               weights' gradients
-enum TgEpilogue : int { kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3, kTgSum = 4, kTgFloat = 5, kTgMoeBack = 6 };
+//   kTgRows     sum -> fp16 with a power of two per row and 64 columns
+enum TgEpilogue : int {
+    kTgStore = 0, kTgXent = 1, kTgGlu = 2, kTgGluBack = 3, kTgSum = 4, kTgFloat = 5, kTgMoeBack = 6, kTgRows = 7
+};
 
 // Products of several groups (experts) in one launch, whose sizes only the
-// device knows.  `first` [groups + 1]: the groups' rows lie at first[g] ..
-// first[g + 1] of the operands that the groups share.
+// device knows: a group's rows are some neighbouring ones of the operands that
+// the groups share.
 //   kGroupRows   those are rows of A and of the output; each group has a B
 //                (B's p, and groups' distance group_stride)
 //   kGroupDepth  those are the reduction of A and B; each group has an output
@@ -53,6 +56,12 @@ constexpr int64_t kGatherBytes = 0xFFFF0000ll;
 struct TgTileRow {
     int32_t group, row, end, unused;
 };
+// What a tile of kGroupDepth sums over: rows row .. end - 1 of a group, all of
+// them or, of a group with more than part_rows, a part.  The list's first entry
+// holds the number of items (in `group`), of those that are parts, which come
+// first (in `row`), and of the groups that have parts (in `end`); `joins` lists
+// those: the group, its first item, the item behind its last.
+typedef TgTileRow TgItem;
 
 enum TgAct : int { kActSilu = 0, kActGelu = 1 };
 
@@ -116,11 +125,15 @@ struct TgLaunch {
     const float *share;       // [M]
     float *dot;
     int64_t lddot;
-    // groups (tiles_m, whole, tiles, total and padded of kGroupRows: the kernel's own)
-    const int32_t *first;
-    const int32_t *by_size;   // kGroupDepth: the groups, the largest first
+    // kTgRows: values to prob.out, exponents to row_scale [M, ldscale] (see tg_rows_*)
+    uint8_t *row_scale;
+    int64_t ldscale;
+    // groups (whole, tiles, total and padded are the kernel's own)
     const TgTileRow *tile_row;
-    int32_t groups, slots;    // (no row of a group is past slots)
+    const TgItem *items, *joins;
+    int32_t item_limit, join_limit;  // no more than that many; join_limit 0: no parts
+    int32_t part_rows;        // a multiple of 64
+    int32_t groups, slots;    // (rows of all groups)
     // gathered A (kGroupRows): row r is row token[r] of the operand, which has `tokens`
     // (negative: a row of zeros)
     const int32_t *token;
@@ -286,6 +299,26 @@ __device__ __forceinline__ float tg_scale_in(uint32_t byte) {
 __device__ __forceinline__ float tg_scale_out(uint32_t byte) {
     return byte == 255u ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
+// Rows of sums that a later pass adds up, in 16 bits: fp16 times 2^(exponent -
+// 141), one exponent for 64 neighbouring columns, that of the largest finite value
+// there (at least 14), which so lies in [2^14, 2^15) of fp16.  The rounding is off
+// by 2^-11 of a value, where bf16's 2^-8 would be as much as that of the result
+// itself, or by 2^-39 of the largest.  (fp32 rows would double the bytes of two
+// passes that HBM bounds.)
+constexpr int kRowsGroup = 64;
+__device__ __forceinline__ uint32_t tg_finite_bits(float v) {
+    const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+    return b < 0x7F800000u ? b : 0u;
+}
+__device__ __forceinline__ uint32_t tg_rows_exponent(uint32_t largest_bits) {
+    const uint32_t e = largest_bits >> 23;
+    return e < 14 ? 14u : e;
+}
+__device__ __forceinline__ float tg_rows_in(uint32_t exponent) { return __uint_as_float((268u - exponent) << 23); }
+__device__ __forceinline__ float tg_rows_out(float v, uint32_t exponent) {
+    return __builtin_amdgcn_ldexpf(v, (int)exponent - 141);
+}
+
 // Eight fp32 -> eight e4m3 of v * 2^(127 - byte), round to nearest even, low
 // first.  At the topmost scale, 2^120, 240 is the largest code: the next one,
 // 256, stands for 2^128, which no bf16 holds (and 240 is within 2^-4 of every

@@ -20,6 +20,7 @@
 
 #include <utility>
 
+#include "tile_walk.h"
 #include "train_internal.h"
 
 namespace zopt {
@@ -46,33 +47,6 @@ __device__ __forceinline__ int lane_id() {
     int l;
     asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
     return l;
-}
-
-// Tile t of a tiles_m x tiles_n grid: bands of 16 tile rows, in a band groups
-// of 8 columns, in a group runs of 4 rows, column by column.  A round of 256
-// tiles is then about 16 x 16 and an XCD's 32 about 4 x 8: few operand panels
-// in each L2, and few of them read more than once from HBM.
-__device__ __forceinline__ void tile_at(int t, int tm, int tn, int &ti, int &tj) {
-    const int band = t / (16 * tn), r0 = band * 16;
-    t -= band * 16 * tn;
-    const int h = tm - r0 < 16 ? tm - r0 : 16;
-    const int group = t / (8 * h), c0 = group * 8;
-    t -= group * 8 * h;
-    const int w = tn - c0 < 8 ? tn - c0 : 8;
-    const int run = t / (4 * w), q0 = run * 4;
-    t -= run * 4 * w;
-    const int hh = h - q0 < 4 ? h - q0 : 4;
-    tj = c0 + t / hh;
-    ti = r0 + q0 + t % hh;
-}
-
-// Tile t of kGroupDepth: the groups from the largest on, a group's two problems
-// side by side.
-__device__ __forceinline__ void group_tile(const TgLaunch &L, int t, int &prob, int &group, int &ti, int &tj) {
-    const int per = L.tiles_m * L.tiles_n, which = t / per;
-    prob = which % L.nprob;
-    group = __builtin_amdgcn_readfirstlane(L.by_size[which / L.nprob]);
-    tile_at(t - which * per, L.tiles_m, L.tiles_n, ti, tj);
 }
 
 // v of the lanes (c, q), (c, q ^ 1) and (c, q), (c, q ^ 2): the two values, in
@@ -358,6 +332,53 @@ __device__ __forceinline__ void float_epilogue(const TgLaunch &L, const TgProble
     }
 }
 
+// Rows in 16 bits, padded to a multiple of 8 columns.  A wave's 64 columns have one
+// exponent.  PERM: as below.
+template <int FM, bool PERM>
+__device__ __forceinline__ void rows_epilogue(const TgLaunch &L, const TgProblem &P, tg_f32x4 (&acc)[FM][4], int R0,
+                                              int C0, int rows) {
+    const int lane = lane_id(), c = lane & 15, q = lane >> 4;
+    if (C0 >= L.N) return;
+    const int first = C0 + (PERM ? q * 8 : q * 4), cols = L.N - first;
+    auto at = [](int j) __attribute__((always_inline)) { return PERM ? (j >> 1) * 32 + (j & 1) * 4 : j * 16; };
+    uint16_t *o = P.out + (int64_t)(R0 + c) * L.ldc + first;
+    uint8_t *scale = L.row_scale + (int64_t)(R0 + c) * L.ldscale + C0 / kRowsGroup;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        // (columns past N are sums of zeros)
+        uint32_t big = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t b = tg_finite_bits(acc[i][j][k]);
+                big = b > big ? b : big;
+            }
+        const uint32_t e = tg_rows_exponent(quad_umax(big));
+        const float s = tg_rows_in(e);
+        if (R0 + c + i * 16 < rows) {
+            if (q == 0) *scale = (uint8_t)e;
+#pragma unroll
+            for (int j = 0; j < 4; j += PERM ? 2 : 1) {
+                auto half = [&](int k) __attribute__((always_inline)) {
+                    const tg_f32x4 x = acc[i][k] * s;
+                    return tg_u32x2{tg_pack_f16(x[0], x[1]), tg_pack_f16(x[2], x[3])};
+                };
+                if (at(j) >= cols) continue;
+                if constexpr (PERM) {
+                    const tg_u32x2 a = half(j), b = half(j + 1);
+                    *reinterpret_cast<tg_u32x4 *>(o + at(j)) = tg_u32x4{a.x, a.y, b.x, b.y};
+                } else {
+                    *reinterpret_cast<tg_u32x2 *>(o + at(j)) = half(j);
+                }
+            }
+        }
+        scale += 16 * L.ldscale;
+        o += 16 * L.ldc;
+        __builtin_amdgcn_sched_barrier(0);
+    }
+}
+
 // A tile of sums: alpha * acc to bf16; SUM: plus earlier fp32 sums, or kept as
 // such for a later call.
 // PERM: the column order of a row-major B (eight consecutive per lane).
@@ -436,6 +457,8 @@ __device__ __forceinline__ void finish(const TgLaunch &L, int prob, int group, i
         glu_epilogue<FM, EPI == kTgGluBack, GRP>(L, acc, R0, C0, end);
     else if constexpr (EPI == kTgMoeBack)
         moe_back_epilogue<FM>(L, acc, R0, C0, end);
+    else if constexpr (EPI == kTgRows)
+        rows_epilogue<FM, !BKM>(L, L.prob[prob], acc, R0, C0, end);
     else if constexpr (EPI == kTgFloat)
         float_epilogue<FM>(L, L.prob[prob], acc, R0, C0, end);
     else
@@ -472,12 +495,11 @@ constexpr TileFigures kTileFigures[4] = {{kTile256, 256, 256, 1, 0.66, 0.86, 0.8
 // expcnt[6:4], lgkmcnt[11:8], vmcnt high bits[15:14])
 #define WAIT_VM_LGKM0(n) ((((n) & 15) | (((n) >> 4) << 14) | (7 << 4)))
 
-// A wave's sums of part `split` of split tile t, in register order (16 bytes a
-// lane).
+// A wave's sums of a tile's part, number `at` of all, in register order (16 bytes
+// a lane).
 template <int FM, int NW>
-__device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, int wave, tg_f32x4 (&acc)[FM][4]) {
-    tg_f32x4 *p = reinterpret_cast<tg_f32x4 *>(L.part) +
-                  (((int64_t)t * L.splits + split) * NW + wave) * (FM * 4 * 64) + lane_id();
+__device__ __forceinline__ void keep_part(const TgLaunch &L, int64_t at, int wave, tg_f32x4 (&acc)[FM][4]) {
+    tg_f32x4 *p = reinterpret_cast<tg_f32x4 *>(L.part) + (at * NW + wave) * (FM * 4 * 64) + lane_id();
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
 #pragma unroll
@@ -534,9 +556,8 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int t, int split, i
 // [8192, 4096] x [4096, 131072]; used where tiles are few).
 // Groups.  kGroupRows: the tile rows come from a list in memory, of which the
 // device alone knows the length; a tile ends at its group's last row.
-// kGroupDepth: every group has all tiles, the largest group's first, so that the
-// tiles of a round take about the same time; a group without rows has tiles of
-// zeros.
+// kGroupDepth: a list of items, each of which has all tiles; a group without rows
+// has tiles of zeros.
 // (A wave whose rows lie behind the tile's end multiplies zeros.  Leaving its
 // products out changed nothing, a stage of one wave a SIMD being bound by its
 // synchronisation, nor did taking such tiles last.)
@@ -572,7 +593,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wr = wave / WC, wc = wave % WC;
-    constexpr bool PLAIN = EPI == kTgStore || EPI == kTgSum || EPI == kTgFloat;
+    constexpr bool PLAIN = EPI == kTgStore || EPI == kTgSum || EPI == kTgFloat || EPI == kTgRows;
     const int grid = gridDim.x - (PLAIN && GRP == kNoGroups && L.sum_up.loss != nullptr ? 1 : 0);
     if constexpr (PLAIN && GRP == kNoGroups) {
         if ((int)blockIdx.x == grid) {
@@ -592,8 +613,12 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         int group, first, end;  // the group; kGroupRows: the end of its rows; kGroupDepth: its rows
     };
     const int tiles_m = GRP == kGroupRows ? __builtin_amdgcn_readfirstlane(L.tile_row[0].group) : L.tiles_m;
-    const int total = GRP == kGroupRows ? tiles_m * L.tiles_n : L.total;
-    const int padded = GRP == kGroupRows ? (total + 7) / 8 * 8 : L.padded;
+    const int per_item = L.tiles_m * L.tiles_n * L.nprob;
+    const int parts = GRP == kGroupDepth ? __builtin_amdgcn_readfirstlane(L.items[0].row) : 0;
+    const int total = GRP == kGroupRows    ? tiles_m * L.tiles_n
+                      : GRP == kGroupDepth ? __builtin_amdgcn_readfirstlane(L.items[0].group) * per_item
+                                           : L.total;
+    const int padded = GRP != kNoGroups ? (total + 7) / 8 * 8 : L.padded;
     // slot -> tile (false: a padding slot).  Workgroups go to the 8 XCDs in
     // turn; XCD x takes the x-th contiguous eighth of each round of resident
     // tiles, and consecutive tiles form blocks of the grid, so that each L2
@@ -605,21 +630,22 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         if (t >= total) return false;
         // (parts of the tiles that are split: all first ones, all second ones, ...)
         T.split = -1;
-        if (GRP != kGroupRows && t >= L.whole && L.splits > 1) {
+        if (GRP == kNoGroups && t >= L.whole && L.splits > 1) {
             const int rest = L.tiles - L.whole;
             T.split = (t - L.whole) / rest;
             t -= T.split * rest;
         }
         T.t = t;
-        int ti, tj, all, part = L.split_stages;
+        int ti, tj, all;
         if constexpr (GRP == kGroupDepth) {
-            group_tile(L, t, T.prob, T.group, ti, tj);
-            auto within = [&](int v) __attribute__((always_inline)) { return v < 0 ? 0 : v > L.slots ? L.slots : v; };
-            T.first = within(__builtin_amdgcn_readfirstlane(L.first[T.group]));
-            T.end = within(__builtin_amdgcn_readfirstlane(L.first[T.group + 1]));
-            if (T.end < T.first) T.end = T.first;
+            const int which = t / per_item;
+            const TgItem it = L.items[1 + which];
+            T.group = __builtin_amdgcn_readfirstlane(it.group);
+            T.first = __builtin_amdgcn_readfirstlane(it.row);
+            T.end = __builtin_amdgcn_readfirstlane(it.end);
+            item_tile(L, t - which * per_item, T.prob, ti, tj);
+            if (which < parts) T.split = 0;
             all = (T.end - T.first + 63) / 64 * 2;
-            part = (all / 2 + L.splits - 1) / L.splits * 2;
         } else {
             const int per = tiles_m * L.tiles_n;
             T.prob = GRP == kNoGroups && t >= per ? 1 : 0;
@@ -635,10 +661,9 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
             T.m0 = __builtin_amdgcn_readfirstlane(r.row);
             T.end = __builtin_amdgcn_readfirstlane(r.end);
         }
-        T.stage0 = T.split < 0 ? 0 : T.split * part;
+        T.stage0 = T.split < 0 ? 0 : T.split * L.split_stages;
         T.live = all - T.stage0;
-        if (T.split >= 0 && T.live > part) T.live = part;
-        if (GRP == kGroupDepth && T.live <= 0) T.live = T.stage0 = 0;  // (a part past the group's end: zeros)
+        if (GRP == kNoGroups && T.split >= 0 && T.live > L.split_stages) T.live = L.split_stages;
         T.stages = T.live < 4 ? 4 : T.live;  // (the switch to the next tile is kStages before)
         return true;
     };
@@ -988,7 +1013,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
             body(std::integral_constant<int, 1>{});
         }
         if (cu.split >= 0) {
-            keep_part<FM, NW>(L, cu.t - L.whole, cu.split, wave, acc);
+            keep_part<FM, NW>(L, GRP == kGroupDepth ? cu.t : (int64_t)(cu.t - L.whole) * L.splits + cu.split, wave, acc);
         } else {
             int target[FM];
             read_targets(target);
@@ -1007,7 +1032,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
 // the whole tiles' workgroups do.  A wave takes 16 rows of what one wave of
 // the tile held (four a workgroup, each on its own), so that few tiles still
 // fill the GPU.
-template <int TILE, int EPI, bool BKM, int GRP = kNoGroups>
+template <int TILE, int EPI, bool BKM>
 __global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
     using C = Cfg<TILE>;
     constexpr int NW = C::WR * C::WC, WTM = C::BM / C::WR, FM = WTM / 16;
@@ -1027,15 +1052,9 @@ __global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[0][j] += p[j * 64];
     }
-    const int t = L.whole + rt;
-    int ti, tj, prob, group = 0;
-    if constexpr (GRP == kGroupDepth) {
-        group_tile(L, t, prob, group, ti, tj);
-    } else {
-        const int per = L.tiles_m * L.tiles_n;
-        prob = t >= per ? 1 : 0;
-        tile_at(t - prob * per, L.tiles_m, L.tiles_n, ti, tj);
-    }
+    const int t = L.whole + rt, per = L.tiles_m * L.tiles_n, prob = t >= per ? 1 : 0;
+    int ti, tj;
+    tile_at(t - prob * per, L.tiles_m, L.tiles_n, ti, tj);
     const int R0 = ti * C::BM + (wave / C::WC) * WTM + i * 16;
     int target[1] = {-1};
     if constexpr (EPI == kTgXent) {
@@ -1043,7 +1062,7 @@ __global__ __launch_bounds__(256) void tg_join_kernel(TgLaunch L) {
         const int64_t v = row < L.M ? L.target[row] : -1;
         if (v >= 0 && v <= 0x7FFFFFFF) target[0] = (int)v;
     }
-    finish<EPI, BKM, GRP, 1>(L, prob, group, L.M, read_alpha(L), acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
+    finish<EPI, BKM, kNoGroups, 1>(L, prob, 0, L.M, read_alpha(L), acc, R0, tj * (GLU ? C::BN / 2 : C::BN) + (wave % C::WC) * (GLU ? 32 : 64), target);
 }
 
 // Compute units of the current device (asked for once), a multiple of the 8
@@ -1067,8 +1086,9 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
     // (kGroupRows: as many tile rows as there can be)
     L.tiles_m = GRP == kGroupRows ? L.M / C::BM + (L.groups < L.M ? L.groups : L.M) : (L.M + C::BM - 1) / C::BM;
     L.tiles_n = (L.N + BO - 1) / BO;
-    const int64_t tiles = (int64_t)L.tiles_m * L.tiles_n * L.nprob * (GRP == kGroupDepth ? L.groups : 1);
-    if constexpr (GRP == kGroupRows) L.whole = (int32_t)(tiles > 0x7FFFFF00 ? 0x7FFFFF00 : tiles);
+    const int64_t per = (int64_t)L.tiles_m * L.tiles_n * L.nprob, tiles = per * (GRP == kGroupDepth ? L.item_limit : 1);
+    if (GRP != kNoGroups && tiles > 0x7FFFFF00) return hipErrorInvalidValue;
+    if constexpr (GRP != kNoGroups) L.whole = (int32_t)tiles;
     const int64_t total = L.whole + (tiles - L.whole) * L.splits;
     if (tiles > 0x7FFFFF00 || total > 0x7FFFFF00) return hipErrorInvalidValue;
     L.tiles = (int32_t)tiles;
@@ -1079,9 +1099,10 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
     hipLaunchKernelGGL((tg_kernel<TILE, EPI, AKM, BKM, GRP, LIST>), dim3(grid + ((EPI == kTgStore || EPI == kTgSum) && L.sum_up.loss != nullptr ? 1 : 0)),
                        dim3(threads), 0, stream, L);
     hipError_t e = hipGetLastError();
-    if (GRP != kGroupRows && e == hipSuccess && L.splits > 1) {
+    if constexpr (GRP != kNoGroups) return e;
+    if (e == hipSuccess && L.splits > 1) {
         const int64_t waves = (tiles - L.whole) * (C::BM / 16) * C::WC;
-        hipLaunchKernelGGL((tg_join_kernel<TILE, EPI, BKM, GRP == kGroupRows ? kNoGroups : GRP>), dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, stream, L);
+        hipLaunchKernelGGL((tg_join_kernel<TILE, EPI, BKM>), dim3((uint32_t)((waves + 3) / 4)), dim3(256), 0, stream, L);
         e = hipGetLastError();
     }
     return e;

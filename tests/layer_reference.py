@@ -8,7 +8,7 @@ import math
 
 import torch
 
-from train_reference import HALF_BF16, HALF_F32, act
+from train_reference import HALF_BF16, HALF_F16, HALF_F32, act
 
 FAST = 2.0 ** -19  # the hardware's exponential and reciprocal in an activation, relatively
 
@@ -137,6 +137,12 @@ def plan(chosen, experts):
 
 # -------------------------------------------------------------------- experts
 
+def rows16(size):
+    """The rounding of a slot's row: half a step of fp16, or of fp16's smallest
+    at the scale of the row's largest (2^-25 in 2^14)."""
+    return HALF_F16 * size + 2.0 ** -38 * size.amax(1, keepdim=True)
+
+
 def moe(x, wg, wu, wd, chosen, share, kind, dy=None):
     """y and, with dy, (dx, dw_gate, dw_up, dw_down, dshare) of float64 inputs,
     each as (value, bound)."""
@@ -162,7 +168,7 @@ def moe(x, wg, wu, wd, chosen, share, kind, dy=None):
         hr = HALF_BF16 * (h.abs() + he) + he
         rows = h @ W.t()
         re = hr @ W.abs().t() + f * s * ((h.abs() + hr) @ W.abs().t())
-        re = re + HALF_BF16 * (rows.abs() + re)
+        re = re + rows16(rows.abs() + re)
         y.index_add_(0, row, p * rows)
         ye.index_add_(0, row, p.abs() * (re + 40 * HALF_F32 * (rows.abs() + re)))
         if dy is None:
@@ -182,7 +188,7 @@ def moe(x, wg, wu, wd, chosen, share, kind, dy=None):
             ue * da.abs() + (u.abs() + ue) * 1.2 * ge + FAST * u.abs() * (da.abs() + 1)))
         back = dg @ G + du @ U
         be = dge @ G.abs() + due @ U.abs() + 2 * f * s * ((dg.abs() + dge) @ G.abs() + (du.abs() + due) @ U.abs())
-        be = be + HALF_BF16 * (back.abs() + be)
+        be = be + rows16(back.abs() + be)
         dx.index_add_(0, row, back)
         dxe.index_add_(0, row, be + 40 * HALF_F32 * (back.abs() + be))
         for v, ve, out, oute in ((dg, dge, dwg, dwge), (du, due, dwu, dwue)):
