@@ -1,6 +1,7 @@
 """Builds the GPU test helpers in tests/helpers/ (hipcc, gfx950) into
-tests/helpers/_build/: the programs, and libforced_plan.so, the gradient
-operators with tile and split chosen by the test (plans/forced_plan.hip).
+tests/helpers/_build/: the programs, and libforced_plan.so and
+libforced_moe_plan.so, the gradient operators and the experts' with tile and
+split chosen by the test (plans/).
 Called by __graft_entry__.build(); runs without a GPU."""
 from __future__ import annotations
 
@@ -30,13 +31,16 @@ def build() -> list:
         subprocess.run([hipcc, *FLAGS, src, "-o", exe + ".tmp"], check=True)
         os.replace(exe + ".tmp", exe)
         built.append(exe)
-    lib = os.path.join(OUT, "libforced_plan.so")
-    csrc = zbuild.CSRC
-    subprocess.run([hipcc, *zbuild.HIPCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", csrc,
-                    os.path.join(HERE, "plans", "forced_plan.hip"), os.path.join(csrc, "train_api.hip"),
-                    os.path.join(csrc, "train_rows.hip"), "-o", lib + ".tmp"], check=True)
-    os.replace(lib + ".tmp", lib)
-    return built + [lib]
+    csrc, plans = zbuild.CSRC, os.path.join(HERE, "plans")
+    # each with the library's sources that its operators need
+    libs = {"forced_plan": ("train_api", "train_rows"),
+            "forced_moe_plan": ("moe_api", "moe_back_gemm", "moe_depth_gemm", "moe_route", "moe_rows")}
+    for name, rest in libs.items():
+        lib = os.path.join(OUT, f"lib{name}.so")
+        zbuild.compile_and_link([os.path.join(plans, name + ".hip"),
+                                 *(os.path.join(csrc, r + ".hip") for r in rest)], lib)
+        built.append(lib)
+    return built
 
 
 if __name__ == "__main__":
