@@ -217,8 +217,9 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, int64_t t, dou
     for (int e = lane; e < E; e += 64) {
         const double z = lds[e], x = exp(a.sigmoid ? -z : z - ref);
         double k = (a.sigmoid ? 1.0 : x) / (a.sigmoid ? 1.0 + x : total);
-        if (a.bias != nullptr) k += (double)a.bias[e];
-        lds[e] = z == kNone ? kNone : k != k ? -1.7e308 : k;
+        const double b = a.bias != nullptr ? (double)a.bias[e] : 0.0;
+        k += b;
+        lds[e] = fmin(z, b) == kNone ? kNone : k != k ? -1.7e308 : k;
     }
     wave_sync();
     if (a.groups > 1) {
@@ -408,8 +409,8 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int e = l.gl * NV + i;
-                key[i] = score(z[i], key[i]) + (a.bias != nullptr && e < E ? a.bias[e] : 0.0f);
-                key[i] = z[i] == -INFINITY ? -INFINITY : key[i];
+                const float b = a.bias != nullptr && e < E ? a.bias[e] : 0.0f;
+                key[i] = fminf(z[i], b) == -INFINITY ? -INFINITY : score(z[i], key[i]) + b;
             }
             if (a.groups > 1) {
 #pragma unroll

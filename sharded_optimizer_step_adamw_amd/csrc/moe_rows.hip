@@ -31,6 +31,13 @@ __device__ __forceinline__ void bounds(const MoePrepList &l, int e, int &lo, int
     n = hi > lo ? hi - lo : 0;
 }
 
+// Counts that stop at 2^30: offsets that are no routing's may count every slot for
+// every expert.
+__device__ __forceinline__ int more(int a, int b) {
+    const uint32_t s = (uint32_t)a + (uint32_t)b;  // (both at most 2^30)
+    return (int)(s < (1u << 30) ? s : 1u << 30);
+}
+
 __device__ __forceinline__ void prep_tiles(const MoePrepList &l, const MoePrep &j) {
     __shared__ int at[kMaxExperts];
     __shared__ int part[kThreads];
@@ -48,7 +55,7 @@ __device__ __forceinline__ void prep_tiles(const MoePrepList &l, const MoePrep &
     for (int o = 1; o < kThreads; o <<= 1) {
         const int v = (int)threadIdx.x >= o ? part[threadIdx.x - o] : 0;
         __syncthreads();
-        part[threadIdx.x] += v;
+        part[threadIdx.x] = more(part[threadIdx.x], v);
         __syncthreads();
     }
     int first = part[threadIdx.x] - sum;
@@ -67,8 +74,9 @@ __device__ __forceinline__ void prep_tiles(const MoePrepList &l, const MoePrep &
     const int lane = threadIdx.x & 63;
     for (int e = threadIdx.x >> 6; e < l.experts; e += kThreads / 64) {
         bounds(l, e, lo, n);
-        for (int r = lane; r * j.height < n; r += 64)
-            if (at[e] + r < j.capacity) j.tiles[1 + at[e] + r] = TgTileRow{e, lo + r * j.height, lo + n, 0};
+        const int all = (n + j.height - 1) / j.height, left = j.capacity - at[e];
+        for (int r = lane; r < all && r < left; r += 64)
+            j.tiles[1 + at[e] + r] = TgTileRow{e, lo + r * j.height, lo + n, 0};
     }
 }
 
@@ -99,7 +107,7 @@ __device__ __forceinline__ void prep_items(const MoePrepList &l, const MoePrep &
         const int v = (int)threadIdx.x >= o ? part[0][threadIdx.x - o] : 0;
         const int w = (int)threadIdx.x >= o ? part[1][threadIdx.x - o] : 0;
         __syncthreads();
-        part[0][threadIdx.x] += v;
+        part[0][threadIdx.x] = more(part[0][threadIdx.x], v);
         part[1][threadIdx.x] += w;
         __syncthreads();
     }
