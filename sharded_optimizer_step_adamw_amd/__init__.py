@@ -916,10 +916,13 @@ def _need_heads(t, shape, name, index):
     there) on GPU `index` whose heads are contiguous; returns its strides."""
     if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == index >= 0:
         have = t.shape
-        if len(have) == 3 and (have == shape or all(w is None or h == w for h, w in zip(have, shape))):
-            strides = t.stride()
-            if strides[2] == 1 or have[2] == 1:
-                return strides
+        if len(have) == 3:
+            tokens, heads, width = shape
+            if ((tokens is None or have[0] == tokens) and (heads is None or have[1] == heads)
+                    and (width is None or have[2] == width)):
+                strides = t.stride()
+                if strides[2] == 1 or have[2] == 1:
+                    return strides
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     if t.dtype != torch.bfloat16:
@@ -950,8 +953,9 @@ def _need_shape(t, dtype, shape, name, index):
 
 def _new(on, like, shape, dtype=None):
     """An output of the call's own stream."""
-    dtype = like.dtype if dtype is None else dtype
-    return on.empty(shape, dtype) if on.other else like.new_empty(shape, dtype=dtype)
+    if on.other:
+        return on.empty(shape, like.dtype if dtype is None else dtype)
+    return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
 
 
 def _on_device(device):
@@ -1029,7 +1033,7 @@ def _rope_out(t, like, name, on):
     """An output that is given, or a new one, with its address and strides."""
     shape = like.shape
     if t is None:
-        t = _new(on, like, shape)
+        t = torch.empty_like(like) if not on.other and like.is_contiguous() else _new(on, like, shape)
         return t, (t.data_ptr(), shape[1] * shape[2], shape[2])
     s = _need_heads(t, shape, name, on.device.index)
     return t, (t.data_ptr(), s[0], s[1])
@@ -1082,10 +1086,13 @@ def qk_norm_rope_backward(dyq, dyk, q, k, table, position=None, w_q=None, w_k=No
         elif dw is None:
             dw = _new(on, w, w.shape)
         grads += [dx, dw, _need_shape(dw, torch.bfloat16, (sizes[3],), f"dw_{name}", index)]
+    args = (*sizes, *ins, *heads, *rest, *outs, grads[2], grads[5])
     with _on_device(on.device):
-        _sized(lib().zopt_qk_norm_rope_backward,
-               (*sizes, *ins, *heads, *rest, *outs, grads[2], grads[5]),
-               "zopt_qk_norm_rope_backward", on, workspace)
+        if grads[2] is None and grads[5] is None and workspace is None:  # nothing to add up, no workspace
+            _check(lib().zopt_qk_norm_rope_backward(*args, 256, ctypes.byref(ctypes.c_size_t(0)), on.handle),
+                   "zopt_qk_norm_rope_backward")
+        else:
+            _sized(lib().zopt_qk_norm_rope_backward, args, "zopt_qk_norm_rope_backward", on, workspace)
     return grads[0], grads[3], grads[1], grads[4]
 
 
