@@ -332,6 +332,24 @@ __device__ __forceinline__ void float_epilogue(const TgLaunch &L, const TgProble
     }
 }
 
+// a and b, four 16-bit columns each of two blocks of 16 (lane group q: columns 4 q
+// on), to eight neighbours of both: group q then holds columns 8 q on, and a
+// store of 16 bytes a lane writes 64 in a row instead of 32.  (The two gradients
+// of 64 experts' 1024 x 2048 matrices, reductions of 512: 370 and 191 us, 402 and
+// 216 with 8 bytes a lane; of 16 experts' 2048 x 4096, of 2048: 987 and 511, 1020
+// and 547; their dx 970, 998.)
+__device__ __forceinline__ tg_u32x4 join_blocks(tg_u32x2 a, tg_u32x2 b) {
+    tg_u32x4 v;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const auto h = __builtin_amdgcn_permlane32_swap(a[k], b[k], false, false);
+        const auto r = __builtin_amdgcn_permlane16_swap(h[0], h[1], false, false);
+        v[k] = r[0];
+        v[2 + k] = r[1];
+    }
+    return v;
+}
+
 // Rows in 16 bits, padded to a multiple of 8 columns.  A wave's 64 columns have one
 // exponent.  PERM: as below.
 template <int FM, bool PERM>
@@ -339,8 +357,7 @@ __device__ __forceinline__ void rows_epilogue(const TgLaunch &L, const TgProblem
                                               int C0, int rows) {
     const int lane = lane_id(), c = lane & 15, q = lane >> 4;
     if (C0 >= L.N) return;
-    const int first = C0 + (PERM ? q * 8 : q * 4), cols = L.N - first;
-    auto at = [](int j) __attribute__((always_inline)) { return PERM ? (j >> 1) * 32 + (j & 1) * 4 : j * 16; };
+    const int first = C0 + q * 8, cols = L.N - first;
     uint16_t *o = P.out + (int64_t)(R0 + c) * L.ldc + first;
     uint8_t *scale = L.row_scale + (int64_t)(R0 + c) * L.ldscale + C0 / kRowsGroup;
 #pragma unroll
@@ -356,22 +373,17 @@ __device__ __forceinline__ void rows_epilogue(const TgLaunch &L, const TgProblem
             }
         const uint32_t e = tg_rows_exponent(quad_umax(big));
         const float s = tg_rows_in(e);
-        if (R0 + c + i * 16 < rows) {
-            if (q == 0) *scale = (uint8_t)e;
+        const bool live = R0 + c + i * 16 < rows;
+        if (live && q == 0) *scale = (uint8_t)e;
 #pragma unroll
-            for (int j = 0; j < 4; j += PERM ? 2 : 1) {
-                auto half = [&](int k) __attribute__((always_inline)) {
-                    const tg_f32x4 x = acc[i][k] * s;
-                    return tg_u32x2{tg_pack_f16(x[0], x[1]), tg_pack_f16(x[2], x[3])};
-                };
-                if (at(j) >= cols) continue;
-                if constexpr (PERM) {
-                    const tg_u32x2 a = half(j), b = half(j + 1);
-                    *reinterpret_cast<tg_u32x4 *>(o + at(j)) = tg_u32x4{a.x, a.y, b.x, b.y};
-                } else {
-                    *reinterpret_cast<tg_u32x2 *>(o + at(j)) = half(j);
-                }
-            }
+        for (int j = 0; j < 4; j += 2) {
+            auto half = [&](int k) __attribute__((always_inline)) {
+                const tg_f32x4 x = acc[i][k] * s;
+                return tg_u32x2{tg_pack_f16(x[0], x[1]), tg_pack_f16(x[2], x[3])};
+            };
+            const tg_u32x2 a = half(j), b = half(j + 1);
+            const tg_u32x4 v = PERM ? tg_u32x4{a.x, a.y, b.x, b.y} : join_blocks(a, b);
+            if (live && j * 16 < cols) *reinterpret_cast<tg_u32x4 *>(o + j * 16) = v;
         }
         scale += 16 * L.ldscale;
         o += 16 * L.ldc;
@@ -393,7 +405,8 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
     const bool in = SUM && L.sum_in != 0;
     float *s = P.sum + (int64_t)(R0 + c) * L.ldsum + first;  // (rows of fp32 sums are padded to a multiple of 4)
     const int64_t sstep = 16 * L.ldsum;
-    uint16_t *o = out + (int64_t)(R0 + c) * L.ldc + first;
+    const int col = C0 + q * 8, left = L.N - col;  // ... of the bf16 values
+    uint16_t *o = out + (int64_t)(R0 + c) * L.ldc + col;
     const int64_t step = 16 * L.ldc;
     // the earlier sums are read a row block ahead of the stores: loads and
     // stores are counted in order, so a load behind a store waits for it
@@ -415,22 +428,21 @@ __device__ __forceinline__ void store_epilogue(const TgLaunch &L, const TgProble
             for (int j = 0; j < FN; ++j) v[j] += ahead[j];
             fetch(i + 1);
         }
+        if (SUM && L.sum_out) {
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            if (i * 16 < rows && at(j) < cols) {
-                if (SUM && L.sum_out) {
-                    *reinterpret_cast<tg_f32x4 *>(s + i * sstep + at(j)) = v[j];
-                } else {
-                    const tg_f32x4 x = v[j] * alpha;
-                    const tg_u32x2 p{tg_pack_bf16(x[0], x[1]), tg_pack_bf16(x[2], x[3])};
-                    if (at(j) + 4 <= cols) {
-                        tg_store(o + at(j), p);
-                    } else {
-                        o[at(j)] = (uint16_t)p.x;
-                        if (at(j) + 1 < cols) o[at(j) + 1] = (uint16_t)(p.x >> 16);
-                        if (at(j) + 2 < cols) o[at(j) + 2] = (uint16_t)p.y;
-                    }
-                }
+            for (int j = 0; j < FN; ++j)
+                if (i * 16 < rows && at(j) < cols) *reinterpret_cast<tg_f32x4 *>(s + i * sstep + at(j)) = v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < FN; j += 2) {
+                auto half = [&](int k) __attribute__((always_inline)) {
+                    const tg_f32x4 x = v[k] * alpha;
+                    return tg_u32x2{tg_pack_bf16(x[0], x[1]), tg_pack_bf16(x[2], x[3])};
+                };
+                const tg_u32x2 a = half(j), b = half(j + 1);
+                const tg_u32x4 p = PERM ? tg_u32x4{a.x, a.y, b.x, b.y} : join_blocks(a, b);
+                const int n = left - j * 16;
+                if (i * 16 < rows && n > 0) tg_store8h(o + j * 16, p, n > 8 ? 8 : n);
             }
         }
         o += step;
