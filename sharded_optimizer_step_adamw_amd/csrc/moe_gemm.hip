@@ -17,6 +17,7 @@ hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
 }  // namespace
 
 int tile_height(int tile) { return tile == kTile64 ? 64 : tile == kTile128 ? 128 : 256; }
+bool tile_seeks(int tile) { return seeks_rows(tile); }
 void tile_shape(int tile, int32_t &height, int32_t &width, int32_t &rows, int32_t &cols) {
     auto set = [&](auto C) {
         height = C.BM;

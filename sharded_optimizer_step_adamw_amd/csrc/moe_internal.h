@@ -59,18 +59,16 @@ hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);
 //   kMoeItems   the items of a sum over the experts' rows (TgItem [1 + capacity])
 //               and the joins of their parts, of `height` rows at most: the parts,
 //               and behind them the experts of one part, the largest first
-//   kMoeTokens  token [slots]: the slots' tokens (-1: none); share (or
-//               NULL): their weights
+//   kMoeShares  share [slots]: the slots' weights
 //   kMoeGather  dst [slots, round8(cols)] = the slots' rows of src, zero beyond cols
 //   kMoeCopy    dst [rows, round8(cols)] = src's rows, of which each
 //               `group_rows` lie `group_stride` apart
-enum MoePrepKind : int { kMoeTiles = 0, kMoeItems = 1, kMoeGather = 2, kMoeCopy = 3, kMoeTokens = 4 };
+enum MoePrepKind : int { kMoeTiles = 0, kMoeItems = 1, kMoeGather = 2, kMoeCopy = 3, kMoeShares = 4 };
 struct MoePrep {
     int32_t kind;
     uint32_t blocks;              // set by the launch
     int32_t height, capacity;
     TgTileRow *tiles, *joins;
-    int32_t *token;
     int64_t rows, cols;
     const uint16_t *src;
     int64_t ld, group_rows, group_stride;
@@ -124,6 +122,7 @@ hipError_t launch_fill_zero_groups(uint16_t *dst, int64_t ld, int64_t group_stri
 // The products (train_internal.h's kinds, over groups).
 void plan_groups(TgEpilogue epi, TgGroups kind, bool b_km, TgLaunch &L);
 int tile_height(int tile);
+bool tile_seeks(int tile);  // finds the tile rows of 64 groups or less without a list
 // rows and columns of a tile and its waves across them
 void tile_shape(int tile, int32_t &height, int32_t &width, int32_t &rows, int32_t &cols);
 size_t group_part_bytes(const TgLaunch &L);  // kGroupDepth

@@ -167,12 +167,10 @@ __device__ __forceinline__ void prep_gather(const MoePrepList &l, const MoePrep 
     }
 }
 
-__device__ __forceinline__ void prep_tokens(const MoePrepList &l, const MoePrep &j, int64_t block) {
+__device__ __forceinline__ void prep_shares(const MoePrepList &l, const MoePrep &j, int64_t block) {
     for (int64_t s = block * kThreads + threadIdx.x; s < l.slots; s += (int64_t)j.blocks * kThreads) {
         const int slot = l.order[s];
-        const bool some = slot >= 0 && slot < l.slots;
-        j.token[s] = some ? slot / l.top : -1;
-        if (j.share != nullptr) j.share[s] = some ? j.weights[slot] : 0.0f;
+        j.share[s] = slot >= 0 && slot < l.slots ? j.weights[slot] : 0.0f;
     }
 }
 
@@ -196,8 +194,8 @@ __global__ __launch_bounds__(kThreads) void moe_prep_kernel(MoePrepList list) {
         prep_items(list, j);
     else if (j.kind == kMoeGather)
         prep_gather(list, j, block);
-    else if (j.kind == kMoeTokens)
-        prep_tokens(list, j, block);
+    else if (j.kind == kMoeShares)
+        prep_shares(list, j, block);
     else
         prep_copy(j, block);
 }
@@ -311,7 +309,7 @@ hipError_t launch_moe_prep(MoePrepList &list, hipStream_t stream) {
         MoePrep &j = list.job[k];
         const int64_t per = (j.cols + 7) / 8;
         j.blocks = j.kind == kMoeTiles || j.kind == kMoeItems ? 1
-                   : j.kind == kMoeTokens                     ? blocks_for(list.slots)
+                   : j.kind == kMoeShares                     ? blocks_for(list.slots)
                    : j.kind == kMoeGather ? blocks_for(list.slots * ((per + kGatherPieces - 1) / kGatherPieces) * 64)
                                           : blocks_for(j.rows * per);
         total += j.blocks;

@@ -129,15 +129,24 @@ struct TgLaunch {
     uint8_t *row_scale;
     int64_t ldscale;
     // groups (whole, tiles, total and padded are the kernel's own)
-    const TgTileRow *tile_row;
+    const TgTileRow *tile_row;  // kGroupRows; NULL: from offsets [groups + 1] (64 groups at most)
+    const int32_t *offsets;
     const TgItem *items, *joins;
     int32_t item_limit, join_limit;  // no more than that many; join_limit 0: no parts
     int32_t part_rows;        // a multiple of 64
     int32_t groups, slots;    // (rows of all groups)
-    // gathered A (kGroupRows): row r is row token[r] of the operand, which has `tokens`
-    // (negative: a row of zeros)
-    const int32_t *token;
-    int32_t tokens;
+    // gathered A (kGroupRows): row r is row order[r] / top of the operand, which has
+    // `tokens` (an order that is no slot: a row of zeros).  The quotient of s < 2^30 by
+    // top <= 2^k is s times top_times = ceil(2^(31 + k) / top), over 2^(31 + k): too
+    // large by less than s 2^k / (2^(31 + k) top) < 1 / top.
+    const int32_t *order;
+    int32_t tokens, top_shift;
+    uint32_t top_times;
+    void set_top(int32_t top) {
+        top_shift = 0;
+        while ((1 << top_shift) < top) ++top_shift;
+        top_times = (uint32_t)((((uint64_t)1 << (31 + top_shift)) + top - 1) / top);
+    }
     int64_t group_stride, group_out;
 };
 

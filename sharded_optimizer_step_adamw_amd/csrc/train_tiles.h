@@ -573,11 +573,15 @@ __device__ __forceinline__ void keep_part(const TgLaunch &L, int64_t at, int wav
 // (A wave whose rows lie behind the tile's end multiplies zeros.  Leaving its
 // products out changed nothing, a stage of one wave a SIMD being bound by its
 // synchronisation, nor did taking such tiles last.)
-// A gathered A: a lane's rows have offsets of their own, read from the list of
-// rows a tile ahead.  On [32768, 4096] gathered from 8192 tokens the gate's
+// A gathered A: a lane's rows have offsets of their own, read from the slots'
+// order a tile ahead.  On [32768, 4096] gathered from 8192 tokens the gate's
 // products take 877 us so, 899 and 77 for a copy in order otherwise.  (Gathering
 // the k-major operands of the weight gradients by scalar loads a stage ahead was
 // 30% slower than from such a copy, and the copies cost 12%.)
+// Without a list of tile rows (kGroupRows) a wave finds them by the groups' offsets,
+// three registers that 256 x 256 tiles do not have; the forward pass's alone, a
+// backward pass having its list from a launch that copies as well.
+constexpr bool seeks_rows(int tile) { return tile != kTile256; }
 template <int TILE, int EPI, bool AKM, bool BKM, int GRP = kNoGroups, bool LIST = false>
 __global__ __launch_bounds__(Cfg<TILE>::WR *Cfg<TILE>::WC * 64)
 __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) {
@@ -624,7 +628,33 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         int t, prob, split, m0, n0, stage0, live, stages;  // split: -1 whole; live: real stages; stages: padded
         int group, first, end;  // the group; kGroupRows: the end of its rows; kGroupDepth: its rows
     };
-    const int tiles_m = GRP == kGroupRows ? __builtin_amdgcn_readfirstlane(L.tile_row[0].group) : L.tiles_m;
+    // kGroupRows without a list of tile rows: lane g has group g's rows, and how many
+    // tile rows there are to its end
+    constexpr bool SEEKS = GRP == kGroupRows && seeks_rows(TILE) && !BKM && EPI != kTgMoeBack;
+    int glo = 0, ghi = 0, gend = 0;
+    const bool seeks = SEEKS && L.tile_row == nullptr;
+    if (seeks) {
+        auto bound = [&](int g) __attribute__((always_inline)) {  // (as moe_rows.hip's)
+            const int v = L.offsets[g];
+            return v < 0 ? 0 : v > L.slots ? L.slots : v;
+        };
+        if (lane < L.groups) {
+            glo = bound(lane);
+            ghi = bound(lane + 1);
+        }
+        gend = ghi > glo ? (ghi - glo + BM - 1) / BM : 0;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(gend, o);
+            gend += lane >= o ? v : 0;
+        }
+    }
+    auto rows_of_tiles = [&]() __attribute__((always_inline)) -> int {
+        if (!seeks) return __builtin_amdgcn_readfirstlane(L.tile_row[0].group);
+        const int all = __builtin_amdgcn_readlane(gend, 63);
+        return all < L.tiles_m ? all : L.tiles_m;
+    };
+    const int tiles_m = GRP == kGroupRows ? rows_of_tiles() : L.tiles_m;
     const int per_item = L.tiles_m * L.tiles_n * L.nprob;
     const int parts = GRP == kGroupDepth ? __builtin_amdgcn_readfirstlane(L.items[0].row) : 0;
     const int total = GRP == kGroupRows    ? tiles_m * L.tiles_n
@@ -668,10 +698,18 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         T.m0 = ti * BM;
         T.n0 = tj * BO;
         if constexpr (GRP == kGroupRows) {
-            const TgTileRow r = L.tile_row[1 + ti];
-            T.group = __builtin_amdgcn_readfirstlane(r.group);
-            T.m0 = __builtin_amdgcn_readfirstlane(r.row);
-            T.end = __builtin_amdgcn_readfirstlane(r.end);
+            if (seeks) {
+                T.group = __builtin_ctzll(__ballot(gend > ti));
+                const int lo = __builtin_amdgcn_readlane(glo, T.group);
+                T.end = __builtin_amdgcn_readlane(ghi, T.group);
+                const int first = __builtin_amdgcn_readlane(gend, T.group) - (T.end - lo + BM - 1) / BM;
+                T.m0 = lo + (ti - first) * BM;
+            } else {
+                const TgTileRow r = L.tile_row[1 + ti];
+                T.group = __builtin_amdgcn_readfirstlane(r.group);
+                T.m0 = __builtin_amdgcn_readfirstlane(r.row);
+                T.end = __builtin_amdgcn_readfirstlane(r.end);
+            }
         }
         T.stage0 = T.split < 0 ? 0 : T.split * L.split_stages;
         T.live = all - T.stage0;
@@ -738,7 +776,7 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
 #pragma unroll
             for (int x = 0; x < LA; ++x) {
                 const int row = T.m0 + first_a * (16 / SPL) + krow + rows_a(x);
-                ahead[x] = row < T.end ? L.token[row] : -1;
+                ahead[x] = row < T.end ? L.order[row] : -1;
             }
         }
     };
@@ -803,7 +841,10 @@ __attribute__((amdgpu_waves_per_eu(Cfg<TILE>::WPE))) void tg_kernel(TgLaunch L) 
         if constexpr (LIST) {
 #pragma unroll
             for (int x = 0; x < LA; ++x)
-                va[x] = ahead[x] < 0 ? kFar : (int)(((uint32_t)ahead[x] * (uint32_t)lda + (uint32_t)chunk8) * 2u);
+                va[x] = (uint32_t)ahead[x] < (uint32_t)L.slots
+                            ? (int)(((__umulhi((uint32_t)ahead[x] * 2u, L.top_times) >> L.top_shift) * (uint32_t)lda +
+                                     (uint32_t)chunk8) * 2u)
+                            : kFar;
         } else {
 #pragma unroll
             for (int x = 0; x < (PAIRS ? 1 : LA); ++x) va[x] = plus(base_a, rows_a(x) * lda);

@@ -133,3 +133,22 @@ def test_offsets_that_are_none_over_the_most_slots():
     assert grads[0].shape == (t, d) and torch.equal(offsets[1::2], torch.full_like(offsets[1::2], t * top))
     del y, grads, none, route, x
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("e", [63, 64, 65])
+def test_experts_around_a_wave(e):
+    """Up to 64 the forward products find each expert's rows themselves, beyond by a list: the same results."""
+    t, top, d, f = 500, 4, 72, 96
+    x, dy = randn(t, d, seed=50), randn(t, d, seed=51)
+    wg, wu, wd = randn(e, f, d, seed=52), randn(e, f, d, seed=53), randn(e, d, f, seed=54)
+    g = torch.Generator().manual_seed(e)
+    chosen = (torch.rand((t, top), generator=g) ** 3 * (e + 2)).to(torch.int32) - 1  # (some none, most the first ones)
+    chosen[chosen == 5] = -1  # one without tokens
+    share = torch.rand((t, top), generator=g).to(DEV)
+    route = z.moe_plan(chosen.to(DEV), share, e)
+    y, grads = z.moe_forward(x, wg, wu, wd, route), z.moe_backward(dy, x, wg, wu, wd, route)
+    at = torch.where((chosen >= 0) & (chosen < e), chosen, -1).to(DEV)
+    (ry, ey), back = ref.moe(x.double(), wg.double(), wu.double(), wd.double(), at, share.double(), "silu", dy.double())
+    inside(y, ry, ey, "y")
+    for name, got, (want, bound) in zip(("dx", "dw_gate", "dw_up", "dw_down", "dweights"), grads, back):
+        inside(got, want, bound, name)
