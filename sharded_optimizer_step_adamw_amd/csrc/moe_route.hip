@@ -68,6 +68,10 @@ __device__ __forceinline__ uint32_t rank_of(float v) {
     const uint32_t r = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
     return v != v ? 1u : v == -INFINITY ? 0u : r;
 }
+// The value of a rank above 1.
+__device__ __forceinline__ float value_of(uint32_t r) {
+    return __uint_as_float(r ^ ((uint32_t)((int32_t)~r >> 31) | 0x80000000u));
+}
 __device__ __forceinline__ uint64_t rank_of(double v) {
     const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
     const uint64_t r = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
@@ -357,10 +361,14 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 // formed in fp32 first, off by less than 2^-22 (p + |rank|), p the score: an
 // exponential by a step or two of its own size, 1 + it and the quotient by half
 // a step each (the softmax's sum is kept in 64 bits), the bias's addition by half a
-// step of the rank.  Then the best and two more are looked at again, the logistic's
-// scores in 64 bits: each has to lie before the next, by more than both may be off
-// if they are not of the same logit and bias, and the last before whatever was left.
-// A token where that does not hold is ranked again in 64 bits throughout; with
+// step of the rank.  Then the chosen ones are looked at again, the logistic's scores
+// in 64 bits: each has to lie before the next, by more than both may be off if they
+// are not of the same logit and bias, and the last before all that are left, each
+// with what it may be off itself: one far down the order may have a large score and
+// a bias that takes it away, and so be off by more than the best one left.  That is
+// asked for the largest rank left and the largest score there can be first, and
+// expert by expert in waves with a token where that does not settle it.
+// A token where all that does not hold is ranked again in 64 bits throughout; with
 // the next one's 32-bit rank for all of them instead, sixteen times as many were.
 // Bound by instruction issue and latency (16384 tokens over 256 experts in 8
 // groups, 16.8 MB: 35 us; 45 with 4 experts a lane, and 54 held to 80 registers for
@@ -420,29 +428,50 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) rank[i] = rank_of(key[i]);
-            expert = choose<NV, G>(l, rank, a.top + 2);
+            expert = choose<NV, G>(l, rank, a.top);
+            auto may_be_off = [&](float p, float rank) __attribute__((always_inline)) {
+                return 0x1p-22f * (p + fabsf(rank));
+            };
             float bc = 0.0f;
             double exactly = -INFINITY, off = 0.0;  // the rank again, and how far it may be off
-            float about = -INFINITY, about_off = 0.0f;
             if (expert >= 0) {
                 zc = read_logit(a.logits, t * a.ld + expert, a.bf16);
                 bc = a.bias != nullptr ? a.bias[expert] : 0.0f;
-                const float p = score(zc, a.sigmoid ? 0.0f : expf(zc - ref));
-                about = p + bc;
-                about_off = 0x1p-22f * (p + fabsf(about));
+                const float p = score(zc, a.sigmoid ? 0.0f : expf(zc - ref)), about = p + bc;
                 exactly = a.sigmoid ? 1.0 / (1.0 + exp(-(double)zc)) + (double)bc : (double)about;
-                off = a.sigmoid ? 0.0 : (double)about_off;
+                off = a.sigmoid ? 0.0 : (double)may_be_off(p, about);
                 near |= about != about;
             }
             const double before = __shfl_up(exactly, 1), before_off = __shfl_up(off, 1);
-            const bool same = __shfl_up(zc, 1) == zc && __shfl_up(bc, 1) == bc && __shfl_up(expert, 1) >= 0 && expert >= 0;
-            // before this one; before this one and all that were left
-            const bool first = expert < 0 || before - exactly > before_off + off || same;
-            const bool clear = expert < 0 || before - (double)about > before_off + (double)about_off;
-            // (lane top: the first one left; if it is the last one's equal, the next)
-            const uint64_t clears = __ballot(clear) >> l.first, sames = __ballot(same) >> l.first;
-            near |= l.gl > 0 && l.gl < a.top && !first;
-            near |= !((clears >> a.top & 1) || ((sames >> a.top & 1) && (clears >> (a.top + 1) & 1)));
+            const bool same = __shfl_up(zc, 1) == zc && __shfl_up(bc, 1) == bc;
+            near |= l.gl > 0 && l.gl < a.top && expert >= 0 && !(before - exactly > before_off + off || same);
+            // The last chosen against what is left.  (Ranks as numbers are in the order of
+            // rank + 2^-22 |rank|, too; fewer chosen than `top`: nothing is left.)
+            uint32_t most = rank[0];
+#pragma unroll
+            for (int i = 1; i < NV; ++i) most = rank[i] > most ? rank[i] : most;
+            most = group_max(most, G);
+            const bool last = l.gl == a.top - 1 && expert >= 0 && most > 1;
+            const double least = exactly - off;
+            const float left = value_of(most);
+            const bool unclear = last && !(least > (double)left + (double)may_be_off(a.sigmoid ? 1.0f : 1.0f / sum, left));
+            if (__ballot(unclear) != 0) {
+                const float zl = __shfl(zc, l.first + a.top - 1), bl = __shfl(bc, l.first + a.top - 1);
+                double worst = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    // (one expert after the other: few registers; an equal of the last one lies behind it)
+                    __builtin_amdgcn_sched_barrier(0);
+                    if (rank[i] <= 1) continue;
+                    const int e = l.gl * NV + i;
+                    const float z = read_logit(a.logits, t * a.ld + e, a.bf16), b = a.bias != nullptr ? a.bias[e] : 0.0f;
+                    const float p = score(z, a.sigmoid ? 0.0f : expf(z - ref)), about = value_of(rank[i]);
+                    const double most = (double)about + (double)may_be_off(p, about);
+                    worst = (z != zl || b != bl) && most > worst ? most : worst;
+                }
+                worst = join(worst, G, [](double x, double y) { return x > y ? x : y; });
+                near |= unclear && !(least > worst);
+            }
             uint64_t again = __ballot(near && live);
             while (again != 0) {
                 // the lowest token of those, by all lanes
