@@ -358,16 +358,20 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 }
 
 // G lanes a token, NV neighbouring experts a lane.  Ranks by score and bias are
-// formed in fp32 first, off by less than 2^-22 (p + |rank|), p the score: an
-// exponential by a step or two of its own size, 1 + it and the quotient by half
-// a step each (the softmax's sum is kept in 64 bits), the bias's addition by half a
-// step of the rank.  Then the chosen ones are looked at again, the logistic's scores
-// in 64 bits: each has to lie before the next, by more than both may be off if they
-// are not of the same logit and bias, and the last before all that are left, each
-// with what it may be off itself: one far down the order may have a large score and
-// a bias that takes it away, and so be off by more than the best one left.  That is
-// asked for the largest rank left and the largest score there can be first, and
-// expert by expert in waves with a token where that does not settle it.
+// formed in fp32 first.  With steps of 2^-24, a score p is off by
+//   logistic   p times 2 x 2 (the exponential) + 1 + 1 (1 + it, the quotient)
+//   softmax    p times d (the rounding of its logit's distance d to the largest) + 4 (the
+//              exponential) + 4 + 7 (the sum, kept in 64 bits, of terms that are off so,
+//              whose mean distance is below the logarithm of 1024 experts) + 1 + 1
+// and a rank by one step of its own besides.  may_be_off takes 8, d + 20 and 2 steps, and
+// no distance past 128, of which no score is left.
+// Then the chosen ones are looked at again, the logistic's scores in 64 bits: each has
+// to lie before the next, by more than both may be off if they are not of the same
+// logit and bias, and the last before all that are left, each with what it may be off
+// itself: one far down the order may have a large score and a bias that takes it away,
+// and so be off by more than the best one left.  That is asked for the largest rank left
+// and the largest score there can be first, and expert by expert in waves with a token
+// where that does not settle it.
 // A token where all that does not hold is ranked again in 64 bits throughout; with
 // the next one's 32-bit rank for all of them instead, sixteen times as many were.
 // Bound by instruction issue and latency (16384 tokens over 256 experts in 8
@@ -424,13 +428,17 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
 #pragma unroll
                 for (int i = 0; i < NV; ++i) near |= fabsf(key[i]) > 2.0f && key[i] != -INFINITY;
                 const float gap = choose_ranges<NV, G>(a, l, key, rows + l.row * a.row_floats);
-                near |= !(gap > 0x1p-18f);  // (of sums of two, each p + |rank| at most 3)
+                // (Two sums of two ranks that are 2 at most.  Logistic scores: 4 x 8 steps, 4 x 2 of the
+                // ranks and 2 x 4 of the sums, 48 in all; a softmax's scores are together 1 at
+                // most and p d below 1 / e, 22 + 16.)
+                near |= !(gap > 0x1p-18f);
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) rank[i] = rank_of(key[i]);
             expert = choose<NV, G>(l, rank, a.top);
-            auto may_be_off = [&](float p, float rank) __attribute__((always_inline)) {
-                return 0x1p-22f * (p + fabsf(rank));
+            // (d: how far its logit lies below the largest)
+            auto may_be_off = [&](float p, float d, float rank) __attribute__((always_inline)) {
+                return 0x1p-24f * (p * (a.sigmoid ? 8.0f : 20.0f + fminf(d, 128.0f)) + 2.0f * fabsf(rank));
             };
             float bc = 0.0f;
             double exactly = -INFINITY, off = 0.0;  // the rank again, and how far it may be off
@@ -439,14 +447,15 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
                 bc = a.bias != nullptr ? a.bias[expert] : 0.0f;
                 const float p = score(zc, a.sigmoid ? 0.0f : expf(zc - ref)), about = p + bc;
                 exactly = a.sigmoid ? 1.0 / (1.0 + exp(-(double)zc)) + (double)bc : (double)about;
-                off = a.sigmoid ? 0.0 : (double)may_be_off(p, about);
+                off = a.sigmoid ? 0.0 : (double)may_be_off(p, ref - zc, about);
                 near |= about != about;
             }
             const double before = __shfl_up(exactly, 1), before_off = __shfl_up(off, 1);
             const bool same = __shfl_up(zc, 1) == zc && __shfl_up(bc, 1) == bc;
             near |= l.gl > 0 && l.gl < a.top && expert >= 0 && !(before - exactly > before_off + off || same);
             // The last chosen against what is left.  (Ranks as numbers are in the order of
-            // rank + 2^-22 |rank|, too; fewer chosen than `top`: nothing is left.)
+            // rank + 2^-23 |rank|, too, and e^-d (d + 20) is largest for d = 0; fewer chosen
+            // than `top`: nothing is left.)
             uint32_t most = rank[0];
 #pragma unroll
             for (int i = 1; i < NV; ++i) most = rank[i] > most ? rank[i] : most;
@@ -454,7 +463,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
             const bool last = l.gl == a.top - 1 && expert >= 0 && most > 1;
             const double least = exactly - off;
             const float left = value_of(most);
-            const bool unclear = last && !(least > (double)left + (double)may_be_off(a.sigmoid ? 1.0f : 1.0f / sum, left));
+            const bool unclear = last && !(least > (double)left + (double)may_be_off(a.sigmoid ? 1.0f : 1.0f / sum, 0.0f, left));
             if (__ballot(unclear) != 0) {
                 const float zl = __shfl(zc, l.first + a.top - 1), bl = __shfl(bc, l.first + a.top - 1);
                 double worst = -INFINITY;
@@ -466,7 +475,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
                     const int e = l.gl * NV + i;
                     const float z = read_logit(a.logits, t * a.ld + e, a.bf16), b = a.bias != nullptr ? a.bias[e] : 0.0f;
                     const float p = score(z, a.sigmoid ? 0.0f : expf(z - ref)), about = value_of(rank[i]);
-                    const double most = (double)about + (double)may_be_off(p, about);
+                    const double most = (double)about + (double)may_be_off(p, ref - z, about);
                     worst = (z != zl || b != bl) && most > worst ? most : worst;
                 }
                 worst = join(worst, G, [](double x, double y) { return x > y ? x : y; });

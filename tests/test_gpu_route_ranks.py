@@ -2,6 +2,8 @@
 unequal parts, against a 64-bit sort.  Inputs come from a seed; each test first
 shows that 64 bits settle them: no two ranks that matter are within 2^-48 of the
 larger."""
+import math
+
 import pytest
 import torch
 
@@ -65,3 +67,32 @@ def unequal_parts(score, experts, seed):
 def test_one_left_out_may_be_further_off_than_the_first_left_out(score, experts, top):
     x, bias = unequal_parts(score, experts, experts + top)
     check(x, bias, score, top)
+
+
+def far_below(experts, distance, seed):
+    """Two experts whose logits lie `distance` and some 3 more below the largest, with biases
+    of their scores' size: of the first, 0.1 is left, to which the second's 0.05 and its bias
+    add up within 2e-6 of the first's score.  Of the others none comes near."""
+    g = torch.Generator().manual_seed(seed)
+    uniform = lambda lo, hi: lo + (hi - lo) * torch.rand(T, generator=g, dtype=torch.float64)  # noqa: E731
+    x = torch.full((T, experts), -200.0)
+    x[:, 0] = uniform(6.0, 8.0).float()
+    top = x[:, 0].double()
+    at = math.exp(-distance)  # (the largest has all of the sum but some 1e-3 at most)
+    bias = torch.full((experts,), -1.0)
+    bias[0], bias[1], bias[2] = -1.5, -0.9 * at, 0.05 * at
+    x[:, 1] = (top - distance + uniform(-2e-3, 2e-3)).float()
+    first = (x[:, 1].double() - top).exp()
+    for _ in range(3):  # (the second's score is a part of the sum)
+        total = 1 + first + torch.where(x[:, 2] > -200.0, (x[:, 2].double() - top).exp(), 0.0)
+        second = first / total + bias[1].double() - bias[2].double() + 2e-6 * at * uniform(-1, 1)
+        x[:, 2] = (top + (second * total).log()).float()
+    return x, bias
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("distance", [7, 20, 40, 60])
+@pytest.mark.parametrize("experts", [8, 60, 256])
+def test_softmax_scores_far_below_the_largest_are_off_by_more(experts, distance, top):
+    check(*far_below(experts, distance, distance + experts), "softmax", top)
