@@ -363,8 +363,9 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 //   softmax    p times d (the rounding of its logit's distance d to the largest) + 4 (the
 //              exponential) + 4 + 7 (the sum, kept in 64 bits, of terms that are off so,
 //              whose mean distance is below the logarithm of 1024 experts) + 1 + 1
-// and a rank by one step of its own besides.  may_be_off takes 8, d + 20 and 2 steps, and
-// no distance past 128, of which no score is left.
+// and a rank by one step of its own besides; below fp32's range (or where an exponential
+// overflows) by 2^-126.  may_be_off takes 8, d + 20 and 2 steps, and no distance past 128,
+// of which no score is left.
 // Then the chosen ones are looked at again, the logistic's scores in 64 bits: each has
 // to lie before the next, by more than both may be off if they are not of the same
 // logit and bias, and the last before all that are left, each with what it may be off
@@ -438,7 +439,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
             expert = choose<NV, G>(l, rank, a.top);
             // (d: how far its logit lies below the largest)
             auto may_be_off = [&](float p, float d, float rank) __attribute__((always_inline)) {
-                return 0x1p-24f * (p * (a.sigmoid ? 8.0f : 20.0f + fminf(d, 128.0f)) + 2.0f * fabsf(rank));
+                return 0x1p-24f * (p * (a.sigmoid ? 8.0f : 20.0f + fminf(d, 128.0f)) + 2.0f * fabsf(rank)) + 0x1p-126f;
             };
             float bc = 0.0f;
             double exactly = -INFINITY, off = 0.0;  // the rank again, and how far it may be off

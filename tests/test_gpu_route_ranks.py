@@ -96,3 +96,15 @@ def far_below(experts, distance, seed):
 @pytest.mark.parametrize("experts", [8, 60, 256])
 def test_softmax_scores_far_below_the_largest_are_off_by_more(experts, distance, top):
     check(*far_below(experts, distance, distance + experts), "softmax", top)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("groups", [1, 2])
+@pytest.mark.parametrize("experts", [8, 200])
+def test_scores_below_fp32_keep_their_order(experts, groups):
+    """Logistic scores that fp32 does not hold, down to e^-700."""
+    g = torch.Generator().manual_seed(experts)
+    x = -90.0 - 20.0 * torch.rand((T, experts), generator=g)
+    x[:, ::3] *= 5.0
+    for top in (1, 4):
+        check(x, torch.zeros(experts), "sigmoid", top, groups, groups)
