@@ -110,7 +110,8 @@ struct BestTwo {
 template <int NV, int G>
 __device__ __forceinline__ float choose_ranges(const RouteArgs &a, const RouteLane &l, float (&key)[NV], float *sums) {
     const int size = a.experts / a.groups, lanes = size / NV, e0 = l.gl * NV;
-    auto order = [](float v) __attribute__((always_inline)) { return v != v ? -3.0e38f : v; };
+    // (a NaN's place behind every number; two of them are still a number)
+    auto order = [](float v) __attribute__((always_inline)) { return v != v ? -1.5e38f : v; };
     float last = INFINITY, left = -INFINITY;
     // whether range x, of sum v, stays
     auto stays = [&](float v, int x) __attribute__((always_inline)) {
@@ -223,7 +224,7 @@ __device__ __forceinline__ int choose_exactly(const RouteArgs &a, int64_t t, dou
         double k = (a.sigmoid ? 1.0 : x) / (a.sigmoid ? 1.0 + x : total);
         const double b = a.bias != nullptr ? (double)a.bias[e] : 0.0;
         k += b;
-        lds[e] = fmin(z, b) == kNone ? kNone : k != k ? -1.7e308 : k;
+        lds[e] = fmin(z, b) == kNone ? kNone : k != k ? -0.85e308 : k;  // (as in choose_ranges)
     }
     wave_sync();
     if (a.groups > 1) {
