@@ -152,8 +152,7 @@ __global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
         uint16_t *const out = S.out + t * S.ot + head * S.oh;
         const int64_t pos = cur.pos;
         const bool none = pos < 0, known = !none && pos < a.positions;
-        // (a row without a position is zeros, one whose position the table lacks is NaN)
-        const float fill = none || known ? 0.0f : NAN;
+        const bool strange = __ballot(!known) != 0;
         float x[NP][2 * V], d[NP][2 * V];
         float2 cs[NP][V];
 #pragma unroll
@@ -173,15 +172,29 @@ __global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
                 widen<V>(cur.d[j], &d[j][0]);
                 widen<V>(cur.d2[j], &d[j][V]);
             }
-            // (places past the row's end, in a wrong row too, add nothing)
+            // (places past the row's end add nothing)
 #pragma unroll
             for (int k = 0; k < 2 * V; ++k) {
                 const bool in = k < V ? have[j] : have2[j];
-                x[j][k] = !in ? 0.0f : known ? x[j][k] : fill;
-                if constexpr (BACK) d[j][k] = !in ? 0.0f : known ? d[j][k] : fill;
-                ss += x[j][k] * x[j][k];
+                x[j][k] = in ? x[j][k] : 0.0f;
+                if constexpr (BACK) d[j][k] = in ? d[j][k] : 0.0f;
             }
         }
+        if (__builtin_expect(strange, 0)) {
+            // (a row without a position is zeros, one whose position the table lacks is NaN)
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int k = 0; k < 2 * V; ++k) {
+                    const float fill = none || !(k < V ? have[j] : have2[j]) ? 0.0f : NAN;
+                    x[j][k] = known ? x[j][k] : fill;
+                    if constexpr (BACK) d[j][k] = known ? d[j][k] : fill;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int k = 0; k < 2 * V; ++k) ss += x[j][k] * x[j][k];
         cur = next;
         ss = group_sum(ss, G);
         const float r = none ? 0.0f : 1.0f / sqrtf(ss * inv_width + a.eps);
@@ -210,6 +223,12 @@ __global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
             for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int k = 0; k < 2 * V; ++k) x[j][k] = r * (d[j][k] - x[j][k] * m);
+        }
+        if (__builtin_expect(strange, 0)) {  // (zeros whatever the weights are)
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int k = 0; k < 2 * V; ++k) x[j][k] = none ? 0.0f : x[j][k];
         }
         if (live) {
 #pragma unroll
