@@ -197,7 +197,25 @@ __global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
             for (int k = 0; k < 2 * V; ++k) ss += x[j][k] * x[j][k];
         cur = next;
         ss = group_sum(ss, G);
-        const float r = none ? 0.0f : 1.0f / sqrtf(ss * inv_width + a.eps);
+        // A row whose squares pass fp32's range, or lie so far down that some that count are
+        // no normal numbers (which needs an eps of next to nothing), is multiplied by a
+        // power of two first: r is 0 or above 2^40 then, of rows without a position too.
+        float r = 1.0f / sqrtf(ss * inv_width + a.eps);
+        const bool odd = __float_as_uint(r) - 1 >= __float_as_uint(0x1p40f), rescaled = __ballot(odd) != 0;
+        const float factor = !odd ? 1.0f : r == 0.0f ? 0x1p-70f : 0x1p70f;
+        if (__builtin_expect(rescaled, 0)) {
+            float sq = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int k = 0; k < 2 * V; ++k) {
+                    x[j][k] *= factor;
+                    sq += x[j][k] * x[j][k];
+                }
+            sq = group_sum(sq, G);
+            r = 1.0f / sqrtf(sq * inv_width + a.eps * factor * factor);
+        }
+        r = none ? 0.0f : r;
         if constexpr (!BACK) {
 #pragma unroll
             for (int j = 0; j < NP; ++j) {
@@ -223,6 +241,12 @@ __global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
             for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int k = 0; k < 2 * V; ++k) x[j][k] = r * (d[j][k] - x[j][k] * m);
+            if (__builtin_expect(rescaled, 0)) {
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+#pragma unroll
+                    for (int k = 0; k < 2 * V; ++k) x[j][k] *= factor;
+            }
         }
         if (__builtin_expect(strange, 0)) {  // (zeros whatever the weights are)
 #pragma unroll
