@@ -1042,6 +1042,13 @@ def _rope_out(t, like, name, on):
 _NO_HEADS = (None, 0, 0)
 
 
+def _need_no_keys(**given):
+    """Refuses what belongs to keys in a call without any."""
+    for name, t in given.items():
+        if t is not None:
+            raise ValueError(f"{name}: given without k")
+
+
 def qk_norm_rope(q, k, table, position=None, w_q=None, w_k=None, eps: float = 1e-6,
                  style: str = "half", out_q: Optional[torch.Tensor] = None,
                  out_k: Optional[torch.Tensor] = None, stream=None):
@@ -1053,6 +1060,8 @@ def qk_norm_rope(q, k, table, position=None, w_q=None, w_k=None, eps: float = 1e
     w_k bf16 [width] or None, style "half" or "pairs".  Returns (yq, yk), bf16;
     out_q may be q, and out_k k."""
     sizes, heads, rest = _rope_args(q, k, table, position, w_q, w_k, eps, style)
+    if k is None:
+        _need_no_keys(out_k=out_k)
     on = _On(q.device, stream)
     out_q, yq = _rope_out(out_q, q, "out_q", on)
     out_k, yk = (None, _NO_HEADS) if k is None else _rope_out(out_k, k, "out_k", on)
@@ -1068,8 +1077,11 @@ def qk_norm_rope_backward(dyq, dyk, q, k, table, position=None, w_q=None, w_k=No
                           workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients (dq, dk, dw_q, dw_k) of qk_norm_rope from those of its outputs
     and its arguments (zopt_qk_norm_rope_backward); dw_q and dw_k are None
-    where there is no weight.  dq may be dyq, and dk dyk."""
+    where there is no weight, unless they are given (those of weights that are
+    all 1).  dq may be dyq, and dk dyk."""
     sizes, heads, rest = _rope_args(q, k, table, position, w_q, w_k, eps, style)
+    if k is None:
+        _need_no_keys(dyk=dyk, dk=dk, dw_k=dw_k)
     on = _On(q.device, stream)
     index = on.device.index
     ins, outs, grads = (), (), []
@@ -1081,9 +1093,7 @@ def qk_norm_rope_backward(dyq, dyk, q, k, table, position=None, w_q=None, w_k=No
         s = _need_heads(dy, x.shape, f"dy{name}", index)
         dx, to = _rope_out(dx, x, f"d{name}", on)
         ins, outs = ins + (dy.data_ptr(), s[0], s[1]), outs + to
-        if w is None:
-            dw = None
-        elif dw is None:
+        if w is not None and dw is None:
             dw = _new(on, w, w.shape)
         grads += [dx, dw, _need_shape(dw, torch.bfloat16, (sizes[3],), f"dw_{name}", index)]
     args = (*sizes, *ins, *heads, *rest, *outs, grads[2], grads[5])
