@@ -36,19 +36,19 @@ struct Weight {
     bool copy;
     size_t at;
 };
+bool weight_needs_copy(const uint16_t *p, int64_t ld, int64_t group, int64_t cols) {
+    return !aligned16(p) || (ld & 7) || (group & 7) || (cols & 7) || ld > kMaxStride;
+}
 Weight weight(const uint16_t *p, int64_t ld, int64_t group, int64_t experts, int64_t rows, int64_t cols, bool force,
               Carve &c) {
     Weight w{p, ld, group, false, 0};
-    w.copy = force || !aligned16(p) || (ld & 7) || (group & 7) || (cols & 7) || ld > kMaxStride;
+    w.copy = force || weight_needs_copy(p, ld, group, cols);
     if (w.copy) {
         w.ld = up(cols, 8);
         w.group = rows * w.ld;
         w.at = c.take(experts * w.group * 2);
     }
     return w;
-}
-bool weight_needs_copy(const uint16_t *p, int64_t ld, int64_t group, int64_t cols) {
-    return !aligned16(p) || (ld & 7) || (group & 7) || (cols & 7) || ld > kMaxStride;
 }
 
 // A matrix [tokens, cols] whose rows the products take by expert: gathered as it

@@ -4,17 +4,6 @@
 #include "train_tiles.h"
 
 namespace zopt {
-namespace {
-
-template <int EPI, bool AKM, bool BKM, int GRP, bool LIST>
-hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
-    if (L.tile == kTile256) return run<kTile256, EPI, AKM, BKM, GRP, LIST>(L, stream);
-    if (L.tile == kTile256x128) return run<kTile256x128, EPI, AKM, BKM, GRP, LIST>(L, stream);
-    if (L.tile == kTile128) return run<kTile128, EPI, AKM, BKM, GRP, LIST>(L, stream);
-    return run<kTile64, EPI, AKM, BKM, GRP, LIST>(L, stream);
-}
-
-}  // namespace
 
 int tile_height(int tile) { return tile == kTile64 ? 64 : tile == kTile128 ? 128 : 256; }
 bool tile_seeks(int tile) { return seeks_rows(tile); }

@@ -56,9 +56,10 @@ hipError_t launch_route_back(const RouteBackArgs &a, hipStream_t stream);
 // What precedes the products, all in one launch:
 //   kMoeTiles   the tile rows of height `height` (TgTileRow [1 + capacity]) from
 //               the offsets
-//   kMoeItems   the items of a sum over the experts' rows (TgItem [1 + capacity])
-//               and the joins of their parts, of `height` rows at most: the parts,
-//               and behind them the experts of one part, the largest first
+//   kMoeItems   the items of a sum over the experts' rows (TgItem [1 + experts + 2 (slots
+//               / height)]) and the joins of their parts, of `height` rows at most (TgItem
+//               [slots / height], no more than the experts): the parts, and behind
+//               them the experts of one part, the largest first
 //   kMoeShares  share [slots]: the slots' weights
 //   kMoeGather  dst [slots, round8(cols)] = the slots' rows of src, zero beyond cols
 //   kMoeCopy    dst [rows, round8(cols)] = src's rows, of which each
@@ -67,7 +68,7 @@ enum MoePrepKind : int { kMoeTiles = 0, kMoeItems = 1, kMoeGather = 2, kMoeCopy 
 struct MoePrep {
     int32_t kind;
     uint32_t blocks;              // set by the launch
-    int32_t height, capacity;
+    int32_t height, capacity;     // (capacity: of kMoeTiles)
     TgTileRow *tiles, *joins;
     int64_t rows, cols;
     const uint16_t *src;

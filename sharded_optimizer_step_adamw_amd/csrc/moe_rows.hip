@@ -15,11 +15,6 @@ uint32_t blocks_for(int64_t n) {
     return (uint32_t)(b < 1 ? 1 : b > (1 << 20) ? (1 << 20) : b);
 }
 
-__device__ __forceinline__ tg_u32x4 pack8(const float (&v)[8]) {
-    return tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
-                    tg_pack_bf16(v[6], v[7])};
-}
-
 // A value of the routing's arrays as an index in [0, n], whatever was given:
 // arrays that are not a routing's give wrong sums, but no access out of range.
 __device__ __forceinline__ int within(int v, int64_t n) { return v < 0 ? 0 : v > n ? (int)n : v; }
@@ -220,7 +215,7 @@ __device__ __forceinline__ void combine_rows(const MoeCombine &c, int64_t block)
                 sum[2 * i + 1] += w * tg_rows_out((float)h.y, e);
             }
         }
-        tg_store8h(c.out + t * c.ldo + col, pack8(sum), left > 8 ? 8 : (int)left);
+        tg_store8h(c.out + t * c.ldo + col, tg_pack8(sum), left > 8 ? 8 : (int)left);
     }
 }
 

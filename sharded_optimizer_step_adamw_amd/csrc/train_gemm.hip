@@ -3,17 +3,6 @@
 #include "train_tiles.h"
 
 namespace zopt {
-namespace {
-
-template <int EPI, bool AKM, bool BKM>
-hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
-    if (L.tile == kTile256) return run<kTile256, EPI, AKM, BKM>(L, stream);
-    if (L.tile == kTile256x128) return run<kTile256x128, EPI, AKM, BKM>(L, stream);
-    if (L.tile == kTile128) return run<kTile128, EPI, AKM, BKM>(L, stream);
-    return run<kTile64, EPI, AKM, BKM>(L, stream);
-}
-
-}  // namespace
 
 // Tile and split, by an estimate of the launch's time in microseconds from
 // figures measured on the card (256 CUs):

@@ -266,6 +266,17 @@ typedef uint32_t tg_u32x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ uint32_t tg_pack_bf16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(tg_f32x2{lo, hi}, tg_bf16x2));
 }
+__device__ __forceinline__ tg_u32x4 tg_pack8(const float (&v)[8]) {
+    return tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
+                    tg_pack_bf16(v[6], v[7])};
+}
+__device__ __forceinline__ void tg_unpack8(tg_u32x4 p, float (&v)[8]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        v[2 * k] = __uint_as_float(p[k] << 16);
+        v[2 * k + 1] = __uint_as_float(p[k] & 0xFFFF0000u);
+    }
+}
 __device__ __forceinline__ uint32_t tg_pack_f16(float lo, float hi) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(tg_f32x2{lo, hi}, tg_f16x2));
 }

@@ -22,18 +22,6 @@ uint32_t blocks_for(int64_t n) {
 // (a [8192, 4096] one 41 and 39).
 bool past_half(int64_t bytes) { return bytes > kCacheBytes / 2; }
 
-__device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(p[k] << 16);
-        v[2 * k + 1] = __uint_as_float(p[k] & 0xFFFF0000u);
-    }
-}
-__device__ __forceinline__ tg_u32x4 pack8(const float (&v)[8]) {
-    return tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
-                    tg_pack_bf16(v[6], v[7])};
-}
-
 __global__ __launch_bounds__(kThreads) void fill_zero_kernel(uint16_t *__restrict__ dst, int64_t ld, int64_t rows,
                                                              int64_t cols) {
     const int64_t total = rows * cols;
@@ -59,7 +47,7 @@ __global__ __launch_bounds__(kThreads) void act8_pack_kernel(const uint16_t *__r
         tg_u32x4 p{0, 0, 0, 0};
         if (n > 0) p = tg_load8h<PAST>(x + r * ld + c, n);
         float v[8];
-        unpack8(p, v);
+        tg_unpack8(p, v);
         uint32_t big = 0;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -92,7 +80,7 @@ __global__ __launch_bounds__(kThreads) void act8_unpack_kernel(const uint8_t *__
         const int n = cols - c > 8 ? 8 : (int)(cols - c);
         float v[8];
         act8_values(q, scale, r, c, cols, blocks, n, v);
-        tg_store8h<PAST>(x + r * ld + c, pack8(v), n);
+        tg_store8h<PAST>(x + r * ld + c, tg_pack8(v), n);
     }
 }
 
@@ -182,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void xent_rows_kernel(const float2 *__res
                     if (rel == k) v[k] = expm1f(-loss);
                     if (c + k >= V) v[k] = 0.0f;
                 }
-                out = pack8(v);
+                out = tg_pack8(v);
             }
             tg_store<PAST>(at, out);
         }
@@ -214,7 +202,7 @@ __device__ __forceinline__ void prep_unpack(const TgPrep &j, int64_t block) {
         act8_values(j.q, j.scale, r, c, j.cols, blocks, n, v);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = k < n ? v[k] : 0.0f;
-        *reinterpret_cast<tg_u32x4 *>(j.dst + id * 8) = pack8(v);
+        *reinterpret_cast<tg_u32x4 *>(j.dst + id * 8) = tg_pack8(v);
     }
 }
 // dg = dh u act'(g), du = dh act(g), h = act(g) u
@@ -226,7 +214,7 @@ __device__ __forceinline__ void prep_back(const TgPrep &j, int64_t block) {
         float g[8], u[8], d[8], og[8], ou[8], oh[8];
         act8_values(j.q, j.scale, r, c, j.cols, blocks, n, g);
         act8_values(j.q2, j.scale2, r, c, j.cols, blocks, n, u);
-        unpack8(tg_load8h(j.src + r * j.ld + c, n), d);
+        tg_unpack8(tg_load8h(j.src + r * j.ld + c, n), d);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             const TgActValue a = tg_act(g[k], j.act);
@@ -234,9 +222,9 @@ __device__ __forceinline__ void prep_back(const TgPrep &j, int64_t block) {
             ou[k] = k < n ? d[k] * a.a : 0.0f;
             oh[k] = a.a * u[k];
         }
-        *reinterpret_cast<tg_u32x4 *>(j.dst + r * j.dst_ld + c) = pack8(og);
-        *reinterpret_cast<tg_u32x4 *>(j.dst2 + r * j.dst_ld + c) = pack8(ou);
-        if (j.h != nullptr) tg_store8h(j.h + r * j.h_ld + c, pack8(oh), n);
+        *reinterpret_cast<tg_u32x4 *>(j.dst + r * j.dst_ld + c) = tg_pack8(og);
+        *reinterpret_cast<tg_u32x4 *>(j.dst2 + r * j.dst_ld + c) = tg_pack8(ou);
+        if (j.h != nullptr) tg_store8h(j.h + r * j.h_ld + c, tg_pack8(oh), n);
     }
 }
 __device__ __forceinline__ void prep_count(const TgPrep &j) {

@@ -161,18 +161,6 @@ __device__ __forceinline__ void xent_epilogue(const TgLaunch &L, tg_f32x4 (&acc)
     }
 }
 
-__device__ __forceinline__ tg_u32x4 pack8(const float (&v)[8]) {
-    return tg_u32x4{tg_pack_bf16(v[0], v[1]), tg_pack_bf16(v[2], v[3]), tg_pack_bf16(v[4], v[5]),
-                    tg_pack_bf16(v[6], v[7])};
-}
-__device__ __forceinline__ void unpack8(tg_u32x4 p, float (&v)[8]) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        v[2 * k] = __uint_as_float(p[k] << 16);
-        v[2 * k + 1] = __uint_as_float(p[k] & 0xFFFF0000u);
-    }
-}
-
 // One row's 32-column block of an 8-bit checkpoint, eight values in each of
 // the lanes q = 0 .. 3 of column c: the scale from the largest magnitude of
 // all four, then the lane's eight bytes.
@@ -227,10 +215,10 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
             for (int k = 0; k < 8; ++k) h[k] = tg_act(g[k], L.act).a * u[k];
             if constexpr (GRP != kNoGroups) {
                 // (rows in the workspace, padded to 8: beyond F the products, and so h, are 0)
-                if (live && n > 0) *reinterpret_cast<tg_u32x4 *>(L.h + (int64_t)row * L.ldc + col) = pack8(h);
+                if (live && n > 0) *reinterpret_cast<tg_u32x4 *>(L.h + (int64_t)row * L.ldc + col) = tg_pack8(h);
                 continue;
             }
-            if (live && n > 0) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n);
+            if (live && n > 0) tg_store8h(L.h + (int64_t)row * L.ldc + col, tg_pack8(h), n);
             if (L.g8 != nullptr) {
                 act8_store(g, n, L.g8 + (int64_t)row * F, L.gs + (int64_t)row * blocks, col, q, live);
                 act8_store(u, n, L.u8 + (int64_t)row * F, L.us + (int64_t)row * blocks, col, q, live);
@@ -238,7 +226,7 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
         } else {
             if (live && n > 0) {
                 float dh[8], dg[8], du[8];
-                unpack8(ahead[i % kAhead], dh);
+                tg_unpack8(ahead[i % kAhead], dh);
                 fetch(i + kAhead);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -248,9 +236,9 @@ __device__ __forceinline__ void glu_epilogue(const TgLaunch &L, tg_f32x4 (&acc)[
                     dg[k] = k < n ? dh[k] * u[k] * a.da : 0.0f;
                 }
                 // (the padded row has room for all eight)
-                *reinterpret_cast<tg_u32x4 *>(L.dg + (int64_t)row * L.lddg + col) = pack8(dg);
-                *reinterpret_cast<tg_u32x4 *>(L.du + (int64_t)row * L.lddg + col) = pack8(du);
-                if (L.h != nullptr) tg_store8h(L.h + (int64_t)row * L.ldc + col, pack8(h), n);
+                *reinterpret_cast<tg_u32x4 *>(L.dg + (int64_t)row * L.lddg + col) = tg_pack8(dg);
+                *reinterpret_cast<tg_u32x4 *>(L.du + (int64_t)row * L.lddg + col) = tg_pack8(du);
+                if (L.h != nullptr) tg_store8h(L.h + (int64_t)row * L.ldc + col, tg_pack8(h), n);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -305,9 +293,9 @@ __device__ __forceinline__ void moe_back_epilogue(const TgLaunch &L, tg_f32x4 (&
                 du[k] = k < n ? share * d * a.a : 0.0f;
                 dg[k] = k < n ? share * d * u * a.da : 0.0f;
             }
-            *reinterpret_cast<tg_u32x4 *>(L.dg + (int64_t)row * L.lddg + col) = pack8(dg);
-            *reinterpret_cast<tg_u32x4 *>(L.du + (int64_t)row * L.lddg + col) = pack8(du);
-            *reinterpret_cast<tg_u32x4 *>(L.h + (int64_t)row * L.ldc + col) = pack8(h);
+            *reinterpret_cast<tg_u32x4 *>(L.dg + (int64_t)row * L.lddg + col) = tg_pack8(dg);
+            *reinterpret_cast<tg_u32x4 *>(L.du + (int64_t)row * L.lddg + col) = tg_pack8(du);
+            *reinterpret_cast<tg_u32x4 *>(L.h + (int64_t)row * L.ldc + col) = tg_pack8(h);
         }
         dot = quad_sum(dot);
         if (live && q == 0) L.dot[(int64_t)row * L.lddot + C0 / 32] = dot;
@@ -1159,6 +1147,15 @@ hipError_t run(TgLaunch &L, hipStream_t stream) {
         e = hipGetLastError();
     }
     return e;
+}
+
+// ... with the tile that the plan chose
+template <int EPI, bool AKM, bool BKM, int GRP = kNoGroups, bool LIST = false>
+hipError_t run_tile(TgLaunch &L, hipStream_t stream) {
+    if (L.tile == kTile256) return run<kTile256, EPI, AKM, BKM, GRP, LIST>(L, stream);
+    if (L.tile == kTile256x128) return run<kTile256x128, EPI, AKM, BKM, GRP, LIST>(L, stream);
+    if (L.tile == kTile128) return run<kTile128, EPI, AKM, BKM, GRP, LIST>(L, stream);
+    return run<kTile64, EPI, AKM, BKM, GRP, LIST>(L, stream);
 }
 
 }  // namespace
