@@ -10,10 +10,16 @@ namespace zopt {
 namespace {
 
 constexpr int kRouteThreads = 512, kPlanThreads = 256, kAloneThreads = 1024;
-// A grid of one block chooses and sorts in one launch; experts already chosen are
-// sorted by one block of 1024 threads up to so many slots (5331 of 13 experts: 11
-// us, in three launches of more blocks 14).
-constexpr int64_t kOneBlockSlots = 2048, kAloneSlots = 8192;
+// One block, in one launch, instead of several and three launches, which also cost the host
+// 6 us more.  Measured with the host ahead, one block and three launches, us:
+//   the choice and the sort, in two rounds of what a block chooses at once   7.1 and 9.9 (8
+//   experts), 9.4 and 11.7 (64), with ranks of scores 10.4 and 11.8, 12.7 and 13.2; in four
+//   9.9 and 10.5, 14.5 and 11.6, with ranks of scores 16.4 and 12.2, 20.9 and 13.3
+//   the sort alone   4096 slots of 8 to 512 experts 7.0 to 9.1 and 8.3 to 9.7, 8192 10.0 to
+//   13.6 and 8.4 to 9.8; 1024 slots of 1024 experts, by 256 threads, 7.9 and 10.5, 2048
+//   11.4 and 10.7
+constexpr int kRounds = 4, kScoredRounds = 2;
+constexpr int64_t kAloneSlots = 4096, kManyExpertsSlots = 2048;
 constexpr int kAloneExperts = 512;
 
 // ------------------------------------------------------------------ scores
@@ -709,10 +715,10 @@ constexpr size_t kRouteLds = 48 << 10;
 
 int32_t route_block_tokens(int64_t tokens, int32_t experts, int32_t groups, int32_t top, bool scored) {
     const int64_t at_once = experts > 0 ? kRouteThreads / lanes_of(experts, top).G : 0;
-    if (experts < 0 && tokens * top <= kAloneSlots && -experts <= kAloneExperts) return (int32_t)(tokens > 0 ? tokens : 1);
-    if (tokens * top <= kOneBlockSlots &&
-        (experts < 0 || (tokens <= 4 * at_once && route_lds(experts, groups, top, scored, kRouteThreads) <= kRouteLds)))
-        return (int32_t)(tokens > 0 ? tokens : 1);
+    const bool one = experts < 0 ? tokens * top <= (-experts <= kAloneExperts ? kAloneSlots : kManyExpertsSlots)
+                                 : tokens <= (scored ? kScoredRounds : kRounds) * at_once &&
+                                       route_lds(experts, groups, top, scored, kRouteThreads) <= kRouteLds;
+    if (one) return (int32_t)(tokens > 0 ? tokens : 1);
     // at most 1024 blocks, of 256 slots or of what a block chooses at once or more
     const int64_t each = (tokens + 1023) / 1024, least = experts > 0 ? at_once : (256 + top - 1) / top;
     return (int32_t)(each < least ? least : each);
