@@ -366,13 +366,13 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 
 // G lanes a token, NV neighbouring experts a lane.  Ranks by score and bias are
 // formed in fp32 first.  With steps of 2^-24, a score p is off by
-//   logistic   p times 2 x 2 (the exponential) + 1 + 1 (1 + it, the quotient)
+//   logistic   p times 2 x 2 (the exponential) + 1 + 1 (1 + it, the quotient): 6
 //   softmax    p times d (the rounding of its logit's distance d to the largest) + 4 (the
 //              exponential) + 4 + 7 (the sum, kept in 64 bits, of terms that are off so,
-//              whose mean distance is below the logarithm of 1024 experts) + 1 + 1
-// and a rank by one step of its own besides; below fp32's range (or where an exponential
-// overflows) by 2^-126.  may_be_off takes 8, d + 20 and 2 steps, and no distance past 128,
-// of which no score is left.
+//              whose mean distance is below the logarithm of 1024 experts) + 1 + 1: d + 17
+// and a rank by one step of its own besides (all of them with 2^-8 more, for what is of the
+// second order); below fp32's range, or where an exponential overflows, by 2^-126.  No
+// distance past 128 counts, of which no score is left.
 // Then the chosen ones are looked at again, the logistic's scores in 64 bits: each has
 // to lie before the next, by more than both may be off if they are not of the same
 // logit and bias, and the last before all that are left, each with what it may be off
@@ -380,10 +380,10 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 // and so be off by more than the best one left.  That is asked for the largest rank left
 // and the largest score there can be first, and expert by expert in waves with a token
 // where that does not settle it.
-// A token where all that does not hold is ranked again in 64 bits throughout; with
-// the next one's 32-bit rank for all of them instead, sixteen times as many were.
+// A token where all that does not hold is ranked again in 64 bits throughout, by the
+// whole wave: one of 16384 makes the launch 1 us longer.
 // Bound by instruction issue and latency (16384 tokens over 256 experts in 8
-// groups, 16.8 MB: 35 us; 45 with 4 experts a lane, and 54 held to 80 registers for
+// groups, 16.8 MB: 35 us; 40 with 4 experts a lane, and 55 held to 80 registers for
 // more waves).
 template <int NV, int G>
 __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, PlanArgs plan) {
@@ -436,9 +436,9 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
 #pragma unroll
                 for (int i = 0; i < NV; ++i) near |= fabsf(key[i]) > 2.0f && key[i] != -INFINITY;
                 const float gap = choose_ranges<NV, G>(a, l, key, rows + l.row * a.row_floats);
-                // (Two sums of two ranks that are 2 at most.  Logistic scores: 4 x 8 steps, 4 x 2 of the
-                // ranks and 2 x 4 of the sums, 48 in all; a softmax's scores are together 1 at
-                // most and p d below 1 / e, 22 + 16.)
+                // (Two sums of two ranks that are 2 at most.  Logistic scores: 4 x 6 steps, 4 x 2 of the
+                // ranks and 2 x 4 of the sums, 40 in all; a softmax's scores are together 1 at
+                // most and p d below 1 / e, 19 + 16.)
                 near |= !(gap > 0x1p-18f);
             }
 #pragma unroll
@@ -446,7 +446,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
             expert = choose<NV, G>(l, rank, a.top);
             // (d: how far its logit lies below the largest)
             auto may_be_off = [&](float p, float d, float rank) __attribute__((always_inline)) {
-                return 0x1p-24f * (p * (a.sigmoid ? 8.0f : 20.0f + fminf(d, 128.0f)) + 2.0f * fabsf(rank)) + 0x1p-126f;
+                return 0x1.01p-24f * (p * (a.sigmoid ? 6.0f : 17.0f + fminf(d, 128.0f)) + fabsf(rank)) + 0x1p-126f;
             };
             float bc = 0.0f;
             double exactly = -INFINITY, off = 0.0;  // the rank again, and how far it may be off
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(kRouteThreads, 4) void route_kernel(RouteArgs a, Pl
             const bool same = __shfl_up(zc, 1) == zc && __shfl_up(bc, 1) == bc;
             near |= l.gl > 0 && l.gl < a.top && expert >= 0 && !(before - exactly > before_off + off || same);
             // The last chosen against what is left.  (Ranks as numbers are in the order of
-            // rank + 2^-23 |rank|, too, and e^-d (d + 20) is largest for d = 0; fewer chosen
+            // rank + 2^-24 |rank|, too, and e^-d (d + 17) is largest for d = 0; fewer chosen
             // than `top`: nothing is left.)
             uint32_t most = rank[0];
 #pragma unroll
@@ -672,8 +672,8 @@ __global__ __launch_bounds__(256) void route_back_kernel(RouteBackArgs a) {
 
 // Lanes of a token, 4 or more and as many as the experts chosen at least, and experts of
 // a lane: 8 from 128 experts on, else 4 (and 16 where a wave's lanes do not do).
-// Choosing 8 of 128 for 16384 tokens takes 10.4 us with 8, 14.3 with 4; 6 of 60 for
-// 4099 7.4 with 4.
+// Choosing 8 of 128 for 16384 tokens takes 11.4 us with 8, 13.8 with 4; 6 of 60 for
+// 4099 7.3 with 4.
 struct Lanes {
     int G, nv;
 };
