@@ -797,7 +797,9 @@ zopt_status zopt_rope_table(int64_t positions, int32_t rot, double base, float *
  *   eps       finite, >= 0.     style   ZOPT_ROPE_*.
  *   yq, yk    bf16 [T, heads, width], written; their heads may not overlap.
  *             yq may be q, with the same strides, and yk k.
- * Norms and sums are held in fp32; the only rounding to bf16 is the output's.
+ * Norms and sums are held in fp32 (a row whose squares pass its range, or vanish
+ * in it beside an eps as small, is multiplied by a power of two first); the only
+ * rounding to bf16 is the output's.
  * Errors: ZOPT_ERR_NULL; ZOPT_ERR_SIZE (sizes, strides); ZOPT_ERR_HYPER (eps,
  * style); ZOPT_ERR_DEVICE.
  */
@@ -849,7 +851,9 @@ enum {
  * An expert whose logit or bias is -inf is not there: where fewer than `top`
  * are, a token's last experts are -1 with weight 0 (a row of -inf: all of them),
  * and the token takes no part in the products there.  A NaN ranks behind every
- * number.  Ranks are settled in 64 bits.
+ * number and before what is not there, and a range's sum with one behind every sum.
+ * Ranks and sums are settled in 64 bits (sums of unlike terms that only their
+ * rounding there tells apart come in either order).
  *   T         tokens, 0 .. 2^30, with T top <= 2^30.
  *   experts   1 .. 1024.      top   1 .. min(experts, 32).
  *   logits    fp32 (bf16 = 0) or bf16 (1) [T, experts], row stride ld.

@@ -366,7 +366,8 @@ __device__ __forceinline__ void sort_block(const PlanArgs &a, int block, int blo
 
 // G lanes a token, NV neighbouring experts a lane.  Ranks by score and bias are
 // formed in fp32 first.  With steps of 2^-24, a score p is off by
-//   logistic   p times 2 x 2 (the exponential) + 1 + 1 (1 + it, the quotient): 6
+//   logistic   p times 4 (the exponential; over all arguments 1.4) + 1 + 1 (1 + it, the
+//              quotient): 6 (2.8)
 //   softmax    p times d (the rounding of its logit's distance d to the largest) + 4 (the
 //              exponential) + 4 + 7 (the sum, kept in 64 bits, of terms that are off so,
 //              whose mean distance is below the logarithm of 1024 experts) + 1 + 1: d + 17

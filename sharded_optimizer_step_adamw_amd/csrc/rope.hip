@@ -75,10 +75,15 @@ __device__ __forceinline__ void turn(float (&v)[2 * V], const float2 (&cs)[V], i
 // so that a rotation needs no other lane, and a row's two sums (of squares, and
 // back of g n w) are joined in registers.  A block walks rows of one side, the
 // next row's elements on their way while it works on one.
-// Bound by HBM: 65536 tokens of 32 + 8 heads of 128 take 242 us forward (1.34 GB,
-// 5.55 TB/s; a 2 GiB copy reaches 4.97) and 358 back (2.01 GB, 5.6), 13% and 23%
-// less than without the row read ahead and with accesses through the caches.
-// 8-byte pieces on twice the lanes took 279 and 442.
+// Bound by HBM in pieces of 16 bytes (V = 8): 65536 tokens of 32 + 8 heads of 128 take
+// 240 us forward (1.34 GB, 5.6 TB/s; a 2 GiB copy reaches 4.97) and 363 back (2.01 GB, 5.55);
+// 8-byte pieces on twice the lanes took 297 and 396.  Smaller pieces, which a width or a
+// turned part that is no multiple of 2 V leaves, are bound by instruction issue, and most
+// where lanes of a row have nothing: heads of 96 with 24 turned (V = 4, 1.01 GB forward) 284
+// and 359 us, of 80 with 20 (V = 2, 0.84 GB) 474 and 629, of 128 with 62 (V = 1) 975 and 1496,
+// of 66 (V = 1, 33 of a wave's lanes, 0.69 GB) 939 and 1476.
+// What only rows of a kind need (no position, one past the table, squares past fp32's
+// range) is done in the waves that have one.
 template <int V, int NP, bool BACK, bool PAST>
 __global__ __launch_bounds__(kThreads, 4) void rope_kernel(RopeArgs a) {
     const bool second = (int)blockIdx.x >= a.first_blocks;
@@ -345,7 +350,7 @@ hipError_t run(const RopeArgs &a, hipStream_t stream) {
 template <bool BACK>
 hipError_t run(const RopeArgs &a, hipStream_t stream) {
     // Rows that do not fit the memory-side cache go past it: 65536 tokens of 40
-    // heads of 128 take 251 us forward and 358 back so, 273 and 404 otherwise; 8192
+    // heads of 128 take 240 us forward and 363 back so, 256 and 409 otherwise; 8192
     // (84 MB in) the same either way.
     const int64_t bytes = a.tokens * (a.side[0].heads + a.side[1].heads) * a.width * 2 * (BACK ? 3 : 2);
     return bytes > 2 * kCacheBytes ? run<BACK, true>(a, stream) : run<BACK, false>(a, stream);
@@ -358,8 +363,9 @@ void plan_rope(RopeArgs &a) {
     int g = 1;
     while (g < pieces && g < 64) g <<= 1;
     a.group = g;
-    // (as many blocks as the GPU's 256 CUs hold: forward 242 us with 1024, 251 with
-    // 4096; backward, whose blocks' sums are added up, 358, 364 with 2048)
+    // (as many blocks as the GPU's 256 CUs hold: the call above takes 240 us forward with
+    // 1024, 251 with 4096; backward, whose blocks' sums are added up, 363, 367 with 2048 and 372
+    // with 4096)
     const int64_t per = kThreads / g, most = 1024;
     const int64_t q = (a.tokens * a.side[0].heads + per - 1) / per, k = (a.tokens * a.side[1].heads + per - 1) / per;
     int64_t bq = q, bk = k;
