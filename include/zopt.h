@@ -851,7 +851,7 @@ enum {
  * An expert whose logit or bias is -inf is not there: where fewer than `top`
  * are, a token's last experts are -1 with weight 0 (a row of -inf: all of them),
  * and the token takes no part in the products there.  A NaN ranks behind every
- * number and before what is not there, and a range's sum with one behind every sum.
+ * number and before what is not there; so does a range with one among its two best.
  * Ranks and sums are settled in 64 bits (sums of unlike terms that only their
  * rounding there tells apart come in either order).
  *   T         tokens, 0 .. 2^30, with T top <= 2^30.
